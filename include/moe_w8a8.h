@@ -340,6 +340,204 @@ int moe_w8a8_router_logits(const moe_w8a8_dims *dims, const uint16_t *x, int64_t
 int moe_w8a8_pack(int64_t count, int32_t N, int32_t K, const int8_t *src, int8_t *dst,
                   void *stream);
 
+/* ------------------------------------------------ the block around the layer
+ * Operators of the decoder block that holds the layer, in the layer's own
+ * quantisation scheme ("MiniMax-M3 W8A8 inference on K100AI" §3.2: per-channel
+ * weights, per-token activations; §4.3: consecutive matmuls stay in the 8-bit
+ * domain, conversion only where a norm or a residual needs it):
+ *   moe_w8a8_act_quant  per-token codes of bf16 rows;
+ *   moe_w8a8_linear     the matrix product with a scale per token and per
+ *                       output channel (QKV and output projections, LM head);
+ *   moe_w8a8_ffn        the gated feed-forward block (a dense layer's FFN, or
+ *                       a shared expert whose gated result is added to the
+ *                       routed experts' output);
+ *   moe_w8a8_add_norm   the norms before and after a block with its gate,
+ *                       residual scale and residual add, and the codes the
+ *                       next product takes.
+ *
+ * Per-token codes, for a row v of fp32 values (v_j = fl32(x_j * inv_smooth_j)):
+ * a = max |v_j|, code = rint(fl32(v_j * fl32(127/a))) clamped to [-127, 127]
+ * (FP8: the nearest e4m3 of fl32(v_j * fl32(448/a)) clamped to +-448), scale =
+ * fl32(a/127) (a/448). a = 0 gives codes 0 and scale 0. A row that holds a NaN
+ * or an infinity gets codes 0 and a NaN scale, so that everything computed
+ * from it is NaN and no other row is touched. For a < 2^-64 both v_j and a are
+ * multiplied by 2^64 (exactly) before the two divisions, so that 127/a cannot
+ * overflow; the scale is then taken back by 2^-64.
+ *
+ * Code rows q are row-major int8 (or e4m3 bytes) [T][Kp] with the row pitch
+ * Kp = moe_w8a8_row_pitch(K), K rounded up to a multiple of 128. The operators
+ * that make codes write zeros into columns K..Kp-1; codes from elsewhere must
+ * have zeros there too (the products multiply those columns by zero weights:
+ * INT8 garbage is harmless, but an e4m3 NaN is not).
+ *
+ * Rows of other matrices may be strided: ld_* is the distance between two rows
+ * in elements, at least the row's width and at most 2^26. bf16 and fp32 rows
+ * need only the alignment of their element type. T is below 2^22.
+ *
+ * T == 0 is a successful no-op whatever the other pointers are. */
+
+/* Code rows' pitch in bytes for K columns; 0 for K outside [1, 65536]. */
+int64_t moe_w8a8_row_pitch(int32_t K);
+
+/* A quantised weight matrix W[N][K] (device memory; the struct is host memory).
+ *   w          codes in the fragment-tiled layout of moe_w8a8_weights, with N
+ *              padded to a multiple of 16 rows and K to Kp columns, zero codes
+ *              in the padding: moe_w8a8_linear_codes_bytes(N, K, gated) bytes.
+ *   scale      fp32 [moe_w8a8_linear_scales(N, gated)], one per (padded) row.
+ *   inv_smooth fp32 [K], the reciprocal SmoothQuant scales that the tokens are
+ *              multiplied by before they are coded, or NULL (all 1). Not used
+ *              when the call is given codes.
+ *   bias       fp32 [N], or NULL. Must be NULL where gated.
+ *   gated      0: plain. 1: the gate and up projections of moe_w8a8_ffn,
+ *              N = 2F rows given gate 0..F-1, then up 0..F-1, and held as F
+ *              rounded up to a multiple of 32 rows of each, in alternating
+ *              runs of 32 gate and 32 up rows (so that a gate value and its
+ *              up value come out of one tile); `scale` follows that order.
+ * Supported: K in [1, 65536], N in [1, 1048576]. */
+typedef struct {
+  int32_t in_features;  /* K */
+  int32_t out_features; /* N (gated: 2F) */
+  int32_t format;       /* MOE_W8A8_FORMAT_INT8 or _FP8 */
+  int32_t gated;
+  int8_t *w;
+  float *scale;
+  float *inv_smooth;
+  float *bias;
+} moe_w8a8_linear_weights;
+
+/* Sizes of the buffers above; 0 for unsupported N, K or (gated) odd N. */
+size_t moe_w8a8_linear_codes_bytes(int32_t N, int32_t K, int32_t gated);
+int64_t moe_w8a8_linear_scales(int32_t N, int32_t gated);
+
+/* Fill out->w and out->scale from unquantised weights: src fp32 (src_type
+ * MOE_W8A8_F32) or bf16 (MOE_W8A8_BF16) [N][K] with row pitch ld_src. Rows are
+ * multiplied by smooth (fp32 [K], or NULL) in fp32, then coded per row by the
+ * rule above (a row with a NaN or an infinity gets codes 0 and scale NaN). */
+#define MOE_W8A8_BF16 0
+#define MOE_W8A8_F32 1
+int moe_w8a8_linear_quantise(const moe_w8a8_linear_weights *out, const void *src,
+                             int32_t src_type, int64_t ld_src, const float *smooth,
+                             void *stream);
+
+/* The same from codes quantised elsewhere: src int8 (or e4m3 bytes) [N][K]
+ * with row pitch ld_src, src_scale fp32 [N]. */
+int moe_w8a8_linear_pack(const moe_w8a8_linear_weights *out, const int8_t *src, int64_t ld_src,
+                         const float *src_scale, void *stream);
+
+/* Activations of a product: exactly one of x and (q, s).
+ *   x  bf16 [T][K], row pitch ld_x: coded per token inside the call;
+ *   q  codes [T][Kp] (16-byte aligned, pitch Kp), s fp32 [T]. */
+typedef struct {
+  const uint16_t *x;
+  int64_t ld_x;
+  const int8_t *q;
+  const float *s;
+} moe_w8a8_act;
+
+/* Result of a product y[T][N]: out[t][n] = round(gate[t] * y[t][n] + add[t][n]),
+ * all in fp32 before the one rounding to out_type.
+ *   out   bf16 or fp32 [T][N], row pitch ld_out; columns past N and rows past
+ *         T are left as they were;
+ *   gate  fp32 [T], or NULL (1);
+ *   add   bf16 [T][N], row pitch ld_add, or NULL (0). May be `out` itself
+ *         (out_type MOE_W8A8_BF16 and ld_add == ld_out); otherwise it must not
+ *         overlap it. `out` overlaps no other input (column blocks of one
+ *         buffer with one pitch do not overlap). */
+typedef struct {
+  void *out;
+  int64_t ld_out;
+  int32_t out_type;
+  const float *gate;
+  const uint16_t *add;
+  int64_t ld_add;
+} moe_w8a8_result;
+
+/* Per-token codes of bf16 rows x[T][K] (row pitch ld_x) in `format`, after
+ * multiplying by inv_smooth (fp32 [K], or NULL): q [T][Kp], s fp32 [T]. One
+ * launch, no workspace. Errors: MOE_W8A8_ERR_INVALID, MOE_W8A8_ERR_UNSUPPORTED
+ * (K outside [1, 65536]), MOE_W8A8_ERR_HIP. */
+int moe_w8a8_act_quant(int32_t K, int32_t format, const uint16_t *x, int64_t ld_x, int64_t T,
+                       const float *inv_smooth, int8_t *q, float *s, void *stream);
+
+/* y[t][n] = s[t] * scale[n] * sum_k q[t][k] * w[n][k] + bias[n], then the
+ * result's gate and add. INT8: the sum is exact (INT32); FP8: exact products
+ * accumulated in fp32 by the matrix instructions. The sum's order depends on
+ * the shape (T, N, K) only. `workspace` holds at least
+ * moe_w8a8_linear_workspace_size(N, K, T) bytes (NULL where that is 0).
+ * Errors: MOE_W8A8_ERR_INVALID (NULL or misaligned pointer, T outside
+ * [0, 2^22), bad pitch, format or types, overlap, gated weights),
+ * MOE_W8A8_ERR_UNSUPPORTED, MOE_W8A8_ERR_WORKSPACE, MOE_W8A8_ERR_HIP. */
+size_t moe_w8a8_linear_workspace_size(int32_t N, int32_t K, int64_t T);
+int moe_w8a8_linear(const moe_w8a8_linear_weights *weights, const moe_w8a8_act *act, int64_t T,
+                    const moe_w8a8_result *result, void *workspace, size_t workspace_bytes,
+                    void *stream);
+
+/* Gated feed-forward block: (g, u) = the two halves of act . gate_up^T,
+ * h = g / (1 + exp(-g)) * u in fp32, h coded per token by the rule above, then
+ * y = h . down^T and the result's gate and add, as moe_w8a8_linear.
+ *   gate_up  gated weights, N = 2F, K = H (no bias);
+ *   down     plain weights, K = F, any N, the same format; inv_smooth NULL.
+ * Workspace: moe_w8a8_ffn_workspace_size(H, F, N, T) bytes. */
+size_t moe_w8a8_ffn_workspace_size(int32_t H, int32_t F, int32_t N, int64_t T);
+int moe_w8a8_ffn(const moe_w8a8_linear_weights *gate_up, const moe_w8a8_linear_weights *down,
+                 const moe_w8a8_act *act, int64_t T, const moe_w8a8_result *result,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* Norms before and after a block, fused with its gate and residual scale. For
+ * each of T rows, in fp32:
+ *   b = block_scale * gate * post(y)
+ *   r = residual_scale * residual + b          -> residual_out (rounded once)
+ *   n = pre(r)                                 -> normed (rounded once)
+ *   codes of n (times inv_smooth)              -> q, s
+ * r and n are not rounded in between. post and pre are one of
+ *   MOE_W8A8_NORM_NONE   the identity (weight and bias must be NULL)
+ *   MOE_W8A8_NORM_RMS    v / sqrt(mean(v^2) + eps) * weight + bias
+ *   MOE_W8A8_NORM_LAYER  (v - mean) / sqrt(mean((v - mean)^2) + eps) * weight + bias
+ * with fp32 [H] weight (NULL: 1) and bias (NULL: 0).
+ *   y            bf16 [T][H], row pitch ld_y: the block's output
+ *   residual     bf16 or fp32 (residual_type) [T][H], pitch ld_residual, or
+ *                NULL (0); residual_out, of the same type with pitch
+ *                ld_residual_out, or NULL. It may be `residual` itself with
+ *                the same pitch.
+ *   gate_token   fp32 [T], or NULL (1); and
+ *   gate_rows    bf16 [ceil(T / gate_group)][H], pitch ld_gate: row t takes
+ *                gate row t / gate_group (gate_group >= T: one gate per
+ *                channel; 1: a gate of its own; the tokens of a sequence: a
+ *                gate per sequence), or NULL (1). At most one of the two.
+ *   normed       bf16 [T][H], pitch ld_normed, or NULL; may be `y` itself with
+ *                the same pitch.
+ *   q, s         codes [T][Kp] and scales [T] in `format`, or both NULL.
+ * At least one of residual_out, normed and q. Apart from what is said above,
+ * outputs overlap neither inputs nor each other. Supported: H in [1, 65536].
+ * One launch, no workspace. */
+#define MOE_W8A8_NORM_NONE 0
+#define MOE_W8A8_NORM_RMS 1
+#define MOE_W8A8_NORM_LAYER 2
+typedef struct {
+  int32_t hidden;
+  int32_t pre_norm, post_norm;
+  int32_t residual_type; /* MOE_W8A8_BF16 or MOE_W8A8_F32 */
+  int32_t format;        /* of q */
+  float eps, residual_scale, block_scale;
+  const uint16_t *y;
+  int64_t ld_y;
+  const void *residual;
+  int64_t ld_residual;
+  void *residual_out;
+  int64_t ld_residual_out;
+  const float *post_weight, *post_bias;
+  const float *pre_weight, *pre_bias;
+  const float *gate_token;
+  const uint16_t *gate_rows;
+  int64_t ld_gate, gate_group;
+  uint16_t *normed;
+  int64_t ld_normed;
+  const float *inv_smooth;
+  int8_t *q;
+  float *s;
+} moe_w8a8_add_norm_args;
+int moe_w8a8_add_norm(const moe_w8a8_add_norm_args *args, int64_t T, void *stream);
+
 /* Static description of a return code (never NULL). */
 const char *moe_w8a8_strerror(int code);
 

@@ -1,0 +1,210 @@
+"""Refusals of the block operators, on the host: the C ABI validates its
+arguments before anything is enqueued, the binding checks every tensor before
+it hands out a pointer (no GPU is touched by these cases)."""
+import os
+
+import pytest
+import torch
+
+import w8a8_int8_expert_amd as m
+
+FAKE, FAR = 0x100000, 1 << 40   # never dereferenced; FAR overlaps nothing near FAKE
+OK, INV, UNS, WS = (m.MOE_W8A8_OK, m.MOE_W8A8_ERR_INVALID, m.MOE_W8A8_ERR_UNSUPPORTED,
+                    m.MOE_W8A8_ERR_WORKSPACE)
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not os.path.exists(m.LIB_PATH):
+        from w8a8_int8_expert_amd import build
+        build.build()
+    return m.load_library()
+
+
+def weights(K=300, N=70, fmt=0, gated=0, w=FAKE, scale=FAKE, inv=None, bias=None):
+    return m.moe_w8a8_linear_weights(K, N, fmt, gated, w, scale, inv, bias)
+
+
+def act(x=FAKE, ld=300, q=None, s=None):
+    return m.moe_w8a8_act(x, ld, q, s)
+
+
+def result(out=FAR, ld=70, t=0, gate=None, add=None, ld_add=70):
+    return m.moe_w8a8_result(out, ld, t, gate, add, ld_add)
+
+
+def linear(w=None, a=None, T=4, r=None, ws=2 * FAR, n=1 << 40):
+    return m.moe_w8a8_linear(w or weights(), a or act(), T, r or result(), ws, n, stream=0)
+
+
+def test_sizes():
+    assert [m.moe_w8a8_row_pitch(k) for k in (1, 128, 129, 65536)] == [128, 128, 256, 65536]
+    assert [m.moe_w8a8_row_pitch(k) for k in (0, -1, 65537)] == [0, 0, 0]
+    assert m.moe_w8a8_linear_scales(17) == 32 and m.moe_w8a8_linear_scales(66, 1) == 128
+    assert m.moe_w8a8_linear_scales(0) == 0 and m.moe_w8a8_linear_scales(65, 1) == 0
+    assert m.moe_w8a8_linear_codes_bytes(17, 129) == 32 * 256
+    assert m.moe_w8a8_linear_codes_bytes(66, 129, 1) == 128 * 256
+    assert m.moe_w8a8_linear_codes_bytes(17, 0) == 0
+    assert m.moe_w8a8_linear_codes_bytes((1 << 20) + 1, 1) == 0
+    assert m.moe_w8a8_linear_codes_bytes(1 << 20, 65536) == 1 << 36
+    for f in (lambda T: m.moe_w8a8_linear_workspace_size(1000, 4096, T),
+              lambda T: m.moe_w8a8_ffn_workspace_size(4096, 1000, 70, T)):
+        sizes = [f(T) for T in list(range(0, 600)) + [1023, 1024, 1025, 4096, 100000]]
+        assert sizes[0] == 0 and all(b >= a > 0 for a, b in zip(sizes[1:], sizes[2:]))
+        assert f(-1) == 0 and f(1 << 22) == 0 and f((1 << 22) - 1) > 0
+    assert m.moe_w8a8_linear_workspace_size(0, 1, 1) == 0
+    assert m.moe_w8a8_ffn_workspace_size(1, 65537, 1, 1) == 0
+
+
+def test_linear_refusals():
+    assert linear(T=-1) == INV and linear(T=1 << 22) == INV and linear(T=(1 << 63) - 1) == INV
+    for w in (weights(K=0), weights(N=-1), weights(fmt=2), weights(gated=1), weights(gated=2),
+              weights(w=None), weights(scale=None), weights(w=FAKE + 8), weights(scale=FAKE + 2),
+              weights(inv=FAKE + 1), weights(bias=FAKE + 2)):
+        assert linear(w=w) == INV
+    assert linear(w=weights(K=65537), a=act(ld=65537)) == UNS
+    assert linear(w=weights(N=(1 << 20) + 1), r=result(ld=1 << 21)) == UNS
+    for a in (act(x=None), act(x=FAKE + 1), act(ld=299), act(ld=(1 << 26) + 1),
+              act(q=FAKE, s=FAKE), act(x=None, q=FAKE), act(x=None, s=FAKE),
+              act(x=None, q=FAKE + 8, s=FAKE), act(x=None, q=FAKE, s=FAKE + 2)):
+        assert linear(a=a) == INV
+    for r in (result(out=None), result(out=FAR + 1), result(t=2), result(out=FAR + 2, t=1),
+              result(ld=69), result(gate=FAKE + 1), result(add=FAKE + 1),
+              result(add=FAKE, ld_add=69), result(add=FAR, ld_add=71),   # over out, another pitch
+              result(add=FAR, t=1),                                     # over an fp32 out
+              result(add=FAR + 2), result(out=FAKE + 64),               # over add, over x
+              result(gate=FAR + 8)):                                    # the gate inside out
+        assert linear(r=r) == INV
+    assert linear(ws=None) == WS
+    need = m.moe_w8a8_linear_workspace_size(70, 300, 4)
+    assert linear(n=need - 1) == WS and linear(ws=2 * FAR + 128) == INV
+    assert linear(T=0, a=m.moe_w8a8_act(), r=m.moe_w8a8_result(), ws=None, n=0) == OK
+    assert linear(w=weights(K=0), T=0) == INV
+
+
+def test_ffn_refusals():
+    gu, dn = weights(K=300, N=64, gated=1), weights(K=32, N=70)
+
+    def ffn(g=gu, d=dn, a=None, T=4, r=None, ws=2 * FAR, n=1 << 40):
+        return m.moe_w8a8_ffn(g, d, a or act(), T, r or result(), ws, n, stream=0)
+    assert ffn(T=-1) == INV
+    assert ffn(g=weights(K=300, N=64)) == INV                 # not gated
+    assert ffn(g=weights(K=300, N=63, gated=1)) == INV        # odd
+    assert ffn(g=weights(K=300, N=64, gated=1, bias=FAKE)) == INV
+    assert ffn(g=weights(K=300, N=66, gated=1)) == INV        # F differs
+    assert ffn(d=weights(K=32, N=70, fmt=1)) == INV           # formats differ
+    assert ffn(d=weights(K=32, N=70, inv=FAKE)) == INV
+    assert ffn(d=weights(K=32, N=70, gated=1)) == INV
+    assert ffn(a=act(ld=299)) == INV and ffn(r=result(ld=69)) == INV
+    assert ffn(ws=None) == WS
+    assert ffn(n=m.moe_w8a8_ffn_workspace_size(300, 32, 70, 4) - 1) == WS
+    assert ffn(T=0, a=m.moe_w8a8_act(), r=m.moe_w8a8_result(), ws=None, n=0) == OK
+
+
+def test_weight_refusals():
+    def quantise(w=None, src=FAR, t=1, ld=300, sm=None):
+        return m.moe_w8a8_linear_quantise(w or weights(), src, t, ld, sm, stream=0)
+    assert quantise(w=weights(w=None)) == INV and quantise(src=None) == INV
+    assert quantise(t=2) == INV and quantise(src=FAR + 2) == INV and quantise(ld=299) == INV
+    assert quantise(src=FAR + 1, t=0) == INV and quantise(sm=FAKE + 2) == INV
+    assert quantise(w=weights(K=65537), ld=65537) == UNS
+
+    def pack(w=None, src=FAR, ld=300, s=2 * FAR):
+        return m.moe_w8a8_linear_pack(w or weights(), src, ld, s, stream=0)
+    assert pack(src=None) == INV and pack(s=None) == INV and pack(s=2 * FAR + 2) == INV
+    assert pack(ld=299) == INV and pack(src=FAKE) == INV and pack(s=FAKE) == INV
+
+
+def test_act_quant_refusals():
+    def aq(K=300, fmt=0, x=FAKE, ld=300, T=4, inv=None, q=FAR, s=2 * FAR):
+        return m.moe_w8a8_act_quant(K, fmt, x, ld, T, inv, q, s, stream=0)
+    for kw in (dict(K=0), dict(fmt=2), dict(x=None), dict(x=FAKE + 1), dict(ld=299), dict(T=-1),
+               dict(T=1 << 22), dict(inv=FAKE + 2), dict(q=None), dict(s=None), dict(q=FAR + 8),
+               dict(s=2 * FAR + 2), dict(q=FAKE), dict(s=FAKE + 4), dict(s=FAR + 4)):
+        assert aq(**kw) == INV, kw
+    assert aq(K=65537, ld=65537) == UNS
+    assert aq(T=0, x=None, q=None, s=None) == OK
+
+
+def test_add_norm_refusals():
+    def an(T=4, **kw):
+        a = m.moe_w8a8_add_norm_args()
+        base = dict(hidden=300, pre_norm=1, post_norm=0, eps=1e-6, residual_scale=1.0,
+                    block_scale=1.0, y=FAKE, ld_y=300, normed=FAR, ld_normed=300)
+        for k, v in {**base, **kw}.items():
+            setattr(a, k, v)
+        return m.moe_w8a8_add_norm(a, T, stream=0)
+    for kw in (dict(T=-1), dict(T=1 << 22), dict(hidden=0), dict(pre_norm=3), dict(post_norm=-1),
+               dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")),
+               dict(residual_scale=float("inf")), dict(block_scale=float("nan")),
+               dict(residual_type=2), dict(format=2), dict(y=None), dict(y=FAKE + 1),
+               dict(ld_y=299), dict(normed=None), dict(normed=FAR + 1), dict(ld_normed=299),
+               dict(pre_norm=0, pre_weight=FAKE), dict(post_weight=FAKE), dict(post_bias=FAKE),
+               dict(q=3 * FAR), dict(s=3 * FAR), dict(q=3 * FAR + 8, s=4 * FAR),
+               dict(q=3 * FAR, s=4 * FAR + 2), dict(residual=2 * FAR, ld_residual=299),
+               dict(residual=2 * FAR + 2, ld_residual=300, residual_type=1),
+               dict(residual_out=2 * FAR + 1, ld_residual_out=300),
+               dict(gate_token=FAKE + 1), dict(gate_token=3 * FAR, gate_rows=2 * FAR, ld_gate=300,
+                                               gate_group=1),
+               dict(gate_rows=2 * FAR, ld_gate=300, gate_group=0),
+               dict(gate_rows=2 * FAR, ld_gate=299, gate_group=1), dict(inv_smooth=FAKE + 2),
+               # overlaps the header does not allow
+               dict(normed=FAKE + 2), dict(normed=FAKE, ld_normed=301),
+               dict(residual=FAR, ld_residual=300),
+               dict(residual_out=FAR, ld_residual_out=300),
+               dict(residual=2 * FAR, ld_residual=300, residual_out=2 * FAR, ld_residual_out=302),
+               dict(q=FAR, s=4 * FAR), dict(q=3 * FAR, s=3 * FAR + 16),
+               dict(gate_rows=FAR, ld_gate=300, gate_group=4),
+               dict(pre_weight=FAR + 4)):
+        assert an(**kw) == INV, kw
+    assert an(hidden=65537, ld_y=65537, ld_normed=65537) == UNS
+    assert an(T=0, y=None, normed=None) == OK
+
+
+def test_binding_refusals():
+    """CPU tensors on CPU-placed operators: every case is refused before the
+    library is called."""
+    lin = m.W8A8Linear(70, 30, device="cpu")
+    ffn = m.W8A8FFN(70, 30, device="cpu")
+    T = 5
+    x = torch.zeros(T, 70, dtype=BF)
+    q, s = torch.zeros(T, 128, dtype=torch.int8), torch.zeros(T)
+    for op, N in ((lin, 30), (ffn, 70)):
+        for kw in (dict(), dict(x=x, codes=(q, s)), dict(x=x.float()), dict(x=x[:, :69]),
+                   dict(x=x.t()), dict(x=x[0]), dict(x=x[:1].expand(T, 70)),
+                   dict(codes=(q[:, :70], s)), dict(codes=(q, s[:4])), dict(codes=(q, None)),
+                   dict(codes=(q.float(), s)), dict(codes=(q, s.double())),
+                   dict(x=x, out=torch.zeros(T, N)[:4]), dict(x=x, out=torch.zeros(T, N).double()),
+                   dict(x=x, out=torch.zeros(T, N), out_dtype=BF),
+                   dict(x=x, add=torch.zeros(T, N)), dict(x=x, add=torch.zeros(T, N + 1, dtype=BF)),
+                   dict(x=x, gate=torch.zeros(T + 1)), dict(x=x, gate=torch.zeros(T, dtype=BF)),
+                   dict(x=x, out_dtype=torch.float16)):
+            with pytest.raises(m.MoEW8A8Error):
+                op.forward(**kw)
+        with pytest.raises(m.MoEW8A8Error, match="GPU"):   # nothing else is wrong
+            op.forward(x)
+    with pytest.raises(m.MoEW8A8Error):
+        lin.load_quantized(torch.zeros(30, 69, dtype=torch.int8), torch.zeros(30))
+    with pytest.raises(m.MoEW8A8Error):
+        lin.load_quantized(torch.zeros(30, 70), torch.zeros(30))
+    with pytest.raises(m.MoEW8A8Error):
+        lin.quantise(torch.zeros(30, 70, dtype=torch.float16))
+    for shape in ((0, 1), (1, 0), (65537, 1), (1, (1 << 20) + 1)):
+        with pytest.raises(m.MoEW8A8Error):
+            m.W8A8Linear(*shape, device="cpu")
+    with pytest.raises(m.MoEW8A8Error):
+        m.act_quant(x.float())
+    with pytest.raises(m.MoEW8A8Error):
+        m.act_quant(x, torch.zeros(71))
+    w = torch.ones(70)
+    for kw in (dict(y=x.float()), dict(y=x[0]), dict(residual=x[:4]), dict(residual=x.double()),
+               dict(norm="l2"), dict(post_norm="x"), dict(weight=w[:69]), dict(weight=w.to(BF)),
+               dict(bias=w[:1]), dict(codes="int4"), dict(gate=torch.zeros(3)),
+               dict(gate=torch.zeros(T, 70)), dict(gate=torch.zeros(0, 70, dtype=BF)),
+               dict(gate=torch.zeros(2, 70, dtype=BF), gate_group=2), dict(gate=w.to(BF)),
+               dict(gate=torch.zeros(2, 70, dtype=BF), gate_group=0), dict(normed=x[:4]),
+               dict(residual=x, residual_out=torch.zeros(T, 70)), dict(codes="int8",
+                                                                      inv_smooth=w[:3])):
+        with pytest.raises(m.MoEW8A8Error):
+            m.add_norm(**{"y": x, **kw})

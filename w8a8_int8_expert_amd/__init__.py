@@ -47,13 +47,45 @@ class moe_w8a8_debug(ctypes.Structure):
                 ("h", _P), ("qh", _P), ("sh", _P), ("y", _P), ("gemm_path", ctypes.c_int32),
                 ("stage_events", ctypes.POINTER(_P)), ("router_logits", _P)]
 
+class moe_w8a8_linear_weights(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("format", ctypes.c_int32), ("gated", ctypes.c_int32), ("w", _P), ("scale", _P),
+                ("inv_smooth", _P), ("bias", _P)]
+
+
+class moe_w8a8_act(ctypes.Structure):
+    _fields_ = [("x", _P), ("ld_x", ctypes.c_int64), ("q", _P), ("s", _P)]
+
+
+class moe_w8a8_result(ctypes.Structure):
+    _fields_ = [("out", _P), ("ld_out", ctypes.c_int64), ("out_type", ctypes.c_int32),
+                ("gate", _P), ("add", _P), ("ld_add", ctypes.c_int64)]
+
+
+class moe_w8a8_add_norm_args(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("pre_norm", ctypes.c_int32),
+                ("post_norm", ctypes.c_int32), ("residual_type", ctypes.c_int32),
+                ("format", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("block_scale", ctypes.c_float),
+                ("y", _P), ("ld_y", ctypes.c_int64), ("residual", _P),
+                ("ld_residual", ctypes.c_int64), ("residual_out", _P),
+                ("ld_residual_out", ctypes.c_int64), ("post_weight", _P), ("post_bias", _P),
+                ("pre_weight", _P), ("pre_bias", _P), ("gate_token", _P), ("gate_rows", _P),
+                ("ld_gate", ctypes.c_int64), ("gate_group", ctypes.c_int64), ("normed", _P),
+                ("ld_normed", ctypes.c_int64), ("inv_smooth", _P), ("q", _P), ("s", _P)]
+
+
 STAGES = ("route", "scan", "scatter", "act_quant", "gemm1", "requant", "gemm2", "combine",
           "router")
 
 
 EXPORTS = ("moe_w8a8_workspace_size", "moe_w8a8_calibrate", "moe_w8a8_calibrate_clip",
            "moe_w8a8_forward", "moe_w8a8_forward_noalloc", "moe_w8a8_router_logits",
-           "moe_w8a8_pack", "moe_w8a8_strerror")
+           "moe_w8a8_pack", "moe_w8a8_strerror", "moe_w8a8_row_pitch",
+           "moe_w8a8_linear_codes_bytes", "moe_w8a8_linear_scales", "moe_w8a8_linear_quantise",
+           "moe_w8a8_linear_pack", "moe_w8a8_act_quant", "moe_w8a8_linear_workspace_size",
+           "moe_w8a8_linear", "moe_w8a8_ffn_workspace_size", "moe_w8a8_ffn",
+           "moe_w8a8_add_norm")
 
 _lib = None
 
@@ -94,6 +126,22 @@ def load_library(path: str = LIB_PATH):
                                            _P]
     lib.moe_w8a8_pack.restype = ctypes.c_int
     lib.moe_w8a8_pack.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P]
+    LW, AC, RS = (ctypes.POINTER(c) for c in (moe_w8a8_linear_weights, moe_w8a8_act,
+                                              moe_w8a8_result))
+    i32, i64, size_t = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    for name, ret, args in (
+            ("row_pitch", i64, [i32]), ("linear_codes_bytes", size_t, [i32, i32, i32]),
+            ("linear_scales", i64, [i32, i32]),
+            ("linear_quantise", ctypes.c_int, [LW, _P, i32, i64, _P, _P]),
+            ("linear_pack", ctypes.c_int, [LW, _P, i64, _P, _P]),
+            ("act_quant", ctypes.c_int, [i32, i32, _P, i64, i64, _P, _P, _P, _P]),
+            ("linear_workspace_size", size_t, [i32, i32, i64]),
+            ("linear", ctypes.c_int, [LW, AC, i64, RS, _P, size_t, _P]),
+            ("ffn_workspace_size", size_t, [i32, i32, i32, i64]),
+            ("ffn", ctypes.c_int, [LW, LW, AC, i64, RS, _P, size_t, _P]),
+            ("add_norm", ctypes.c_int, [ctypes.POINTER(moe_w8a8_add_norm_args), i64, _P])):
+        f = getattr(lib, "moe_w8a8_" + name)
+        f.restype, f.argtypes = ret, args
     lib.moe_w8a8_strerror.restype = ctypes.c_char_p
     lib.moe_w8a8_strerror.argtypes = [ctypes.c_int]
     _lib = lib
@@ -173,6 +221,63 @@ def moe_w8a8_router_logits(d, x, T, w_router, logits, workspace, workspace_bytes
 def moe_w8a8_pack(count, N, K, src, dst, stream=None) -> int:
     return int(load_library().moe_w8a8_pack(int(count), int(N), int(K), _ptr(src), _ptr(dst),
                                              _stream(stream)))
+
+
+def moe_w8a8_row_pitch(K: int) -> int:
+    return int(load_library().moe_w8a8_row_pitch(K))
+
+
+def moe_w8a8_linear_codes_bytes(N: int, K: int, gated: int = 0) -> int:
+    return int(load_library().moe_w8a8_linear_codes_bytes(N, K, gated))
+
+
+def moe_w8a8_linear_scales(N: int, gated: int = 0) -> int:
+    return int(load_library().moe_w8a8_linear_scales(N, gated))
+
+
+def moe_w8a8_linear_quantise(out: moe_w8a8_linear_weights, src, src_type, ld_src, smooth=None,
+                             stream=None) -> int:
+    return int(load_library().moe_w8a8_linear_quantise(
+        ctypes.byref(out), _ptr(src), int(src_type), int(ld_src), _ptr(smooth), _stream(stream)))
+
+
+def moe_w8a8_linear_pack(out: moe_w8a8_linear_weights, src, ld_src, src_scale,
+                         stream=None) -> int:
+    return int(load_library().moe_w8a8_linear_pack(
+        ctypes.byref(out), _ptr(src), int(ld_src), _ptr(src_scale), _stream(stream)))
+
+
+def moe_w8a8_act_quant(K, fmt, x, ld_x, T, inv_smooth, q, s, stream=None) -> int:
+    return int(load_library().moe_w8a8_act_quant(
+        int(K), int(fmt), _ptr(x), int(ld_x), int(T), _ptr(inv_smooth), _ptr(q), _ptr(s),
+        _stream(stream)))
+
+
+def moe_w8a8_linear_workspace_size(N: int, K: int, T: int) -> int:
+    return int(load_library().moe_w8a8_linear_workspace_size(N, K, T))
+
+
+def moe_w8a8_linear(weights: moe_w8a8_linear_weights, act: moe_w8a8_act, T,
+                    result: moe_w8a8_result, workspace, workspace_bytes, stream=None) -> int:
+    return int(load_library().moe_w8a8_linear(
+        ctypes.byref(weights), ctypes.byref(act), T, ctypes.byref(result), _ptr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
+def moe_w8a8_ffn_workspace_size(H: int, F: int, N: int, T: int) -> int:
+    return int(load_library().moe_w8a8_ffn_workspace_size(H, F, N, T))
+
+
+def moe_w8a8_ffn(gate_up: moe_w8a8_linear_weights, down: moe_w8a8_linear_weights,
+                 act: moe_w8a8_act, T, result: moe_w8a8_result, workspace, workspace_bytes,
+                 stream=None) -> int:
+    return int(load_library().moe_w8a8_ffn(
+        ctypes.byref(gate_up), ctypes.byref(down), ctypes.byref(act), T, ctypes.byref(result),
+        _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def moe_w8a8_add_norm(args: moe_w8a8_add_norm_args, T, stream=None) -> int:
+    return int(load_library().moe_w8a8_add_norm(ctypes.byref(args), T, _stream(stream)))
 
 
 class MoEW8A8Error(RuntimeError):
@@ -372,3 +477,6 @@ class MoEW8A8:
             out = torch.empty(T, H, dtype=torch.bfloat16, device=self.device)
         self._expect(out, "out", torch.bfloat16, (T, H))
         return out
+
+
+from .block import AddNorm, W8A8FFN, W8A8Linear, act_quant, add_norm  # noqa: E402,F401

@@ -1,0 +1,375 @@
+"""The decoder block around the W8A8 expert layer: torch plumbing of the block
+operators of libmoe_w8a8 (include/moe_w8a8.h).
+
+    q, s = act_quant(x, inv_smooth)                 per-token codes
+    W8A8Linear(K, N).forward(x or codes=(q, s))     W8A8 matrix product
+    W8A8FFN(H, F).forward(x or codes=(q, s))        W8A8 gated feed-forward block
+    add_norm(y, residual, ...)                      norms around a block, gate,
+                                                    residual add, codes
+
+Every tensor is checked (type, shape, strides, device) before a pointer is
+handed to the library. Calls run on torch's current stream of the operands'
+device, whichever device is current. Outputs and workspaces come from torch's
+allocator call by call, so calls on different streams, and graphs captured
+from them, share nothing but the weights.
+"""
+from __future__ import annotations
+
+import contextlib
+from typing import NamedTuple, Optional
+
+import w8a8_int8_expert_amd as _m
+
+_FORMATS = {"int8": 0, "fp8": 1}
+_NORMS = {None: 0, "none": 0, "rms": 1, "layer": 2}
+_SAME = contextlib.nullcontext()
+
+
+def _fail(msg):
+    raise _m.MoEW8A8Error(msg)
+
+
+def _device(device):
+    import torch
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
+def _on(device):
+    """Context in which `device` is current (nothing to do if it already is)."""
+    import torch
+    if device.type != "cuda":
+        _fail("the operands must be on a GPU")
+    if torch.cuda.current_device() == device.index:
+        return _SAME
+    return torch.cuda.device(device)
+
+
+def _rows(t, name, dtypes, T, width, device):
+    """(address, row pitch) of a [T][width] tensor whose rows are contiguous."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        _fail("%s must be a torch tensor" % name)
+    if t.dtype not in dtypes:
+        _fail("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if t.shape != (T, width):
+        _fail("%s must have shape %s, got %s" % (name, (T, width), tuple(t.shape)))
+    if t.device != device:
+        _fail("%s must be on %s, got %s" % (name, device, t.device))
+    ld, step = t.stride()
+    if step != 1 and width > 1:
+        _fail("the rows of %s must be contiguous" % name)
+    if T <= 1:
+        ld = width
+    elif ld < width:
+        _fail("the rows of %s overlap (row stride %d for %d columns)" % (name, ld, width))
+    return t.data_ptr(), ld
+
+
+def _vector(t, name, n, device):
+    """Address of a contiguous fp32 [n] tensor, None for None."""
+    import torch
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.numel() != n or \
+            not t.is_contiguous() or t.device != device:
+        _fail("%s must be a contiguous fp32 tensor of %d values on %s" % (name, n, device))
+    return t.data_ptr()
+
+
+def _code_types(fp8):
+    import torch
+    return (torch.float8_e4m3fn, torch.int8) if fp8 else (torch.int8,)
+
+
+def _empty_codes(T, K, fp8, device):
+    import torch
+    pitch = _m.moe_w8a8_row_pitch(K)
+    if pitch == 0:
+        _fail("unsupported width %d" % K)
+    return (torch.empty(T, pitch, dtype=torch.float8_e4m3fn if fp8 else torch.int8, device=device),
+            torch.empty(T, dtype=torch.float32, device=device))
+
+
+def act_quant(x, inv_smooth=None, fp8: bool = False):
+    """Per-token codes of bf16 rows x [T][K], times inv_smooth (fp32 [K]):
+    (codes [T][Kp], scales fp32 [T]), Kp = moe_w8a8_row_pitch(K), zeros past K."""
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        _fail("x must be a [T][K] tensor")
+    T, K = x.shape
+    dev = x.device
+    px, ld = _rows(x, "x", (torch.bfloat16,), T, K, dev)
+    inv = _vector(inv_smooth, "inv_smooth", K, dev)
+    q, s = _empty_codes(T, K, fp8, dev)
+    with _on(dev):
+        _m._check(_m.moe_w8a8_act_quant(K, int(bool(fp8)), px, ld, T, inv, q, s),
+                  "moe_w8a8_act_quant")
+    return q, s
+
+
+class _Weights:
+    """Packed codes and scales of one weight matrix, and the struct that names
+    them."""
+
+    def __init__(self, K, N, fp8, gated, device):
+        import torch
+        size = _m.moe_w8a8_linear_codes_bytes(N, K, gated)
+        if size == 0:
+            _fail("unsupported weight shape [%d][%d]" % (N, K))
+        self.K, self.N, self.fp8, self.gated, self.device = K, N, fp8, gated, device
+        self.codes = torch.empty(size, dtype=torch.int8, device=device)
+        self.scale = torch.empty(_m.moe_w8a8_linear_scales(N, gated), dtype=torch.float32,
+                                 device=device)
+        self.inv_smooth = self.bias = None
+        self.struct = _m.moe_w8a8_linear_weights(K, N, int(fp8), int(gated),
+                                                 self.codes.data_ptr(), self.scale.data_ptr(),
+                                                 None, None)
+
+    def vectors(self, inv_smooth, bias):
+        """Keep copies of the two optional vectors."""
+        for name, t, n in (("inv_smooth", inv_smooth, self.K), ("bias", bias, self.N)):
+            _vector(t, name, n, self.device)
+            t = None if t is None else t.detach().reshape(n).clone()
+            setattr(self, name, t)
+            setattr(self.struct, name, None if t is None else t.data_ptr())
+
+    def quantise(self, w, smooth):
+        import torch
+        p, ld = _rows(w, "weight", (torch.bfloat16, torch.float32), self.N, self.K, self.device)
+        with _on(self.device):
+            _m._check(_m.moe_w8a8_linear_quantise(
+                self.struct, p, 1 if w.dtype == torch.float32 else 0, ld,
+                _vector(smooth, "smooth", self.K, self.device)), "moe_w8a8_linear_quantise")
+
+    def load(self, q, s):
+        p, ld = _rows(q, "codes", _code_types(self.fp8), self.N, self.K, self.device)
+        with _on(self.device):
+            _m._check(_m.moe_w8a8_linear_pack(self.struct, p, ld,
+                                              _vector(s, "scales", self.N, self.device)),
+                      "moe_w8a8_linear_pack")
+
+
+class _Product:
+    """What the two products share: their operands and their result."""
+
+    def _operands(self, x, codes, K, N, add, gate, out, out_dtype):
+        import torch
+        dev = self.device
+        if (x is None) == (codes is None):
+            _fail("give either x or codes")
+        first = x if codes is None else codes[0]
+        if not isinstance(first, torch.Tensor) or first.dim() != 2:
+            _fail("tokens must be a [T][K] tensor")
+        T = first.shape[0]
+        act = _m.moe_w8a8_act()
+        if codes is None:
+            act.x, act.ld_x = _rows(x, "x", (torch.bfloat16,), T, K, dev)
+        else:
+            pitch = _m.moe_w8a8_row_pitch(K)
+            act.q, ld = _rows(first, "codes", _code_types(self.fp8), T, pitch, dev)
+            if ld != pitch:
+                _fail("codes must be contiguous")
+            act.s = _vector(codes[1], "code scales", T, dev)
+            if act.s is None and T > 0:
+                _fail("codes come with their scales")
+        if out is None:
+            out = torch.empty(T, N, dtype=out_dtype or torch.bfloat16, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            _fail("out must be %s, got %s" % (out_dtype, out.dtype))
+        res = _m.moe_w8a8_result()
+        res.out, res.ld_out = _rows(out, "out", (torch.bfloat16, torch.float32), T, N, dev)
+        res.out_type = 1 if out.dtype == torch.float32 else 0
+        if gate is not None:
+            res.gate = _vector(gate, "gate", T, dev)
+        if add is not None:
+            res.add, res.ld_add = _rows(add, "add", (torch.bfloat16,), T, N, dev)
+        return T, act, res, out
+
+
+def _workspace(n, device):
+    import torch
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+class W8A8Linear(_Product):
+    """y = x . W^T in W8A8: INT8 (or, with fp8=True, e4m3) codes with a scale
+    per token and per output channel. Fill it with quantise() or
+    load_quantized(), then call forward()."""
+
+    def __init__(self, in_features: int, out_features: int, device="cuda", fp8: bool = False):
+        _m.load_library()
+        self.in_features, self.out_features = int(in_features), int(out_features)
+        self.fp8, self.device = bool(fp8), _device(device)
+        self._w = _Weights(self.in_features, self.out_features, self.fp8, False, self.device)
+
+    def quantise(self, weight, smooth=None, bias=None):
+        """weight: fp32 or bf16 [N][K]. smooth: SmoothQuant scales s fp32 [K]
+        (the weight's columns are multiplied by s, the tokens by 1/s)."""
+        self._w.quantise(weight, smooth)
+        self._w.vectors(None if smooth is None else 1.0 / smooth, bias)
+
+    def load_quantized(self, q, s, inv_smooth=None, bias=None):
+        """Codes [N][K] (int8, or float8_e4m3fn) quantised elsewhere and their
+        scales fp32 [N]; inv_smooth fp32 [K] multiplies the tokens."""
+        self._w.load(q, s)
+        self._w.vectors(inv_smooth, bias)
+
+    def forward(self, x=None, codes=None, add=None, gate=None, out=None,
+                out_dtype: Optional["torch.dtype"] = None):  # noqa: F821
+        """out = gate[:, None] * (x . W^T + bias) + add, rounded once to bf16
+        (or fp32). x: bf16 [T][K], or codes=(q, s) as act_quant and add_norm
+        give them. gate fp32 [T]; add bf16 [T][N] (may be out itself)."""
+        T, act, res, out = self._operands(x, codes, self.in_features, self.out_features, add,
+                                          gate, out, out_dtype)
+        n = _m.moe_w8a8_linear_workspace_size(self.out_features, self.in_features, T)
+        ws = _workspace(n, self.device)
+        with _on(self.device):
+            _m._check(_m.moe_w8a8_linear(self._w.struct, act, T, res, ws, n), "moe_w8a8_linear")
+        return out
+
+    __call__ = forward
+
+
+class W8A8FFN(_Product):
+    """Gated feed-forward block in W8A8: down(silu(gate(x)) * up(x)), the hidden
+    rows requantised per token."""
+
+    def __init__(self, hidden: int, ffn: int, device="cuda", fp8: bool = False,
+                 out_features: Optional[int] = None):
+        _m.load_library()
+        self.hidden, self.ffn = int(hidden), int(ffn)
+        self.out_features = self.hidden if out_features is None else int(out_features)
+        self.fp8, self.device = bool(fp8), _device(device)
+        self._gu = _Weights(self.hidden, 2 * self.ffn, self.fp8, True, self.device)
+        self._dn = _Weights(self.ffn, self.out_features, self.fp8, False, self.device)
+
+    def quantise(self, w_gate_up, w_down, smooth=None, bias=None):
+        """w_gate_up: fp32 or bf16 [2F][H], gate rows then up rows; w_down
+        [N][F]; smooth fp32 [H]; bias fp32 [N] of the down projection."""
+        self._gu.quantise(w_gate_up, smooth)
+        self._gu.vectors(None if smooth is None else 1.0 / smooth, None)
+        self._dn.quantise(w_down, None)
+        self._dn.vectors(None, bias)
+
+    def load_quantized(self, q_gate_up, s_gate_up, q_down, s_down, inv_smooth=None, bias=None):
+        """Codes [2F][H] (gate rows, then up rows) and [N][F] quantised
+        elsewhere, their scales fp32 [2F] and [N]."""
+        self._gu.load(q_gate_up, s_gate_up)
+        self._gu.vectors(inv_smooth, None)
+        self._dn.load(q_down, s_down)
+        self._dn.vectors(None, bias)
+
+    def forward(self, x=None, codes=None, add=None, gate=None, out=None,
+                out_dtype: Optional["torch.dtype"] = None):  # noqa: F821
+        """out = gate[:, None] * ffn(x) + add; operands as W8A8Linear.forward.
+        As a shared expert: ffn.forward(x, add=moe.forward(x, ...), gate=g)."""
+        T, act, res, out = self._operands(x, codes, self.hidden, self.out_features, add, gate,
+                                          out, out_dtype)
+        n = _m.moe_w8a8_ffn_workspace_size(self.hidden, self.ffn, self.out_features, T)
+        ws = _workspace(n, self.device)
+        with _on(self.device):
+            _m._check(_m.moe_w8a8_ffn(self._gu.struct, self._dn.struct, act, T, res, ws, n),
+                      "moe_w8a8_ffn")
+        return out
+
+    __call__ = forward
+
+
+class AddNorm(NamedTuple):
+    residual: Optional["torch.Tensor"]  # noqa: F821
+    normed: Optional["torch.Tensor"]  # noqa: F821
+    codes: Optional["torch.Tensor"]  # noqa: F821
+    scales: Optional["torch.Tensor"]  # noqa: F821
+
+
+def add_norm(y, residual=None, norm="rms", weight=None, bias=None, eps: float = 1e-6,
+             post_norm=None, post_weight=None, post_bias=None, gate=None, gate_group=None,
+             residual_scale: float = 1.0, block_scale: float = 1.0, residual_out=True,
+             normed=True, codes: Optional[str] = None, inv_smooth=None) -> AddNorm:
+    """Norms before and after a block, in one pass over its rows:
+
+        r = residual_scale * residual + block_scale * gate * post(y)
+        n = norm(r)
+
+    y: bf16 [T][H]; residual: bf16 or fp32 [T][H], or None.
+    norm, post_norm: "rms", "layer" or "none"; weights and biases fp32 [H].
+    post_norm defaults to `norm`'s kind where post_weight is given, else none.
+    gate: fp32 [T] or [T][1] (per token), or bf16 [G][H]: row t takes gate row
+    t // gate_group, where gate_group defaults to ceil(T / G) (one row: a gate
+    per channel; T rows: a gate of its own; a row per sequence otherwise).
+    residual_out, normed: True (a new tensor), False, or the tensor to write
+    (residual_out may be residual, normed may be y).
+    codes: None, "int8" or "fp8": codes of n * inv_smooth for the next product.
+    Returns AddNorm(residual, normed, codes, scales), None where not asked."""
+    import torch
+    if not isinstance(y, torch.Tensor) or y.dim() != 2:
+        _fail("y must be a [T][H] tensor")
+    T, H = y.shape
+    dev = y.device
+    bf16 = (torch.bfloat16,)
+    if post_norm is None and (post_weight is not None or post_bias is not None):
+        post_norm = norm
+    if norm not in _NORMS or post_norm not in _NORMS:
+        _fail("norm must be 'rms', 'layer' or 'none'")
+    if codes is not None and codes not in _FORMATS:
+        _fail("codes must be 'int8' or 'fp8'")
+    a = _m.moe_w8a8_add_norm_args()
+    a.hidden, a.pre_norm, a.post_norm = H, _NORMS[norm], _NORMS[post_norm]
+    a.eps, a.residual_scale, a.block_scale = eps, residual_scale, block_scale
+    a.y, a.ld_y = _rows(y, "y", bf16, T, H, dev)
+    rtype = torch.bfloat16
+    if residual is not None:
+        a.residual, a.ld_residual = _rows(residual, "residual", (torch.bfloat16, torch.float32),
+                                          T, H, dev)
+        rtype = residual.dtype
+    elif isinstance(residual_out, torch.Tensor):
+        rtype = residual_out.dtype
+    if residual_out is True:
+        residual_out = torch.empty(T, H, dtype=rtype, device=dev)
+    elif residual_out is False:
+        residual_out = None
+    if residual_out is not None:
+        a.residual_out, a.ld_residual_out = _rows(
+            residual_out, "residual_out",
+            (rtype,) if residual is not None else (torch.bfloat16, torch.float32), T, H, dev)
+    a.residual_type = 1 if rtype == torch.float32 else 0
+    if normed is True:
+        normed = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    elif normed is False:
+        normed = None
+    if normed is not None:
+        a.normed, a.ld_normed = _rows(normed, "normed", bf16, T, H, dev)
+    if weight is not None:
+        a.pre_weight = _vector(weight, "weight", H, dev)
+    if bias is not None:
+        a.pre_bias = _vector(bias, "bias", H, dev)
+    if post_weight is not None:
+        a.post_weight = _vector(post_weight, "post_weight", H, dev)
+    if post_bias is not None:
+        a.post_bias = _vector(post_bias, "post_bias", H, dev)
+    if gate is not None and T > 0:
+        if isinstance(gate, torch.Tensor) and gate.dtype == torch.float32:
+            if gate.shape not in ((T,), (T, 1)):
+                _fail("an fp32 gate must be [T] or [T][1]")
+            a.gate_token = _vector(gate, "gate", T, dev)
+        else:
+            if not isinstance(gate, torch.Tensor) or gate.dim() != 2 or gate.shape[0] < 1:
+                _fail("gate must be fp32 [T] or bf16 [G][H]")
+            G = gate.shape[0]
+            a.gate_rows, a.ld_gate = _rows(gate, "gate", bf16, G, H, dev)
+            a.gate_group = -(-T // G) if gate_group is None else int(gate_group)
+            if a.gate_group < 1 or -(-T // a.gate_group) > G:
+                _fail("gate has %d rows, too few for %d tokens in groups of %d" %
+                      (G, T, a.gate_group))
+    q = s = None
+    if codes is not None:
+        q, s = _empty_codes(T, H, codes == "fp8", dev)
+        a.q, a.s, a.format = q.data_ptr(), s.data_ptr(), _FORMATS[codes]
+        if inv_smooth is not None:
+            a.inv_smooth = _vector(inv_smooth, "inv_smooth", H, dev)
+    with _on(dev):
+        _m._check(_m.moe_w8a8_add_norm(a, T), "moe_w8a8_add_norm")
+    return AddNorm(residual_out, normed, q, s)

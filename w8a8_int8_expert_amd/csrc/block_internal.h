@@ -1,0 +1,76 @@
+// block_internal.h -- internal declarations of the operators of the block
+// around the layer (moe_w8a8_linear, _ffn, _act_quant, _add_norm). Not part of
+// the public ABI (include/moe_w8a8.h).
+#pragma once
+
+#include "moe_internal.h"
+#include "moe_w8a8.h"
+
+namespace moe {
+
+constexpr int kMaxWidth = 65536;      // K, H, F
+constexpr int kMaxOutputs = 1 << 20;  // N
+// Pitch of code rows (and of the h rows): 128 columns are one cache line of
+// codes and the pair of 64-k tiles that an FP8 matrix instruction takes.
+inline __host__ __device__ int row_pitch(int K) { return (K + 127) / 128 * 128; }
+// Rows of a packed weight matrix: N rounded up to whole 16-row tiles; gated,
+// F = N/2 rounded up to 32 in runs of 32 gate rows and 32 up rows.
+inline __host__ __device__ int packed_rows(int N, bool gated) {
+  return gated ? (N / 2 + 31) / 32 * 64 : (N + 15) / 16 * 16;
+}
+// Source row of packed row p, or -1 (padding).
+inline __host__ __device__ int source_row(int p, int N, bool gated) {
+  if (!gated) return p < N ? p : -1;
+  const int F = N / 2, f = p / 64 * 32 + p % 32;
+  return f < F ? (p / 32 % 2) * F + f : -1;
+}
+
+// What a product does with its sums.
+struct Epilogue {
+  const float *row_scale;  // [T]
+  const float *scale;      // per packed row
+  const float *bias;       // [N] or NULL
+  int N;                   // columns of out (plain), F (gated)
+  void *out;               // plain: bf16 or fp32 [T][ld_out]; gated: h fp32 [T][ld_out]
+  int64_t ld_out;
+  int out_f32;
+  const float *gate;  // [T] or NULL
+  const uint16_t *add;
+  int64_t ld_add;
+  uint32_t *amax;  // gated: row max |h| (float bits), or NULL
+};
+
+// Largest batch of the streaming product, and of its form that codes the
+// tokens itself.
+constexpr int kStreamRows = 64;
+constexpr int kFusedRows = 4;
+// Partial sums of the products that split K over blocks.
+constexpr size_t kPartialBytes = (size_t)32 << 20;
+
+hipError_t launch_act_rows(const uint16_t *x, int64_t ld_x, int64_t T, int K, const float *inv,
+                           bool fp8, int8_t *q, float *s, uint32_t *clear, hipStream_t st);
+hipError_t launch_clear(uint32_t *p, int64_t n, hipStream_t st);
+// h fp32 [T][Fp] with row max |h| -> codes [T][Fp], scales
+hipError_t launch_requant_rows(const float *h, const uint32_t *amax, int64_t T, int F, bool fp8,
+                               int8_t *q, float *s, hipStream_t st);
+hipError_t launch_add_norm(const moe_w8a8_add_norm_args &a, int64_t T, hipStream_t st);
+// src_type: MOE_W8A8_BF16, MOE_W8A8_F32, or -1 for codes (with their scales)
+hipError_t launch_pack_rows(const moe_w8a8_linear_weights &w, const void *src, int src_type,
+                            int64_t ld, const float *smooth, const float *src_scale,
+                            hipStream_t st);
+// T <= kStreamRows; codes q/s, or (T <= kFusedRows) bf16 rows x or fp32 rows h
+// that the kernel codes itself.
+struct StreamIn {
+  const int8_t *q;  // codes [T][Kp] (row scales in Epilogue), or NULL
+  const uint16_t *x;
+  const float *h;
+  int64_t ld;        // of x or h
+  const float *inv;  // of x
+};
+hipError_t launch_linear_stream(const StreamIn &in, int T, const int8_t *w, int K, int Np,
+                                bool gated, bool fp8, const Epilogue &ep, hipStream_t st);
+hipError_t launch_linear_tiled(const int8_t *q, int64_t T, const int8_t *w, int K, int Np,
+                               bool gated, bool fp8, const Epilogue &ep, void *partial,
+                               hipStream_t st);
+
+}  // namespace moe

@@ -1,0 +1,65 @@
+// epilogue_device.h -- what the W8A8 products of the decoder block do with a
+// dequantised value: bias, gate per token, add, one rounding to the output
+// type. Included by the HIP sources only.
+#pragma once
+
+#include "lds_dma.h"
+#include "row_device.h"
+
+namespace moe {
+
+// n consecutive columns (n0.., VN of them at most, those below ep.N exist) of
+// row t: v holds the dequantised sums.
+template <int VN>
+__device__ __forceinline__ void finish_columns(const Epilogue &ep, int64_t t, int n0, float *v) {
+  const int rem = ep.N - n0;
+  if (rem <= 0) return;
+  if (ep.bias) {
+#pragma unroll
+    for (int i = 0; i < VN; ++i)
+      if (i < rem) v[i] += ep.bias[n0 + i];
+  }
+  if (ep.gate) {
+    const float g = ep.gate[t];
+#pragma unroll
+    for (int i = 0; i < VN; ++i) v[i] *= g;
+  }
+  if (ep.add) {
+    const uint16_t *p = ep.add + t * ep.ld_add + n0;
+    if constexpr (VN == 8) {
+      float b[8];
+      load8(p, rem, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += b[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < VN; ++i)
+        if (i < rem) v[i] += bf16_to_f32(p[i]);
+    }
+  }
+  if (ep.out_f32) {
+    float *o = static_cast<float *>(ep.out) + t * ep.ld_out + n0;
+    if constexpr (VN == 8) {
+      store8(o, rem, v);
+    } else if (rem >= VN) {
+      *reinterpret_cast<v4f_a4 *>(o) = v4f{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < VN; ++i)
+        if (i < rem) o[i] = v[i];
+    }
+  } else {
+    uint16_t *o = static_cast<uint16_t *>(ep.out) + t * ep.ld_out + n0;
+    if constexpr (VN == 8) {
+      store8(o, rem, v);
+    } else if (rem >= VN) {
+      *reinterpret_cast<v2i_a2 *>(o) = v2i{(int)bf16x2(v[0], v[1]), (int)bf16x2(v[2], v[3])};
+    } else {
+#pragma unroll
+      for (int i = 0; i < VN; ++i)
+        if (i < rem) o[i] = f32_to_bf16(v[i]);
+    }
+  }
+}
+
+}  // namespace moe

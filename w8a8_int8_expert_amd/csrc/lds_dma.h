@@ -1,0 +1,58 @@
+// lds_dma.h -- device building blocks shared by the tiled matrix products: direct
+// global -> LDS loads, the wait that goes with them, and the epilogue's SwiGLU
+// and row maximum. Included by the HIP sources only.
+#pragma once
+
+#include "moe_internal.h"
+
+// The direct-to-LDS loads are issued from inline assembly: the compiler's own
+// intrinsic makes every later LDS read wait for all outstanding loads, which
+// would drain the stage ring on each step. The assembly sets M0 (the LDS base
+// of the wavefront's 1 KB) itself, and the waits are explicit.
+#pragma clang diagnostic ignored "-Winline-asm"
+
+namespace moe {
+
+__device__ __forceinline__ uint32_t lds_addr(const void *p) {
+  return (uint32_t)(uintptr_t)((__attribute__((address_space(3))) const void *)p);
+}
+// 16 bytes per lane from global memory into LDS at lds_base + 16*lane. An
+// LDS-DMA load needs one wait state after M0 is written.
+__device__ __forceinline__ void dma16(const void *g, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :
+               : "v"(g), "s"(lds_base)
+               : "memory", "m0");
+}
+// Wait until at most N of this wavefront's loads are in flight and its LDS
+// accesses are done, then meet the other wavefronts of the block.
+template <int N>
+__device__ __forceinline__ void wait_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+
+// Maximum of a non-negative value over each 32-lane half of the wavefront,
+// by DPP moves (no LDS round trip): row_shr 1, 2, 4, 8 leave each 16-lane
+// row's maximum in its lane 15, and row_bcast15 into rows 1 and 3 adds the
+// row below. The results land in lanes 31 and 63. Non-negative floats order
+// as their bit patterns, so the maximum is taken on those.
+__device__ __forceinline__ uint32_t half_wave_max(uint32_t m) {
+  auto step = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
+  m = step(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x111, 0xF, 0xF, false));
+  m = step(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x112, 0xF, 0xF, false));
+  m = step(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x114, 0xF, 0xF, false));
+  m = step(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x118, 0xF, 0xF, false));
+  m = step(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x142, 0xA, 0xF, false));
+  return m;
+}
+
+// silu(g) * u with the hardware exponential and reciprocal.
+__device__ __forceinline__ float swiglu(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
+// Accumulators: INT32 for INT8 codes, fp32 for FP8 codes.
+template <bool kF8> struct Acc32 { typedef v16i T; };
+template <> struct Acc32<true> { typedef v16f T; };
+
+}  // namespace moe
