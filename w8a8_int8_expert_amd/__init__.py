@@ -479,4 +479,14 @@ class MoEW8A8:
         return out
 
 
-from .block import AddNorm, W8A8FFN, W8A8Linear, act_quant, add_norm  # noqa: E402,F401
+_BLOCK = ("AddNorm", "W8A8FFN", "W8A8Linear", "act_quant", "add_norm")
+
+
+def __getattr__(name):
+    """The block operators come from .block, which imports torch, on first use."""
+    if name in _BLOCK:
+        from . import block
+        for n in _BLOCK:
+            globals()[n] = getattr(block, n)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -15,14 +15,23 @@ from them, share nothing but the weights.
 """
 from __future__ import annotations
 
-import contextlib
+import ctypes
 from typing import NamedTuple, Optional
+
+import torch
 
 import w8a8_int8_expert_amd as _m
 
+_BF16, _F32, _I8, _E4M3 = torch.bfloat16, torch.float32, torch.int8, torch.float8_e4m3fn
+_OUT_TYPES = (_BF16, _F32)
 _FORMATS = {"int8": 0, "fp8": 1}
 _NORMS = {None: 0, "none": 0, "rms": 1, "layer": 2}
-_SAME = contextlib.nullcontext()
+# A call of one token is a few microseconds of GPU work: what the binding does
+# per call is kept as small. The stream's handle comes from the same function
+# that torch.cuda.current_stream wraps in an object.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
+    torch._C, "_cuda_getCurrentRawStream") else \
+    (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _fail(msg):
@@ -30,26 +39,29 @@ def _fail(msg):
 
 
 def _device(device):
-    import torch
     device = torch.device(device)
     if device.type == "cuda" and device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
     return device
 
 
-def _on(device):
-    """Context in which `device` is current (nothing to do if it already is)."""
-    import torch
+def _call(name, device, *args):
+    """One library call with `device` current, on torch's current stream of it."""
     if device.type != "cuda":
         _fail("the operands must be on a GPU")
-    if torch.cuda.current_device() == device.index:
-        return _SAME
-    return torch.cuda.device(device)
+    f = getattr(_m._lib or _m.load_library(), name)
+    i = device.index
+    if torch.cuda.current_device() == i:
+        rc = f(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            rc = f(*args, _raw_stream(i))
+    if rc != 0:
+        _m._check(rc, name)
 
 
 def _rows(t, name, dtypes, T, width, device):
     """(address, row pitch) of a [T][width] tensor whose rows are contiguous."""
-    import torch
     if not isinstance(t, torch.Tensor):
         _fail("%s must be a torch tensor" % name)
     if t.dtype not in dtypes:
@@ -70,43 +82,37 @@ def _rows(t, name, dtypes, T, width, device):
 
 def _vector(t, name, n, device):
     """Address of a contiguous fp32 [n] tensor, None for None."""
-    import torch
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.numel() != n or \
+    if not isinstance(t, torch.Tensor) or t.dtype != _F32 or t.numel() != n or \
             not t.is_contiguous() or t.device != device:
         _fail("%s must be a contiguous fp32 tensor of %d values on %s" % (name, n, device))
     return t.data_ptr()
 
 
 def _code_types(fp8):
-    import torch
-    return (torch.float8_e4m3fn, torch.int8) if fp8 else (torch.int8,)
+    return (_E4M3, _I8) if fp8 else (_I8,)
 
 
 def _empty_codes(T, K, fp8, device):
-    import torch
-    pitch = _m.moe_w8a8_row_pitch(K)
-    if pitch == 0:
+    if not 1 <= K <= 65536:
         _fail("unsupported width %d" % K)
-    return (torch.empty(T, pitch, dtype=torch.float8_e4m3fn if fp8 else torch.int8, device=device),
-            torch.empty(T, dtype=torch.float32, device=device))
+    pitch = (K + 127) // 128 * 128
+    return (torch.empty(T, pitch, dtype=_E4M3 if fp8 else _I8, device=device),
+            torch.empty(T, dtype=_F32, device=device))
 
 
 def act_quant(x, inv_smooth=None, fp8: bool = False):
     """Per-token codes of bf16 rows x [T][K], times inv_smooth (fp32 [K]):
     (codes [T][Kp], scales fp32 [T]), Kp = moe_w8a8_row_pitch(K), zeros past K."""
-    import torch
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         _fail("x must be a [T][K] tensor")
     T, K = x.shape
     dev = x.device
-    px, ld = _rows(x, "x", (torch.bfloat16,), T, K, dev)
+    px, ld = _rows(x, "x", (_BF16,), T, K, dev)
     inv = _vector(inv_smooth, "inv_smooth", K, dev)
     q, s = _empty_codes(T, K, fp8, dev)
-    with _on(dev):
-        _m._check(_m.moe_w8a8_act_quant(K, int(bool(fp8)), px, ld, T, inv, q, s),
-                  "moe_w8a8_act_quant")
+    _call("moe_w8a8_act_quant", dev, K, int(bool(fp8)), px, ld, T, inv, q.data_ptr(), s.data_ptr())
     return q, s
 
 
@@ -115,18 +121,18 @@ class _Weights:
     them."""
 
     def __init__(self, K, N, fp8, gated, device):
-        import torch
         size = _m.moe_w8a8_linear_codes_bytes(N, K, gated)
         if size == 0:
             _fail("unsupported weight shape [%d][%d]" % (N, K))
         self.K, self.N, self.fp8, self.gated, self.device = K, N, fp8, gated, device
-        self.codes = torch.empty(size, dtype=torch.int8, device=device)
-        self.scale = torch.empty(_m.moe_w8a8_linear_scales(N, gated), dtype=torch.float32,
+        self.codes = torch.empty(size, dtype=_I8, device=device)
+        self.scale = torch.empty(_m.moe_w8a8_linear_scales(N, gated), dtype=_F32,
                                  device=device)
         self.inv_smooth = self.bias = None
         self.struct = _m.moe_w8a8_linear_weights(K, N, int(fp8), int(gated),
                                                  self.codes.data_ptr(), self.scale.data_ptr(),
                                                  None, None)
+        self.ref = ctypes.byref(self.struct)
 
     def vectors(self, inv_smooth, bias):
         """Keep copies of the two optional vectors."""
@@ -137,26 +143,20 @@ class _Weights:
             setattr(self.struct, name, None if t is None else t.data_ptr())
 
     def quantise(self, w, smooth):
-        import torch
-        p, ld = _rows(w, "weight", (torch.bfloat16, torch.float32), self.N, self.K, self.device)
-        with _on(self.device):
-            _m._check(_m.moe_w8a8_linear_quantise(
-                self.struct, p, 1 if w.dtype == torch.float32 else 0, ld,
-                _vector(smooth, "smooth", self.K, self.device)), "moe_w8a8_linear_quantise")
+        p, ld = _rows(w, "weight", (_BF16, _F32), self.N, self.K, self.device)
+        _call("moe_w8a8_linear_quantise", self.device, self.ref, p, 1 if w.dtype == _F32 else 0,
+              ld, _vector(smooth, "smooth", self.K, self.device))
 
     def load(self, q, s):
         p, ld = _rows(q, "codes", _code_types(self.fp8), self.N, self.K, self.device)
-        with _on(self.device):
-            _m._check(_m.moe_w8a8_linear_pack(self.struct, p, ld,
-                                              _vector(s, "scales", self.N, self.device)),
-                      "moe_w8a8_linear_pack")
+        _call("moe_w8a8_linear_pack", self.device, self.ref, p, ld,
+              _vector(s, "scales", self.N, self.device))
 
 
 class _Product:
     """What the two products share: their operands and their result."""
 
     def _operands(self, x, codes, K, N, add, gate, out, out_dtype):
-        import torch
         dev = self.device
         if (x is None) == (codes is None):
             _fail("give either x or codes")
@@ -166,9 +166,9 @@ class _Product:
         T = first.shape[0]
         act = _m.moe_w8a8_act()
         if codes is None:
-            act.x, act.ld_x = _rows(x, "x", (torch.bfloat16,), T, K, dev)
+            act.x, act.ld_x = _rows(x, "x", (_BF16,), T, K, dev)
         else:
-            pitch = _m.moe_w8a8_row_pitch(K)
+            pitch = (K + 127) // 128 * 128
             act.q, ld = _rows(first, "codes", _code_types(self.fp8), T, pitch, dev)
             if ld != pitch:
                 _fail("codes must be contiguous")
@@ -176,22 +176,17 @@ class _Product:
             if act.s is None and T > 0:
                 _fail("codes come with their scales")
         if out is None:
-            out = torch.empty(T, N, dtype=out_dtype or torch.bfloat16, device=dev)
+            out = torch.empty(T, N, dtype=out_dtype or _BF16, device=dev)
         elif out_dtype is not None and out.dtype != out_dtype:
             _fail("out must be %s, got %s" % (out_dtype, out.dtype))
         res = _m.moe_w8a8_result()
-        res.out, res.ld_out = _rows(out, "out", (torch.bfloat16, torch.float32), T, N, dev)
-        res.out_type = 1 if out.dtype == torch.float32 else 0
+        res.out, res.ld_out = _rows(out, "out", _OUT_TYPES, T, N, dev)
+        res.out_type = 1 if out.dtype == _F32 else 0
         if gate is not None:
             res.gate = _vector(gate, "gate", T, dev)
         if add is not None:
-            res.add, res.ld_add = _rows(add, "add", (torch.bfloat16,), T, N, dev)
+            res.add, res.ld_add = _rows(add, "add", (_BF16,), T, N, dev)
         return T, act, res, out
-
-
-def _workspace(n, device):
-    import torch
-    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
 class W8A8Linear(_Product):
@@ -224,10 +219,10 @@ class W8A8Linear(_Product):
         give them. gate fp32 [T]; add bf16 [T][N] (may be out itself)."""
         T, act, res, out = self._operands(x, codes, self.in_features, self.out_features, add,
                                           gate, out, out_dtype)
-        n = _m.moe_w8a8_linear_workspace_size(self.out_features, self.in_features, T)
-        ws = _workspace(n, self.device)
-        with _on(self.device):
-            _m._check(_m.moe_w8a8_linear(self._w.struct, act, T, res, ws, n), "moe_w8a8_linear")
+        n = _m._lib.moe_w8a8_linear_workspace_size(self.out_features, self.in_features, T)
+        ws = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+        _call("moe_w8a8_linear", self.device, self._w.ref, ctypes.byref(act), T,
+              ctypes.byref(res), ws.data_ptr() if n else None, n)
         return out
 
     __call__ = forward
@@ -268,11 +263,10 @@ class W8A8FFN(_Product):
         As a shared expert: ffn.forward(x, add=moe.forward(x, ...), gate=g)."""
         T, act, res, out = self._operands(x, codes, self.hidden, self.out_features, add, gate,
                                           out, out_dtype)
-        n = _m.moe_w8a8_ffn_workspace_size(self.hidden, self.ffn, self.out_features, T)
-        ws = _workspace(n, self.device)
-        with _on(self.device):
-            _m._check(_m.moe_w8a8_ffn(self._gu.struct, self._dn.struct, act, T, res, ws, n),
-                      "moe_w8a8_ffn")
+        n = _m._lib.moe_w8a8_ffn_workspace_size(self.hidden, self.ffn, self.out_features, T)
+        ws = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+        _call("moe_w8a8_ffn", self.device, self._gu.ref, self._dn.ref, ctypes.byref(act), T,
+              ctypes.byref(res), ws.data_ptr() if n else None, n)
         return out
 
     __call__ = forward
@@ -304,12 +298,11 @@ def add_norm(y, residual=None, norm="rms", weight=None, bias=None, eps: float = 
     (residual_out may be residual, normed may be y).
     codes: None, "int8" or "fp8": codes of n * inv_smooth for the next product.
     Returns AddNorm(residual, normed, codes, scales), None where not asked."""
-    import torch
     if not isinstance(y, torch.Tensor) or y.dim() != 2:
         _fail("y must be a [T][H] tensor")
     T, H = y.shape
     dev = y.device
-    bf16 = (torch.bfloat16,)
+    bf16 = (_BF16,)
     if post_norm is None and (post_weight is not None or post_bias is not None):
         post_norm = norm
     if norm not in _NORMS or post_norm not in _NORMS:
@@ -320,9 +313,9 @@ def add_norm(y, residual=None, norm="rms", weight=None, bias=None, eps: float = 
     a.hidden, a.pre_norm, a.post_norm = H, _NORMS[norm], _NORMS[post_norm]
     a.eps, a.residual_scale, a.block_scale = eps, residual_scale, block_scale
     a.y, a.ld_y = _rows(y, "y", bf16, T, H, dev)
-    rtype = torch.bfloat16
+    rtype = _BF16
     if residual is not None:
-        a.residual, a.ld_residual = _rows(residual, "residual", (torch.bfloat16, torch.float32),
+        a.residual, a.ld_residual = _rows(residual, "residual", (_BF16, _F32),
                                           T, H, dev)
         rtype = residual.dtype
     elif isinstance(residual_out, torch.Tensor):
@@ -334,10 +327,10 @@ def add_norm(y, residual=None, norm="rms", weight=None, bias=None, eps: float = 
     if residual_out is not None:
         a.residual_out, a.ld_residual_out = _rows(
             residual_out, "residual_out",
-            (rtype,) if residual is not None else (torch.bfloat16, torch.float32), T, H, dev)
-    a.residual_type = 1 if rtype == torch.float32 else 0
+            (rtype,) if residual is not None else (_BF16, _F32), T, H, dev)
+    a.residual_type = 1 if rtype == _F32 else 0
     if normed is True:
-        normed = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        normed = torch.empty(T, H, dtype=_BF16, device=dev)
     elif normed is False:
         normed = None
     if normed is not None:
@@ -351,7 +344,7 @@ def add_norm(y, residual=None, norm="rms", weight=None, bias=None, eps: float = 
     if post_bias is not None:
         a.post_bias = _vector(post_bias, "post_bias", H, dev)
     if gate is not None and T > 0:
-        if isinstance(gate, torch.Tensor) and gate.dtype == torch.float32:
+        if isinstance(gate, torch.Tensor) and gate.dtype == _F32:
             if gate.shape not in ((T,), (T, 1)):
                 _fail("an fp32 gate must be [T] or [T][1]")
             a.gate_token = _vector(gate, "gate", T, dev)
@@ -370,6 +363,5 @@ def add_norm(y, residual=None, norm="rms", weight=None, bias=None, eps: float = 
         a.q, a.s, a.format = q.data_ptr(), s.data_ptr(), _FORMATS[codes]
         if inv_smooth is not None:
             a.inv_smooth = _vector(inv_smooth, "inv_smooth", H, dev)
-    with _on(dev):
-        _m._check(_m.moe_w8a8_add_norm(a, T), "moe_w8a8_add_norm")
+    _call("moe_w8a8_add_norm", dev, ctypes.byref(a), T)
     return AddNorm(residual_out, normed, q, s)

@@ -99,13 +99,15 @@ LinearLayout linear_layout(int K, int64_t T) {
   LinearLayout L{};
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += up256(bytes); return at; };
-  if (T == 0) return L;
+  if (T == 0 || fused_rows(T, K)) return L;
   L.q = take((size_t)T * row_pitch(K));
   L.s = take((size_t)T * 4);
   L.partial = take(T > kStreamRows ? kPartialBytes : 0);
   L.total = o;
   return L;
 }
+// h holds gate and up values (T <= kStreamRows: fp32 [T][packed rows]) or
+// hidden values (fp32 [T][Fp]).
 struct FfnLayout {
   size_t q, s, h, amax, qh, sh, partial, total;
 };
@@ -114,12 +116,20 @@ FfnLayout ffn_layout(int H, int F, int64_t T) {
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += up256(bytes); return at; };
   if (T == 0) return L;
-  L.q = take((size_t)T * row_pitch(H));
-  L.s = take((size_t)T * 4);
-  L.h = take((size_t)T * row_pitch(F) * 4);
-  L.amax = take((size_t)T * 4);
-  L.qh = take((size_t)T * row_pitch(F));
-  L.sh = take((size_t)T * 4);
+  // (the larger of the two for few rows: a workspace never shrinks as T grows)
+  const int64_t few = T < kStreamRows ? T : kStreamRows;
+  const size_t gu = (size_t)few * packed_rows(2 * F, true) * 4;
+  const size_t hid = (size_t)T * row_pitch(F) * 4;
+  L.h = take(gu > hid ? gu : hid);
+  if (!fused_rows(T, H)) {
+    L.q = take((size_t)T * row_pitch(H));
+    L.s = take((size_t)T * 4);
+  }
+  if (!fused_rows(T, F)) {
+    L.amax = take((size_t)T * 4);
+    L.qh = take((size_t)T * row_pitch(F));
+    L.sh = take((size_t)T * 4);
+  }
   L.partial = take(T > kStreamRows ? kPartialBytes : 0);
   L.total = o;
   return L;
@@ -131,7 +141,7 @@ hipError_t product(const StreamIn &in, const int8_t *q, int64_t T,
   const bool gated = w.gated != 0, fp8 = w.format == MOE_W8A8_FORMAT_FP8;
   const int K = w.in_features, Np = packed_rows(w.out_features, gated);
   if (T <= kStreamRows)
-    return launch_linear_stream(in, (int)T, w.w, K, Np, gated, fp8, ep, st);
+    return launch_linear_stream(in, (int)T, w.w, K, Np, fp8, ep, st);
   return launch_linear_tiled(q, T, w.w, K, Np, gated, fp8, ep, partial, st);
 }
 
@@ -219,7 +229,7 @@ extern "C" int moe_w8a8_linear(const moe_w8a8_linear_weights *w, const moe_w8a8_
   MOE_TRY(result_check(res, act, T, K, w->out_features));
   const LinearLayout L = linear_layout(K, T);
   if (!al(workspace, 256)) return MOE_W8A8_ERR_INVALID;
-  if (!workspace || workspace_bytes < L.total) return MOE_W8A8_ERR_WORKSPACE;
+  if (L.total > 0 && (!workspace || workspace_bytes < L.total)) return MOE_W8A8_ERR_WORKSPACE;
   hipStream_t st = (hipStream_t)stream;
   char *ws = (char *)workspace;
   Epilogue ep = epilogue(*w, *res);
@@ -265,35 +275,40 @@ extern "C" int moe_w8a8_ffn(const moe_w8a8_linear_weights *gu, const moe_w8a8_li
   char *ws = (char *)workspace;
   float *h = (float *)(ws + L.h);
   uint32_t *amax = (uint32_t *)(ws + L.amax);
-  // With few rows the down product finds the hidden rows' maxima itself.
-  const bool own_max = fused_rows(T, F);
+  const bool few = T <= kStreamRows;  // else SwiGLU and row maxima in the first product
 
   Epilogue ep{};
-  ep.scale = gu->scale; ep.N = F; ep.out = h; ep.ld_out = row_pitch(F); ep.out_f32 = 1;
-  ep.amax = own_max ? nullptr : amax;
+  ep.scale = gu->scale; ep.out = h; ep.out_f32 = 1;
+  const int Np = packed_rows(2 * F, true);
+  ep.N = few ? Np : F;
+  ep.ld_out = few ? Np : row_pitch(F);
+  ep.amax = amax;
   StreamIn in{};
   if (act->x && fused_rows(T, H)) {
     in.x = act->x; in.ld = act->ld_x; in.inv = gu->inv_smooth;
-    if (!own_max) MOE_CHECK(launch_clear(amax, T, st));
   } else if (act->x) {
     int8_t *q = (int8_t *)(ws + L.q);
     float *s = (float *)(ws + L.s);
-    MOE_CHECK(launch_act_rows(act->x, act->ld_x, T, H, gu->inv_smooth, fp8, q, s, amax, st));
+    MOE_CHECK(launch_act_rows(act->x, act->ld_x, T, H, gu->inv_smooth, fp8, q, s,
+                              few ? nullptr : amax, st));
     in.q = q; ep.row_scale = s;
   } else {
     in.q = act->q; ep.row_scale = act->s;
-    if (!own_max) MOE_CHECK(launch_clear(amax, T, st));
+    if (!few) MOE_CHECK(launch_clear(amax, T, st));
   }
   MOE_CHECK(product(in, in.q, T, *gu, ep, ws + L.partial, st));
 
   Epilogue ed = epilogue(*dn, *res);
   StreamIn hin{};
-  if (own_max) {
-    hin.h = h; hin.ld = row_pitch(F);
+  if (fused_rows(T, F)) {
+    hin.h = h; hin.ld = Np;
   } else {
     int8_t *qh = (int8_t *)(ws + L.qh);
     float *sh = (float *)(ws + L.sh);
-    MOE_CHECK(launch_requant_rows(h, amax, T, F, fp8, qh, sh, st));
+    if (few)
+      MOE_CHECK(launch_hidden_rows(h, Np, T, F, fp8, qh, sh, st));
+    else
+      MOE_CHECK(launch_requant_rows(h, amax, T, F, fp8, qh, sh, st));
     hin.q = qh; ed.row_scale = sh;
   }
   MOE_CHECK(product(hin, hin.q, T, *dn, ed, ws + L.partial, st));

@@ -50,6 +50,10 @@ constexpr size_t kPartialBytes = (size_t)32 << 20;
 hipError_t launch_act_rows(const uint16_t *x, int64_t ld_x, int64_t T, int K, const float *inv,
                            bool fp8, int8_t *q, float *s, uint32_t *clear, hipStream_t st);
 hipError_t launch_clear(uint32_t *p, int64_t n, hipStream_t st);
+// Gate and up values fp32 [T][ld] in packed order (a streaming product's plain
+// output) -> codes [T][Fp] and scales of h = silu(g) u
+hipError_t launch_hidden_rows(const float *gu, int64_t ld, int64_t T, int F, bool fp8, int8_t *q,
+                              float *s, hipStream_t st);
 // h fp32 [T][Fp] with row max |h| -> codes [T][Fp], scales
 hipError_t launch_requant_rows(const float *h, const uint32_t *amax, int64_t T, int F, bool fp8,
                                int8_t *q, float *s, hipStream_t st);
@@ -58,17 +62,18 @@ hipError_t launch_add_norm(const moe_w8a8_add_norm_args &a, int64_t T, hipStream
 hipError_t launch_pack_rows(const moe_w8a8_linear_weights &w, const void *src, int src_type,
                             int64_t ld, const float *smooth, const float *src_scale,
                             hipStream_t st);
-// T <= kStreamRows; codes q/s, or (T <= kFusedRows) bf16 rows x or fp32 rows h
-// that the kernel codes itself.
+// T <= kStreamRows; codes q (row scales in Epilogue), or (T <= kFusedRows) rows
+// that the kernel codes itself: bf16 tokens x, or the hidden rows of gate and
+// up values h in packed order.
 struct StreamIn {
-  const int8_t *q;  // codes [T][Kp] (row scales in Epilogue), or NULL
+  const int8_t *q;  // codes [T][Kp], or NULL
   const uint16_t *x;
   const float *h;
   int64_t ld;        // of x or h
   const float *inv;  // of x
 };
-hipError_t launch_linear_stream(const StreamIn &in, int T, const int8_t *w, int K, int Np,
-                                bool gated, bool fp8, const Epilogue &ep, hipStream_t st);
+hipError_t launch_linear_stream(const StreamIn &in, int T, const int8_t *w, int K, int Np, bool fp8,
+                                const Epilogue &ep, hipStream_t st);
 hipError_t launch_linear_tiled(const int8_t *q, int64_t T, const int8_t *w, int K, int Np,
                                bool gated, bool fp8, const Epilogue &ep, void *partial,
                                hipStream_t st);

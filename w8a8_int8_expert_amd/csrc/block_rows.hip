@@ -94,6 +94,30 @@ __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void act_rows_kernel(
   emit_codes<TPR, NC>(v, lane, Kp, m, fp8, q + t * Kp, s + t);
 }
 
+// Codes of the hidden rows of a streaming gate/up product.
+template <int TPR, int NC>
+__global__ __launch_bounds__(RowGroup<TPR>::kThreads) void hidden_rows_kernel(
+    const float *__restrict__ gu, int64_t ld, int64_t T, int F, bool fp8, int8_t *__restrict__ q,
+    float *__restrict__ s) {
+  typedef RowGroup<TPR> G;
+  __shared__ float cells[G::kWaves];
+  const int lane = threadIdx.x % TPR;
+  const int64_t t = (int64_t)blockIdx.x * G::kRows + threadIdx.x / TPR;
+  if (t >= T) return;  // as in act_rows_kernel
+  float v[NC][8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = (lane + i * TPR) * 8;
+    hidden8(gu + t * ld, c, F - c, v[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = umax(m, abs_bits(v[i][j]));
+  }
+  m = G::max_bits(m, cells);
+  const int Fp = row_pitch(F);
+  emit_codes<TPR, NC>(v, lane, Fp, m, fp8, q + t * Fp, s + t);
+}
+
 __global__ __launch_bounds__(256) void clear_kernel(uint32_t *__restrict__ p, int64_t n) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i < n) p[i] = 0u;
@@ -344,6 +368,11 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const void *__restrict__
 hipError_t launch_act_rows(const uint16_t *x, int64_t ld, int64_t T, int K, const float *inv,
                            bool fp8, int8_t *q, float *s, uint32_t *clear, hipStream_t st) {
   MOE_ROWS_BY_WIDTH(act_rows_kernel, K, x, ld, T, K, inv, fp8, q, s, clear);
+}
+
+hipError_t launch_hidden_rows(const float *gu, int64_t ld, int64_t T, int F, bool fp8, int8_t *q,
+                              float *s, hipStream_t st) {
+  MOE_ROWS_BY_WIDTH(hidden_rows_kernel, F, gu, ld, T, F, fp8, q, s);
 }
 
 hipError_t launch_add_norm(const moe_w8a8_add_norm_args &a, int64_t T, hipStream_t st) {

@@ -8,13 +8,20 @@
 // among its wavefronts in pairs of 64-k tiles (2 KB of a panel, contiguous),
 // interleaved so that the block reads adjacent tiles at any moment. Weights go
 // straight to registers as the A operand (nothing is read twice, so LDS would
-// only add a copy); the tokens are the B operand, 16 per row tile. The W
-// partial sums meet in LDS, and the wavefronts share the epilogue. INT8 sums
-// are exact; FP8 sums are added in wavefront order.
+// only add a copy), through a ring of U pairs: a pair's registers are loaded
+// again as soon as its products are issued, so U - 1 pairs per panel stay in
+// flight. The tokens are the B operand, 16 per row tile. The W partial sums
+// meet in LDS, and the wavefronts share the epilogue. INT8 sums are exact; FP8
+// sums are added in wavefront order.
 //
 // Up to four tokens the kernel codes the rows itself (kSrc 1: bf16 tokens, 2:
-// fp32 hidden rows): every block does it over again, which costs less than a
-// launch of its own, and the weights' first loads are in flight meanwhile.
+// the feed-forward's hidden rows, from its gate and up values): every block
+// does it over again, which costs less than a launch of its own, and the
+// weights' first loads are in flight meanwhile.
+//
+// The gate and up projections run here as one plain product into fp32 rows;
+// whoever codes the hidden rows applies SwiGLU. (Pairing gate and up panels in
+// a block would halve the blocks of a launch that has too few of them.)
 #include "epilogue_device.h"
 
 namespace moe {
@@ -33,46 +40,36 @@ struct StreamArgs {
 template <bool kF8> struct Acc16v { typedef v4i T; };
 template <> struct Acc16v<true> { typedef v4f T; };
 
-template <int RT, int NPW, int W, int U, bool kF8, bool kGated, int kSrc>
+template <int RT, int NPW, int W, int U, bool kF8, int kSrc>
 __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs a) {
   typedef typename Acc16v<kF8>::T Acc;
-  static_assert(!kGated || NPW % 2 == 0, "gate and up panels come in pairs");
   static_assert(kSrc == kCodes || RT == 1, "rows coded by the block");
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int pairs = a.Kp >> 7;
 
-  // Panel of slot i. Gated: slots 0..NPW/2-1 are gate panels, the rest the
-  // matching up panels (runs of two panels alternate in the packed order).
-  auto panel = [&](int i) {
-    if (kGated) {
-      const int unit = blockIdx.x * (NPW / 2) + i % (NPW / 2);
-      return unit / 2 * 4 + (i < NPW / 2 ? 0 : 2) + unit % 2;
-    }
-    return (int)blockIdx.x * NPW + i;
-  };
   const int8_t *wp[NPW];
 #pragma unroll
   for (int i = 0; i < NPW; ++i) {
-    int p = panel(i);
+    int p = (int)blockIdx.x * NPW + i;
     p = p < (a.Np >> 4) ? p : (a.Np >> 4) - 1;  // read, never stored
     wp[i] = a.w + frag_tile(p, 0, a.Kp) + lane * 16;
   }
-  v4i af[U][NPW][2];
-  auto load_w = [&](int b) {
+  // This wavefront's pairs wave, wave + W, ...: n of them, pair s in ring slot
+  // s % U.
+  const int n = wave < pairs ? (pairs - wave + W - 1) / W : 0;
+  v4i af[U][NPW][2], bf[U][RT][2];
+  auto load_w = [&](int u, int s) {
+    const size_t at = (size_t)(wave + s * W) << 11;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int p = wave + (b * U + u) * W;
-      if (p < pairs) {
+    for (int i = 0; i < NPW; ++i)
 #pragma unroll
-        for (int i = 0; i < NPW; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            af[u][i][h] = __builtin_nontemporal_load(
-                reinterpret_cast<const v4i *>(wp[i] + ((size_t)(2 * p + h) << 10)));
-      }
-    }
+      for (int h = 0; h < 2; ++h)
+        af[u][i][h] =
+            __builtin_nontemporal_load(reinterpret_cast<const v4i *>(wp[i] + at + h * 1024));
   };
-  load_w(0);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u < n) load_w(u, u);
 
   extern __shared__ __attribute__((aligned(16))) int8_t codes[];  // kSrc != kCodes: [T][Kp + 16]
   __shared__ float rscale[kFusedRows];
@@ -93,7 +90,7 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs 
           for (int j = 0; j < 8; ++j) o[j] *= f[j];
         }
       } else {
-        load8(a.in.h + t * a.in.ld + c, rem, o);
+        hidden8(a.in.h + t * a.in.ld, c, rem, o);
       }
     };
 #pragma unroll
@@ -151,41 +148,56 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs 
     if constexpr (kSrc == kCodes) bp[rt] = a.in.q + (size_t)r * a.Kp + (lane >> 4) * 16;
     else bp[rt] = codes + r * (a.Kp + 16) + (lane >> 4) * 16;
   }
+  auto load_x = [&](int u, int s) {
+    const size_t at = (size_t)(wave + s * W) * 128;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        bf[u][rt][h] = *reinterpret_cast<const v4i *>(bp[rt] + at + h * 64);
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u < n) load_x(u, u);
   Acc acc[NPW][RT];
 #pragma unroll
   for (int i = 0; i < NPW; ++i)
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) acc[i][rt] = Acc{0, 0, 0, 0};
-  for (int b = 0; wave + b * U * W < pairs; ++b) {
-    if (b > 0) load_w(b);
-    v4i bf[U][RT][2];
+  auto multiply = [&](int u) {
+#pragma unroll
+    for (int i = 0; i < NPW; ++i)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        if constexpr (kF8) {
+          acc[i][rt] = mfma16f8(af[u][i][0], af[u][i][1], bf[u][rt][0], bf[u][rt][1], acc[i][rt]);
+        } else {
+          acc[i][rt] = mfma16(af[u][i][0], bf[u][rt][0], acc[i][rt]);
+          acc[i][rt] = mfma16(af[u][i][1], bf[u][rt][1], acc[i][rt]);
+        }
+      }
+  };
+  int s = 0;
+  for (; s + 2 * U <= n; s += U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int p = wave + (b * U + u) * W;
-      if (p < pairs) {
+      multiply(u);
+      load_w(u, s + U + u);
+      load_x(u, s + U + u);
+    }
+  }
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            bf[u][rt][h] = *reinterpret_cast<const v4i *>(bp[rt] + (size_t)p * 128 + h * 64);
+  for (int u = 0; u < U; ++u)
+    if (s + u < n) {
+      multiply(u);
+      if (s + U + u < n) {
+        load_w(u, s + U + u);
+        load_x(u, s + U + u);
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (wave + (b * U + u) * W >= pairs) break;
-#pragma unroll
-      for (int i = 0; i < NPW; ++i)
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          if constexpr (kF8) {
-            acc[i][rt] = mfma16f8(af[u][i][0], af[u][i][1], bf[u][rt][0], bf[u][rt][1], acc[i][rt]);
-          } else {
-            acc[i][rt] = mfma16(af[u][i][0], bf[u][rt][0], acc[i][rt]);
-            acc[i][rt] = mfma16(af[u][i][1], bf[u][rt][1], acc[i][rt]);
-          }
-        }
-    }
-  }
+  for (int u = 0; u < U; ++u)
+    if (s + U + u < n) multiply(u);
 
   __shared__ Acc red[W][NPW * RT][64];
 #pragma unroll
@@ -200,81 +212,70 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs 
     return s;
   };
   const Epilogue &ep = a.ep;
-  constexpr int kUnits = kGated ? NPW / 2 : NPW;
   const int ch0 = (lane >> 4) * 4;
-  for (int c = wave; c < kUnits * RT; c += W) {
-    const int i = c / RT, rt = c % RT;
-    const int r = rt * 16 + (lane & 15);
-    const int p = panel(i);
-    const bool valid = r < a.T && p < (a.Np >> 4);
-    const float rs = !valid ? 0.0f : kSrc == kCodes ? ep.row_scale[r] : rscale[r];
-    if constexpr (kGated) {
-      const Acc g = total(i * RT + rt), u = total((i + kUnits) * RT + rt);
-      const int f0 = (p >> 2) * 32 + (p & 1) * 16 + ch0;
-      uint32_t m = 0;
-      if (valid) {
-        const v4f sg = *reinterpret_cast<const v4f_a4 *>(ep.scale + p * 16 + ch0);
-        const v4f su = *reinterpret_cast<const v4f_a4 *>(ep.scale + (p + 2) * 16 + ch0);
-        v4f h;
+  for (int c = wave; c < NPW * RT; c += W) {
+    const int r = c % RT * 16 + (lane & 15);
+    const int p = (int)blockIdx.x * NPW + c / RT;
+    const Acc sum = total(c);
+    if (r < a.T && p < (a.Np >> 4)) {
+      const float rs = kSrc == kCodes ? ep.row_scale[r] : rscale[r];
+      const v4f sc = *reinterpret_cast<const v4f_a4 *>(ep.scale + p * 16 + ch0);
+      float v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          h[j] = swiglu((float)g[j] * rs * sg[j], (float)u[j] * rs * su[j]);
-          m = umax(m, f0 + j < ep.N ? abs_bits(h[j]) : 0u);
-        }
-        // h rows have the pitch of code rows: the padding columns are there
-        *reinterpret_cast<v4f *>(static_cast<float *>(ep.out) + (int64_t)r * ep.ld_out + f0) = h;
-      }
-      if (ep.amax) {
-        m = umax(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-        m = umax(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-        if (valid && lane < 16) atomicMax(ep.amax + r, m);
-      }
-    } else {
-      const Acc s = total(c);
-      if (valid) {
-        const v4f sc = *reinterpret_cast<const v4f_a4 *>(ep.scale + p * 16 + ch0);
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = (float)s[j] * rs * sc[j];
-        finish_columns<4>(ep, r, p * 16 + ch0, v);
-      }
+      for (int j = 0; j < 4; ++j) v[j] = (float)sum[j] * rs * sc[j];
+      finish_columns<4>(ep, r, p * 16 + ch0, v);
     }
   }
 }
 
-template <int RT, int NPW, int W, int U, bool kGated, int kSrc>
+template <int RT, int NPW, int W, int U, int kSrc>
 hipError_t run(const StreamArgs &a, bool fp8, hipStream_t st) {
-  const int per = kGated ? NPW / 2 : NPW;
-  const int units = kGated ? a.Np / 32 : a.Np / 16;
-  const dim3 grid((unsigned)((units + per - 1) / per));
+  const dim3 grid((unsigned)((a.Np / 16 + NPW - 1) / NPW));
   const size_t lds = kSrc == kCodes ? 0 : (size_t)a.T * (a.Kp + 16);
   (void)hipGetLastError();
   if (fp8)
-    hipLaunchKernelGGL((linear_stream_kernel<RT, NPW, W, U, true, kGated, kSrc>), grid,
+    hipLaunchKernelGGL((linear_stream_kernel<RT, NPW, W, U, true, kSrc>), grid,
                        dim3(64 * W), lds, st, a);
   else
-    hipLaunchKernelGGL((linear_stream_kernel<RT, NPW, W, U, false, kGated, kSrc>), grid,
+    hipLaunchKernelGGL((linear_stream_kernel<RT, NPW, W, U, false, kSrc>), grid,
                        dim3(64 * W), lds, st, a);
   return hipGetLastError();
 }
 
-template <bool kGated>
+// Panels a block owns: one while a launch has at most a block per compute unit
+// then, more where that leaves enough blocks, so that the tokens are read a
+// half or a quarter as often. Measured on MI355X (codes, INT8, K 4096; us with
+// 1, 2 and 4 panels a block):
+//   4096 outputs:  16 tokens 5.7, 6.7, 9.1   64 tokens 11.7, 12.6, 16.6
+//   8192 outputs:  16 tokens 9.9, 8.3, 10.5  64 tokens 21.9, 14.0, 17.2
+//   16384 outputs: 16 tokens 14.9, 12.7, 12.9  64 tokens 41.4, 25.9, 19.7
+//   32003 outputs: 32 tokens 42.9, 30.5, 25.3 (131 MB of weights: 5.2 TB/s)
+template <int RT, int kSrc>
 hipError_t pick(const StreamArgs &a, bool fp8, hipStream_t st) {
-  constexpr int P = kGated ? 2 : 1;
-  if (a.in.x) return run<1, P, 8, 4, kGated, kTokens>(a, fp8, st);
-  if (a.in.h) return run<1, P, 8, 4, kGated, kHidden>(a, fp8, st);
-  if (a.T <= 16) return run<1, P, 8, 4, kGated, kCodes>(a, fp8, st);
-  if (a.T <= 32) return run<2, 2, 8, 2, kGated, kCodes>(a, fp8, st);
-  return run<4, 2, 8, 2, kGated, kCodes>(a, fp8, st);
+  const int panels = a.Np / 16;
+  if (panels <= 256) {
+    // Rows coded by the block: more wavefronts share that work (one token,
+    // 4096 outputs, K 4096: 5.6 with 16 wavefronts, 6.1 with 8).
+    if constexpr (kSrc != kCodes)
+      if (a.Kp >= 4096) return run<RT, 1, 16, 2, kSrc>(a, fp8, st);
+    return run<RT, 1, 8, 2, kSrc>(a, fp8, st);
+  }
+  if constexpr (kSrc == kCodes && RT == 1) return run<RT, 2, 8, 2, kSrc>(a, fp8, st);
+  if (panels < 1024) return run<RT, 2, 8, 2, kSrc>(a, fp8, st);
+  return run<RT, 4, 4, 2, kSrc>(a, fp8, st);
 }
 
 }  // namespace
 
-hipError_t launch_linear_stream(const StreamIn &in, int T, const int8_t *w, int K, int Np,
-                                bool gated, bool fp8, const Epilogue &ep, hipStream_t st) {
+hipError_t launch_linear_stream(const StreamIn &in, int T, const int8_t *w, int K, int Np, bool fp8,
+                                const Epilogue &ep, hipStream_t st) {
   StreamArgs a{};
   a.in = in; a.T = T; a.K = K; a.Kp = row_pitch(K); a.w = w; a.Np = Np; a.ep = ep;
-  return gated ? pick<true>(a, fp8, st) : pick<false>(a, fp8, st);
+  if (in.x) return pick<1, kTokens>(a, fp8, st);
+  if (in.h) return pick<1, kHidden>(a, fp8, st);
+  if (T <= 16) return pick<1, kCodes>(a, fp8, st);
+  if (T <= 32) return pick<2, kCodes>(a, fp8, st);
+  return pick<4, kCodes>(a, fp8, st);
 }
 
 }  // namespace moe

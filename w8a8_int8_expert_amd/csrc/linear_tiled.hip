@@ -3,13 +3,17 @@
 //
 // "MiniMax-M3 W8A8 inference on K100AI" (mhpq.cn/news/1068415) §1.2, §4.3.
 //
-// A block computes BM tokens x BN packed weight rows. Tokens are read row-major
-// through a ring of two 128-k stages (whole 128-byte lines, XOR-swizzled in
-// LDS so that an operand read is free of bank conflicts), weights through a
-// ring of four 64-k stages of fragment tiles, both by direct global -> LDS
-// loads issued up to three steps ahead. WM x WN wavefronts own MI x NJ
-// accumulators of 32 x 32 each. INT8 multiplies on the 32x32x32 instruction
-// (the 16x16x64 form reaches half its rate), FP8 on 32x32x64.
+// A block computes BM tokens x BN packed weight rows, K in stages of 128. Both
+// operands reach LDS by direct global -> LDS loads: tokens row-major (whole
+// 128-byte lines, XOR-swizzled so that an operand read is free of bank
+// conflicts) through a ring of SA stages, weights as fragment tiles through a
+// ring of SB stages. WM x WN wavefronts own MI x NJ accumulators of 32 x 32.
+// INT8 multiplies on the 32x32x32 instruction (the 16x16x64 form reaches half
+// its rate), FP8 on 32x32x64.
+//
+// What a compute unit gets is the bytes it has in flight over the latency of
+// its slowest line, so the rings fill LDS: the smaller the tile, the more
+// stages ahead.
 //
 // Tiles are numbered (N group, M tile, N tile in group), and each XCD takes a
 // contiguous eighth of that order, so that the blocks that run together on one
@@ -42,20 +46,33 @@ __device__ __forceinline__ void tile_of(const TiledLinear &a, int64_t L, int *m,
   *n = grp * a.gn + (r - *m * g);
 }
 
-template <int WM, int WN, int MI, int NJ, bool kF8, bool kGated, bool kSplit>
+// At most n stages of L loads each stay in flight (n <= M).
+template <int M, int L>
+__device__ __forceinline__ void wait_stages(int n) {
+  if constexpr (M > 0) {
+    if (n < M) {
+      wait_stages<M - 1, L>(n);
+      return;
+    }
+  }
+  wait_barrier<M * L>();
+}
+
+template <int WM, int WN, int MI, int NJ, int SA, int SB, bool kF8, bool kGated, bool kSplit>
 __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const TiledLinear a) {
   typedef typename Acc32<kF8>::T Acc;
   constexpr int W = WM * WN, BM = WM * MI * 32, BN = WN * NJ * 32;
-  constexpr int kA2 = BM * 128, kB = BN * 64;         // one stage of each ring
-  constexpr int kALoads = BM / 8 / W, kBLoads = BN / 16 / W;
-  static_assert(kALoads * W * 8 == BM && kBLoads * W * 16 == BN, "load split");
-  constexpr int kRing = 2 * kA2 + 4 * kB;
+  constexpr int kA = BM * 128, kB = BN * 128;  // one stage of each ring
+  constexpr int kALoads = BM / 8 / W, kBLoads = BN / 8 / W;
+  static_assert(kALoads * W * 8 == BM && kBLoads * W * 8 == BN, "load split");
+  static_assert(SA >= 2 && (SB == SA || (SA == 2 && SB == 3)), "wait cases");
+  constexpr int kRing = SA * kA + SB * kB;
   // Epilogue: 16 rows x the wavefront's columns per pass, pitch padded by 8
   // words so that the two 32-lane halves (rows r and r + 4) use other banks.
   constexpr int kPitch = NJ * 32 + 8, kSlice = 16 * kPitch * 4;
   constexpr int kScaleAt = W * kSlice;
-  constexpr int kLds = kRing > kScaleAt + BM * 4 ? kRing : kScaleAt + BM * 4;
-  __shared__ __attribute__((aligned(1024))) int8_t lds[kLds];
+  static_assert(kScaleAt + BM * 4 <= kRing, "epilogue staging");
+  __shared__ __attribute__((aligned(1024))) int8_t lds[kRing];
 
   const int64_t tiles = (int64_t)a.mt * a.nt, chunk = (tiles + 7) >> 3;
   const int64_t L = (int64_t)(blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
@@ -67,15 +84,15 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const Til
   const int rows = a.T - m0 < BM ? (int)(a.T - m0) : BM;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / WN, wn = wave % WN;
-  // This block's 128-k stages [d0, d1).
-  const int D = a.Kp >> 7;
-  int d0 = 0, d1 = D;
+  // This block's stages of K: [d0, d0 + D).
+  int d0 = 0, D = a.Kp >> 7;
   if (kSplit) {
-    d0 = (int)((int64_t)D * blockIdx.y / a.split);
-    d1 = (int)((int64_t)D * (blockIdx.y + 1) / a.split);
+    d0 = (int)((int64_t)(a.Kp >> 7) * blockIdx.y / a.split);
+    D = (int)((int64_t)(a.Kp >> 7) * (blockIdx.y + 1) / a.split) - d0;
   }
-  const int KT = 2 * (d1 - d0);
 
+  // Instruction i of a token stage fills rows 8i .. 8i+7: lane l brings chunk
+  // (l%8) ^ (row/2 % 8) of row 8i + l/8 to slot l%8.
   const int8_t *asrc[kALoads];
 #pragma unroll
   for (int t = 0; t < kALoads; ++t) {
@@ -85,25 +102,27 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const Til
     asrc[t] = a.q + (m0 + r) * a.Kp + (size_t)d0 * 128 +
               (((lane & 7) ^ ((4 * (i & 1) + (lane >> 4)) & 7)) << 4);
   }
+  // Instruction j of a weight stage brings 1 KB tile (j/2, j%2) of the stage.
   const int8_t *bsrc[kBLoads];
 #pragma unroll
   for (int t = 0; t < kBLoads; ++t) {
-    int p = (n0 >> 4) + kBLoads * wave + t;
+    const int j = kBLoads * wave + t;
+    int p = (n0 >> 4) + (j >> 1);
     p = p < (a.Np >> 4) ? p : (a.Np >> 4) - 1;  // columns past Np: never stored
-    bsrc[t] = a.w + frag_tile(p, 2 * d0, a.Kp) + lane * 16;
+    bsrc[t] = a.w + frag_tile(p, 2 * d0 + (j & 1), a.Kp) + lane * 16;
   }
-  auto issue_a = [&](int d) {
-    int8_t *st = lds + (d & 1) * kA2;
+  auto issue_a = [&](int d, int slot) {
+    int8_t *st = lds + slot * kA;
 #pragma unroll
     for (int t = 0; t < kALoads; ++t)
       dma16(asrc[t] + (size_t)d * 128,
             __builtin_amdgcn_readfirstlane(lds_addr(st + (kALoads * wave + t) * 1024)));
   };
-  auto issue_b = [&](int kt) {
-    int8_t *st = lds + 2 * kA2 + (kt & 3) * kB;
+  auto issue_b = [&](int d, int slot) {
+    int8_t *st = lds + SA * kA + slot * kB;
 #pragma unroll
     for (int t = 0; t < kBLoads; ++t)
-      dma16(bsrc[t] + ((size_t)kt << 10),
+      dma16(bsrc[t] + (size_t)d * 2048,
             __builtin_amdgcn_readfirstlane(lds_addr(st + (kBLoads * wave + t) * 1024)));
   };
 
@@ -115,78 +134,111 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const Til
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][c][v] = 0;
 
-  const int frag = (((lane >> 5) * 16) + (lane & 15)) * 16 + ((lane & 31) >> 4) * 1024;
-  const int boff = wn * NJ * 2048 + frag;
-  int arow[MI], axor[2][2];
+  // 16-row weight tile p of the stage starts at 2048 p, its k half at + 1024.
+  const int boff = wn * NJ * 4096 + (((lane >> 5) * 16) + (lane & 15)) * 16 +
+                   ((lane & 31) >> 4) * 2048;
+  const int aoff = (wm * MI * 32 + (lane & 31)) * 128;
+  int axor[4];  // chunk 2 k + lane/32 of the lane's row, k the 32-k quarter
 #pragma unroll
-  for (int i = 0; i < MI; ++i) arow[i] = ((wm * MI + i) * 32 + (lane & 31)) * 128;
-#pragma unroll
-  for (int par = 0; par < 2; ++par)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      axor[par][h] = ((4 * par + 2 * h + (lane >> 5)) ^ ((lane >> 1) & 7)) << 4;
-  const bool skip = wm * MI * 32 >= rows;  // no row of this wavefront exists
+  for (int k = 0; k < 4; ++k) axor[k] = ((2 * k + (lane >> 5)) ^ ((lane >> 1) & 7)) << 4;
 
-  auto step = [&](const int8_t *as, int par, const int8_t *bst) {
-    v4i af[MI][2];
+  // A stage is kSteps steps of matrix work: 32 k each for INT8, 64 for FP8.
+  // The operands of a step are read while the step before it multiplies, and
+  // the first ones of a stage while the last step of the stage before does, so
+  // that neither the reads nor the barrier between two stages leave the matrix
+  // cores idle.
+  constexpr int kSteps = kF8 ? 2 : 4, kH = kF8 ? 2 : 1;
+  v4i af[2][MI][kH], bf[2][NJ][kH];
+  auto read = [&](int buf, int s, const int8_t *as, const int8_t *bs) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+    for (int h = 0; h < kH; ++h) {
+      const int k = s * kH + h;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        af[i][h] = *reinterpret_cast<const v4i *>(as + arow[i] + axor[par][h]);
-    v4i b0 = *reinterpret_cast<const v4i *>(bst + boff);
-    v4i b1 = *reinterpret_cast<const v4i *>(bst + boff + 512);
+      for (int i = 0; i < MI; ++i)
+        af[buf][i][h] = *reinterpret_cast<const v4i *>(as + aoff + i * 4096 + axor[k]);
 #pragma unroll
-    for (int c = 0; c < NJ; ++c) {
-      v4i n0v = b0, n1v = b1;
-      if (c + 1 < NJ) {
-        n0v = *reinterpret_cast<const v4i *>(bst + boff + (c + 1) * 2048);
-        n1v = *reinterpret_cast<const v4i *>(bst + boff + (c + 1) * 2048 + 512);
-      }
-      if constexpr (kF8) {
-#pragma unroll
-        for (int i = 0; i < MI; ++i) acc[i][c] = mfma32f8(af[i][0], af[i][1], b0, b1, acc[i][c]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < MI; ++i) acc[i][c] = mfma32(af[i][0], b0, acc[i][c]);
-#pragma unroll
-        for (int i = 0; i < MI; ++i) acc[i][c] = mfma32(af[i][1], b1, acc[i][c]);
-      }
-      b0 = n0v;
-      b1 = n1v;
+      for (int c = 0; c < NJ; ++c)
+        bf[buf][c][h] = *reinterpret_cast<const v4i *>(bs + boff + c * 4096 + (k >> 1) * 1024 +
+                                                       (k & 1) * 512);
     }
-    // The A operands and two column fragments first, then each fragment's
-    // instructions followed by the reads of the fragment two ahead.
-    constexpr int kM = kF8 ? MI : 2 * MI;
-    if constexpr (NJ >= 2) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 2 * MI + 4, 0);
+  };
+  auto multiply = [&](int buf) {
 #pragma unroll
-      for (int c = 0; c < NJ - 2; ++c) {
-        __builtin_amdgcn_sched_group_barrier(0x008, kM, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    for (int c = 0; c < NJ; ++c)
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        if constexpr (kF8)
+          acc[i][c] = mfma32f8(af[buf][i][0], af[buf][i][1], bf[buf][c][0], bf[buf][c][1],
+                               acc[i][c]);
+        else
+          acc[i][c] = mfma32(af[buf][i][0], bf[buf][c][0], acc[i][c]);
       }
-      __builtin_amdgcn_sched_group_barrier(0x008, 2 * kM, 0);
+  };
+  // Each of the step's reads goes between its matrix instructions.
+  auto interleave = [&]() {
+    constexpr int kReads = (MI + NJ) * kH, kM = MI * NJ;
+    constexpr int kPer = kM > kReads ? kM / kReads : 1;
+#pragma unroll
+    for (int i = 0; i < kReads; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
     }
   };
 
-  // Issue order: B(0), A(0), B(1), B(2); then at step kt, after the wait,
-  // A(kt/2 + 1) on even kt and B(kt + 3). At step kt, B(kt) and A(kt/2) must
-  // have landed: what may still be in flight is B(kt+1), B(kt+2) and, on odd
-  // kt, A((kt+1)/2). KT is even; the last three steps drain all.
-  issue_b(0);
-  issue_a(0);
-  issue_b(1);
-  if (KT > 2) issue_b(2);
-  for (int kt = 0; kt < KT; ++kt) {
-    if (kt + 3 < KT) {
-      if (kt & 1) wait_barrier<2 * kBLoads + kALoads>();
-      else wait_barrier<2 * kBLoads>();
-    } else {
-      wait_barrier<0>();
+  // Stages 0 .. SA-1 of A and 0 .. SB-1 of B are issued first; at the end of
+  // stage d, once every wavefront has read the last of it, A(d + SA) and
+  // B(d + SB) go to its slots. Loads return in order, so what may still be in
+  // flight when stage d+1 begins is what was issued after A(d+1) and B(d+1):
+  // stages d+2 .. d+SA-1 of both where SA = SB; B(d+2) alone where SA = 2 and
+  // SB = 3.
+#pragma unroll
+  for (int d = 0; d < SA; ++d)
+    if (d < D) {
+      issue_a(d, d);
+      issue_b(d, d);
     }
-    if (!(kt & 1) && kt + 2 < KT) issue_a((kt >> 1) + 1);
-    if (kt + 3 < KT) issue_b(kt + 3);
-    if (!skip) step(lds + ((kt >> 1) & 1) * kA2, kt & 1, lds + 2 * kA2 + (kt & 3) * kB);
+  if constexpr (SB > SA) {
+    if (SA < D) issue_b(SA, SA);
+  }
+  if constexpr (SA == SB) {
+    wait_stages<SA - 1, kALoads + kBLoads>(D - 1);
+  } else {
+    if (D > 2) wait_barrier<kALoads + 2 * kBLoads>();
+    else wait_stages<1, kALoads + kBLoads>(D - 1);
+  }
+  const bool skip = wm * MI * 32 >= rows;  // no row of this wavefront exists
+  int sa = 0, sb = 0;                      // slots of stage d
+  auto next_stage = [&](int d) {           // after stage d's last read
+    const int left = D - 2 - d;            // stages behind d+1
+    if constexpr (SA == SB) wait_stages<SA - 2, kALoads + kBLoads>(left);
+    else wait_stages<1, kBLoads>(left);
+    if (d + SA < D) issue_a(d + SA, sa);
+    if (d + SB < D) issue_b(d + SB, sb);
+    sa = sa + 1 == SA ? 0 : sa + 1;
+    sb = sb + 1 == SB ? 0 : sb + 1;
+  };
+  if (skip) {
+    for (int d = 0; d + 1 < D; ++d) next_stage(d);
+  } else {
+    read(0, 0, lds, lds + SA * kA);
+    auto steps = [&]() {  // all but the last step of the stage in slots sa, sb
+      const int8_t *as = lds + sa * kA, *bs = lds + SA * kA + sb * kB;
+#pragma unroll
+      for (int s = 0; s + 1 < kSteps; ++s) {
+        read((s + 1) & 1, s + 1, as, bs);
+        multiply(s & 1);
+        interleave();
+      }
+    };
+    for (int d = 0; d + 1 < D; ++d) {
+      steps();
+      next_stage(d);
+      read(0, 0, lds + sa * kA, lds + SA * kA + sb * kB);
+      multiply((kSteps - 1) & 1);
+      interleave();
+    }
+    steps();
+    multiply((kSteps - 1) & 1);
   }
   wait_barrier<0>();  // every wavefront is done with the rings
 
@@ -342,50 +394,65 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const TiledLinear a) {
   }
 }
 
-template <int WM, int WN, int MI, int NJ, bool kGated>
+template <int WM, int WN, int MI, int NJ, int SA, int SB, bool kGated, bool kSplit>
 hipError_t run(TiledLinear a, bool fp8, hipStream_t st) {
   constexpr int BM = WM * MI * 32, BN = WN * NJ * 32;
   a.mt = (int)((a.T + BM - 1) / BM);
   a.nt = (a.Np + BN - 1) / BN;
-  a.gn = a.nt < 4 ? a.nt : 4;
   const int64_t tiles = (int64_t)a.mt * a.nt;
+  // N tiles per group: an XCD's share of a single round is then mt x gn (few
+  // M tiles) or 8 x 4 tiles.
+  const int64_t share = ((tiles < 256 ? tiles : 256) + 7) / 8;
+  a.gn = (int)(a.mt >= 8 ? 4 : (share + a.mt - 1) / a.mt);
+  if (a.gn > a.nt) a.gn = a.nt;
   const dim3 grid((unsigned)((tiles + 7) / 8 * 8), (unsigned)a.split);
   const dim3 block(64 * WM * WN);
   const Timing tm{};
-  if (a.split > 1) {
-    const hipError_t e =
-        fp8 ? launch_kernel(linear_tiled_kernel<WM, WN, MI, NJ, true, kGated, true>, grid, block,
-                            st, tm, a)
-            : launch_kernel(linear_tiled_kernel<WM, WN, MI, NJ, false, kGated, true>, grid, block,
-                            st, tm, a);
-    if (e != hipSuccess) return e;
-    const int64_t n = a.T * (kGated ? a.Np / 16 : a.Np / 8);
-    const dim3 jgrid((unsigned)((n + 255) / 256));
-    if (fp8)
-      return launch_kernel(linear_join_kernel<true, kGated>, jgrid, dim3(256), st, tm, a);
-    return launch_kernel(linear_join_kernel<false, kGated>, jgrid, dim3(256), st, tm, a);
-  }
   if (fp8)
-    return launch_kernel(linear_tiled_kernel<WM, WN, MI, NJ, true, kGated, false>, grid, block, st,
-                         tm, a);
-  return launch_kernel(linear_tiled_kernel<WM, WN, MI, NJ, false, kGated, false>, grid, block, st,
-                       tm, a);
+    return launch_kernel(linear_tiled_kernel<WM, WN, MI, NJ, SA, SB, true, kGated, kSplit>, grid,
+                         block, st, tm, a);
+  return launch_kernel(linear_tiled_kernel<WM, WN, MI, NJ, SA, SB, false, kGated, kSplit>, grid,
+                       block, st, tm, a);
+}
+
+template <bool kGated>
+hipError_t join(const TiledLinear &a, bool fp8, hipStream_t st) {
+  const int64_t n = a.T * (kGated ? a.Np / 16 : a.Np / 8);
+  const dim3 grid((unsigned)((n + 255) / 256));
+  if (fp8)
+    return launch_kernel(linear_join_kernel<true, kGated>, grid, dim3(256), st, Timing{}, a);
+  return launch_kernel(linear_join_kernel<false, kGated>, grid, dim3(256), st, Timing{}, a);
+}
+
+// Tile shapes: every one as the wavefronts' arrangement and the depth of its
+// rings.
+template <bool kGated, bool kSplit>
+hipError_t run_shape(int shape, const TiledLinear &a, bool fp8, hipStream_t st) {
+  switch (shape) {
+    case 0: return run<4, 2, 2, 4, 2, 3, kGated, kSplit>(a, fp8, st);  // 256 x 256
+    case 1: return run<4, 2, 2, 2, 3, 3, kGated, kSplit>(a, fp8, st);  // 256 x 128
+    case 2: return run<2, 2, 3, 2, 4, 4, kGated, kSplit>(a, fp8, st);  // 192 x 128
+    case 3: return run<2, 2, 2, 2, 5, 5, kGated, kSplit>(a, fp8, st);  // 128 x 128
+    case 4: return run<2, 2, 1, 2, 6, 6, kGated, kSplit>(a, fp8, st);  // 64 x 128
+    case 5: return run<2, 4, 2, 2, 3, 3, kGated, kSplit>(a, fp8, st);  // 128 x 256
+    case 6: return run<4, 2, 1, 2, 5, 5, kGated, kSplit>(a, fp8, st);  // 128 x 128, 8 waves
+    case 7: return run<2, 2, 4, 4, 2, 3, kGated, kSplit>(a, fp8, st);  // 256 x 256, 4 waves
+    default: return run<4, 2, 2, 6, 2, 2, kGated, kSplit>(a, fp8, st); // 256 x 384
+  }
 }
 
 template <bool kGated>
 hipError_t pick(TiledLinear a, bool fp8, hipStream_t st) {
-  const int64_t t256 = ((a.T + 255) / 256) * ((a.Np + 255) / 256);
+  int shape;
   a.split = 1;
-  if (t256 >= 192) return run<4, 2, 2, 4, kGated>(a, fp8, st);  // 256 x 256
+  const int64_t t256 = ((a.T + 255) / 256) * ((a.Np + 255) / 256);
   const int64_t t128 = ((a.T + 127) / 128) * ((a.Np + 127) / 128);
-  if (t128 >= 128) return run<2, 2, 2, 2, kGated>(a, fp8, st);  // 128 x 128
-  // 64 x 128, K split until the chip is covered
-  const int64_t t64 = ((a.T + 63) / 64) * ((a.Np + 127) / 128);
-  const int D = a.Kp / 128;
-  while (a.split < 8 && t64 * a.split < 256 && D / (a.split + 1) >= 4 &&
-         (size_t)(a.split + 1) * a.T * a.Np * 4 <= kPartialBytes)
-    ++a.split;
-  return run<2, 2, 1, 2, kGated>(a, fp8, st);
+  shape = t256 >= 192 ? 0 : t128 >= 128 ? 3 : 4;
+  if (a.split > 1) {
+    const hipError_t e = run_shape<kGated, true>(shape, a, fp8, st);
+    return e == hipSuccess ? join<kGated>(a, fp8, st) : e;
+  }
+  return run_shape<kGated, false>(shape, a, fp8, st);
 }
 
 }  // namespace

@@ -3,6 +3,7 @@
 // per-token code rule of the block operators. Included by the HIP sources only.
 #pragma once
 
+#include "lds_dma.h"
 #include "block_internal.h"
 
 namespace moe {
@@ -113,6 +114,18 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
 }
 __device__ __forceinline__ uint32_t wave_max_bits(uint32_t m) {
   return __float_as_uint(wave_max(__uint_as_float(m)));
+}
+
+// Hidden values h = silu(g) u of columns c .. c+7 (c a multiple of 8, `rem` of
+// them exist) from a row of gate and up values in packed order: alternating
+// runs of 32.
+__device__ __forceinline__ void hidden8(const float *gu, int c, int rem, float *o) {
+  float u[8];
+  const float *p = gu + c / 32 * 64 + c % 32;
+  load8(p, rem, o);
+  load8(p + 32, rem, u);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = swiglu(o[j], u[j]);
 }
 
 }  // namespace moe
