@@ -8,22 +8,12 @@
 
 namespace moe {
 
-// n consecutive columns (n0.., VN of them at most, those below ep.N exist) of
-// row t: v holds the dequantised sums.
+// Columns n0 .. n0+VN-1 of row t (those below ep.N exist), gated values in v:
+// add, rounding, store.
 template <int VN>
-__device__ __forceinline__ void finish_columns(const Epilogue &ep, int64_t t, int n0, float *v) {
+__device__ __forceinline__ void store_columns(const Epilogue &ep, int64_t t, int n0, float *v) {
   const int rem = ep.N - n0;
   if (rem <= 0) return;
-  if (ep.bias) {
-#pragma unroll
-    for (int i = 0; i < VN; ++i)
-      if (i < rem) v[i] += ep.bias[n0 + i];
-  }
-  if (ep.gate) {
-    const float g = ep.gate[t];
-#pragma unroll
-    for (int i = 0; i < VN; ++i) v[i] *= g;
-  }
   if (ep.add) {
     const uint16_t *p = ep.add + t * ep.ld_add + n0;
     if constexpr (VN == 8) {
@@ -60,6 +50,22 @@ __device__ __forceinline__ void finish_columns(const Epilogue &ep, int64_t t, in
         if (i < rem) o[i] = f32_to_bf16(v[i]);
     }
   }
+}
+
+// The same from the dequantised sums: bias and gate first.
+template <int VN>
+__device__ __forceinline__ void finish_columns(const Epilogue &ep, int64_t t, int n0, float *v) {
+  if (ep.bias) {
+#pragma unroll
+    for (int i = 0; i < VN; ++i)
+      if (n0 + i < ep.N) v[i] += ep.bias[n0 + i];
+  }
+  if (ep.gate) {
+    const float g = ep.gate[t];
+#pragma unroll
+    for (int i = 0; i < VN; ++i) v[i] *= g;
+  }
+  store_columns<VN>(ep, t, n0, v);
 }
 
 }  // namespace moe

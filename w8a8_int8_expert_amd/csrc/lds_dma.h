@@ -24,6 +24,13 @@ __device__ __forceinline__ void dma16(const void *g, uint32_t lds_base) {
                : "v"(g), "s"(lds_base)
                : "memory", "m0");
 }
+// 4 bytes per lane into LDS at lds_base + 4*lane.
+__device__ __forceinline__ void dma4(const void *g, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+               :
+               : "v"(g), "s"(lds_base)
+               : "memory", "m0");
+}
 // Wait until at most N of this wavefront's loads are in flight and its LDS
 // accesses are done, then meet the other wavefronts of the block.
 template <int N>

@@ -6,14 +6,15 @@
 // A block computes BM tokens x BN packed weight rows, K in stages of 128. Both
 // operands reach LDS by direct global -> LDS loads: tokens row-major (whole
 // 128-byte lines, XOR-swizzled so that an operand read is free of bank
-// conflicts) through a ring of SA stages, weights as fragment tiles through a
-// ring of SB stages. WM x WN wavefronts own MI x NJ accumulators of 32 x 32.
-// INT8 multiplies on the 32x32x32 instruction (the 16x16x64 form reaches half
-// its rate), FP8 on 32x32x64.
+// conflicts), weights as fragment tiles, through rings of S stages. WM x WN
+// wavefronts own MI x NJ accumulators of 32 x 32. INT8 multiplies on the
+// 32x32x32 instruction (the 16x16x64 form reaches half its rate), FP8 on
+// 32x32x64.
 //
-// What a compute unit gets is the bytes it has in flight over the latency of
-// its slowest line, so the rings fill LDS: the smaller the tile, the more
-// stages ahead.
+// What bounds the small shapes is the operand feed: a compute unit gets about
+// 50 bytes per ns into LDS, whatever the depth of its rings or the number of its
+// wavefronts (rings of 2 to 6 stages, one to three blocks a unit). A larger tile
+// needs fewer bytes per product, a smaller one uses more compute units.
 //
 // Tiles are numbered (N group, M tile, N tile in group), and each XCD takes a
 // contiguous eighth of that order, so that the blocks that run together on one
@@ -58,21 +59,21 @@ __device__ __forceinline__ void wait_stages(int n) {
   wait_barrier<M * L>();
 }
 
-template <int WM, int WN, int MI, int NJ, int SA, int SB, bool kF8, bool kGated, bool kSplit>
+template <int WM, int WN, int MI, int NJ, int S, bool kF8, bool kGated, bool kSplit>
 __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const TiledLinear a) {
   typedef typename Acc32<kF8>::T Acc;
   constexpr int W = WM * WN, BM = WM * MI * 32, BN = WN * NJ * 32;
   constexpr int kA = BM * 128, kB = BN * 128;  // one stage of each ring
   constexpr int kALoads = BM / 8 / W, kBLoads = BN / 8 / W;
   static_assert(kALoads * W * 8 == BM && kBLoads * W * 8 == BN, "load split");
-  static_assert(SA >= 2 && (SB == SA || (SA == 2 && SB == 3)), "wait cases");
-  constexpr int kRing = SA * kA + SB * kB;
+  constexpr int kRing = S * (kA + kB);
   // Epilogue: 16 rows x the wavefront's columns per pass, pitch padded by 8
   // words so that the two 32-lane halves (rows r and r + 4) use other banks.
   constexpr int kPitch = NJ * 32 + 8, kSlice = 16 * kPitch * 4;
-  constexpr int kScaleAt = W * kSlice;
-  static_assert(kScaleAt + BM * 4 <= kRing, "epilogue staging");
+  static_assert(W * kSlice <= kRing, "epilogue staging");
   __shared__ __attribute__((aligned(1024))) int8_t lds[kRing];
+  __shared__ __attribute__((aligned(16))) float row_scale[BM], row_gate[BM], col_scale[BN],
+      col_bias[BN];
 
   const int64_t tiles = (int64_t)a.mt * a.nt, chunk = (tiles + 7) >> 3;
   const int64_t L = (int64_t)(blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
@@ -119,12 +120,35 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const Til
             __builtin_amdgcn_readfirstlane(lds_addr(st + (kALoads * wave + t) * 1024)));
   };
   auto issue_b = [&](int d, int slot) {
-    int8_t *st = lds + SA * kA + slot * kB;
+    int8_t *st = lds + S * kA + slot * kB;
 #pragma unroll
     for (int t = 0; t < kBLoads; ++t)
       dma16(bsrc[t] + (size_t)d * 2048,
             __builtin_amdgcn_readfirstlane(lds_addr(st + (kBLoads * wave + t) * 1024)));
   };
+
+  // What the epilogue needs of each row and column goes to LDS ahead of the
+  // operands: the K loop hides its latency, and it holds no registers. Rows and
+  // columns that do not exist repeat the last one.
+  const Epilogue &ep = a.ep;
+  const int nw = n0 + wn * NJ * 32;  // first packed row of this wavefront
+  const bool biased = !kGated && ep.bias, gated = !kGated && ep.gate;
+  if (!kSplit) {
+    auto fetch = [&](const float *src, int64_t at, int64_t last, float *dst) {
+      const int64_t i = at + lane;
+      dma4(src + (i < last ? i : last), __builtin_amdgcn_readfirstlane(lds_addr(dst)));
+    };
+    for (int i = wave; i < (BM + BN) / 64; i += W) {
+      const int r = i * 64, c = r - BM;
+      if (r < BM) {
+        fetch(ep.row_scale, m0 + r, a.T - 1, row_scale + r);
+        if (gated) fetch(ep.gate, m0 + r, a.T - 1, row_gate + r);
+      } else {
+        fetch(ep.scale, n0 + c, a.Np - 1, col_scale + c);
+        if (biased) fetch(ep.bias, n0 + c, ep.N - 1, col_bias + c);
+      }
+    }
+  }
 
   Acc acc[MI][NJ];
 #pragma unroll
@@ -185,44 +209,33 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const Til
     }
   };
 
-  // Stages 0 .. SA-1 of A and 0 .. SB-1 of B are issued first; at the end of
-  // stage d, once every wavefront has read the last of it, A(d + SA) and
-  // B(d + SB) go to its slots. Loads return in order, so what may still be in
-  // flight when stage d+1 begins is what was issued after A(d+1) and B(d+1):
-  // stages d+2 .. d+SA-1 of both where SA = SB; B(d+2) alone where SA = 2 and
-  // SB = 3.
+  // Stages 0 .. S-1 are issued first; at the end of stage d, once every
+  // wavefront has read the last of it, stage d + S goes to its slot. Loads
+  // return in order, so what may still be in flight when stage d+1 begins is
+  // what was issued after it: stages d+2 .. d+S-1.
 #pragma unroll
-  for (int d = 0; d < SA; ++d)
+  for (int d = 0; d < S; ++d)
     if (d < D) {
       issue_a(d, d);
       issue_b(d, d);
     }
-  if constexpr (SB > SA) {
-    if (SA < D) issue_b(SA, SA);
-  }
-  if constexpr (SA == SB) {
-    wait_stages<SA - 1, kALoads + kBLoads>(D - 1);
-  } else {
-    if (D > 2) wait_barrier<kALoads + 2 * kBLoads>();
-    else wait_stages<1, kALoads + kBLoads>(D - 1);
-  }
+  wait_stages<S - 1, kALoads + kBLoads>(D - 1);
   const bool skip = wm * MI * 32 >= rows;  // no row of this wavefront exists
-  int sa = 0, sb = 0;                      // slots of stage d
+  int slot = 0;                            // of stage d
   auto next_stage = [&](int d) {           // after stage d's last read
-    const int left = D - 2 - d;            // stages behind d+1
-    if constexpr (SA == SB) wait_stages<SA - 2, kALoads + kBLoads>(left);
-    else wait_stages<1, kBLoads>(left);
-    if (d + SA < D) issue_a(d + SA, sa);
-    if (d + SB < D) issue_b(d + SB, sb);
-    sa = sa + 1 == SA ? 0 : sa + 1;
-    sb = sb + 1 == SB ? 0 : sb + 1;
+    wait_stages<S - 2, kALoads + kBLoads>(D - 2 - d);
+    if (d + S < D) {
+      issue_a(d + S, slot);
+      issue_b(d + S, slot);
+    }
+    slot = slot + 1 == S ? 0 : slot + 1;
   };
   if (skip) {
     for (int d = 0; d + 1 < D; ++d) next_stage(d);
   } else {
-    read(0, 0, lds, lds + SA * kA);
-    auto steps = [&]() {  // all but the last step of the stage in slots sa, sb
-      const int8_t *as = lds + sa * kA, *bs = lds + SA * kA + sb * kB;
+    read(0, 0, lds, lds + S * kA);
+    auto steps = [&]() {  // all but the last step of the stage in `slot`
+      const int8_t *as = lds + slot * kA, *bs = lds + S * kA + slot * kB;
 #pragma unroll
       for (int s = 0; s + 1 < kSteps; ++s) {
         read((s + 1) & 1, s + 1, as, bs);
@@ -233,7 +246,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const Til
     for (int d = 0; d + 1 < D; ++d) {
       steps();
       next_stage(d);
-      read(0, 0, lds + sa * kA, lds + SA * kA + sb * kB);
+      read(0, 0, lds + slot * kA, lds + S * kA + slot * kB);
       multiply((kSteps - 1) & 1);
       interleave();
     }
@@ -245,21 +258,16 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const Til
   // Epilogue through the wavefront's own slice of the rings, 16 rows a pass.
   // Lane holds column lane%32 of each 32 x 32 accumulator and rows 8*(v/4) +
   // 4*(lane/32) + v%4.
-  const Epilogue &ep = a.ep;
-  float *rs = reinterpret_cast<float *>(lds + kScaleAt);
-  if (!kSplit) {
-    for (int i = threadIdx.x; i < BM; i += 64 * W) rs[i] = i < rows ? ep.row_scale[m0 + i] : 0.0f;
-    __syncthreads();
-  }
   if (skip) return;
   float *slice = reinterpret_cast<float *>(lds + wave * kSlice);
-  const int nw = n0 + wn * NJ * 32;  // first packed row of this wavefront
   const int rl = 4 * (lane >> 5);
-  float sc[NJ];
+  float sc[NJ], bs[NJ];
+  if (!kSplit) {
 #pragma unroll
-  for (int c = 0; c < NJ; ++c) {
-    const int n = nw + 32 * c + (lane & 31);
-    sc[c] = !kSplit && n < a.Np ? ep.scale[n] : 0.0f;
+    for (int c = 0; c < NJ; ++c) {
+      sc[c] = col_scale[wn * NJ * 32 + 32 * c + (lane & 31)];
+      bs[c] = biased ? col_bias[wn * NJ * 32 + 32 * c + (lane & 31)] : 0.0f;
+    }
   }
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
@@ -267,20 +275,24 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const Til
     for (int vh = 0; vh < 2; ++vh) {
       const int mr = (wm * MI + i) * 32 + 16 * vh;  // first row of the pass
       if (mr >= rows) return;
-      v4f rsc[2];
+      v4f rsc[2], rgt[2];
       if (!kSplit) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
-          rsc[g] = *reinterpret_cast<const v4f *>(rs + mr + 8 * g + rl);
+        for (int g = 0; g < 2; ++g) {
+          rsc[g] = *reinterpret_cast<const v4f *>(row_scale + mr + 8 * g + rl);
+          rgt[g] = gated ? *reinterpret_cast<const v4f *>(row_gate + mr + 8 * g + rl)
+                         : v4f{1.0f, 1.0f, 1.0f, 1.0f};
+        }
       }
 #pragma unroll
       for (int vv = 0; vv < 8; ++vv) {
         const int v = 8 * vh + vv, r = 8 * (vv >> 2) + rl + (vv & 3);
+        float *row = slice + r * kPitch + (lane & 31);
         if constexpr (kSplit) {
 #pragma unroll
           for (int c = 0; c < NJ; ++c) {
             const auto e = acc[i][c][v];
-            slice[r * kPitch + 32 * c + (lane & 31)] = __builtin_bit_cast(float, e);
+            row[32 * c] = __builtin_bit_cast(float, e);
           }
         } else if constexpr (kGated) {
           const float x = rsc[vv >> 2][vv & 3];
@@ -289,26 +301,33 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const Til
           for (int c = 0; c < NJ; c += 2) {
             const float h = swiglu((float)acc[i][c][v] * x * sc[c],
                                    (float)acc[i][c + 1][v] * x * sc[c + 1]);
-            slice[r * kPitch + 16 * c + (lane & 31)] = h;
+            row[16 * c] = h;
             m = umax(m, nw / 2 + 16 * c + (lane & 31) < ep.N ? abs_bits(h) : 0u);
           }
           m = half_wave_max(m);
           if ((lane & 31) == 31) slice[r * kPitch + NJ * 32] = __uint_as_float(m);
         } else {
           const float x = rsc[vv >> 2][vv & 3];
+          if (!biased && !gated) {
 #pragma unroll
-          for (int c = 0; c < NJ; ++c)
-            slice[r * kPitch + 32 * c + (lane & 31)] = (float)acc[i][c][v] * x * sc[c];
+            for (int c = 0; c < NJ; ++c) row[32 * c] = (float)acc[i][c][v] * x * sc[c];
+          } else {
+            const float g = rgt[vv >> 2][vv & 3];
+#pragma unroll
+            for (int c = 0; c < NJ; ++c)
+              row[32 * c] = ((float)acc[i][c][v] * x * sc[c] + bs[c]) * g;
+          }
         }
       }
       const int left = rows - mr;  // rows of the pass that exist
       if constexpr (kSplit) {
         int32_t *part = a.partial + (size_t)blockIdx.y * a.T * a.Np;
-        for (int j = lane; j < 16 * NJ * 8; j += 64) {
-          const int r = j / (NJ * 8), c4 = j % (NJ * 8) * 4;
+#pragma unroll
+        for (int j = 0; j < NJ * 2; ++j) {
+          const int r = (j * 64 + lane) / (NJ * 8), c4 = (j * 64 + lane) % (NJ * 8) * 4;
+          const v4f x = *reinterpret_cast<const v4f *>(slice + r * kPitch + c4);
           if (r < left && nw + c4 < a.Np)
-            *reinterpret_cast<v4f *>(part + (m0 + mr + r) * a.Np + nw + c4) =
-                *reinterpret_cast<const v4f *>(slice + r * kPitch + c4);
+            *reinterpret_cast<v4f *>(part + (m0 + mr + r) * a.Np + nw + c4) = x;
         }
       } else if constexpr (kGated) {
         if (lane < 16 && lane < left)
@@ -316,15 +335,17 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const Til
         // h columns nw/2 .. + 16 NJ; h rows have the pitch of code rows, so
         // whole 32-column runs exist
         float *h = static_cast<float *>(ep.out);
-        for (int j = lane; j < 16 * NJ * 4; j += 64) {
-          const int r = j / (NJ * 4), c4 = j % (NJ * 4) * 4;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const int r = (j * 64 + lane) / (NJ * 4), c4 = (j * 64 + lane) % (NJ * 4) * 4;
+          const v4f x = *reinterpret_cast<const v4f *>(slice + r * kPitch + c4);
           if (r < left && nw + 2 * c4 < a.Np)
-            *reinterpret_cast<v4f *>(h + (m0 + mr + r) * ep.ld_out + nw / 2 + c4) =
-                *reinterpret_cast<const v4f *>(slice + r * kPitch + c4);
+            *reinterpret_cast<v4f *>(h + (m0 + mr + r) * ep.ld_out + nw / 2 + c4) = x;
         }
       } else {
-        for (int j = lane; j < 16 * NJ * 4; j += 64) {
-          const int r = j / (NJ * 4), c8 = j % (NJ * 4) * 8;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const int r = (j * 64 + lane) / (NJ * 4), c8 = (j * 64 + lane) % (NJ * 4) * 8;
           float v[8];
           const v4f x = *reinterpret_cast<const v4f *>(slice + r * kPitch + c8);
           const v4f y = *reinterpret_cast<const v4f *>(slice + r * kPitch + c8 + 4);
@@ -333,7 +354,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const Til
             v[k] = x[k];
             v[4 + k] = y[k];
           }
-          if (r < left) finish_columns<8>(ep, m0 + mr + r, nw + c8, v);
+          if (r < left) store_columns<8>(ep, m0 + mr + r, nw + c8, v);
         }
       }
     }
@@ -394,7 +415,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const TiledLinear a) {
   }
 }
 
-template <int WM, int WN, int MI, int NJ, int SA, int SB, bool kGated, bool kSplit>
+template <int WM, int WN, int MI, int NJ, int S, bool kGated, bool kSplit>
 hipError_t run(TiledLinear a, bool fp8, hipStream_t st) {
   constexpr int BM = WM * MI * 32, BN = WN * NJ * 32;
   a.mt = (int)((a.T + BM - 1) / BM);
@@ -409,9 +430,9 @@ hipError_t run(TiledLinear a, bool fp8, hipStream_t st) {
   const dim3 block(64 * WM * WN);
   const Timing tm{};
   if (fp8)
-    return launch_kernel(linear_tiled_kernel<WM, WN, MI, NJ, SA, SB, true, kGated, kSplit>, grid,
+    return launch_kernel(linear_tiled_kernel<WM, WN, MI, NJ, S, true, kGated, kSplit>, grid,
                          block, st, tm, a);
-  return launch_kernel(linear_tiled_kernel<WM, WN, MI, NJ, SA, SB, false, kGated, kSplit>, grid,
+  return launch_kernel(linear_tiled_kernel<WM, WN, MI, NJ, S, false, kGated, kSplit>, grid,
                        block, st, tm, a);
 }
 
@@ -424,35 +445,40 @@ hipError_t join(const TiledLinear &a, bool fp8, hipStream_t st) {
   return launch_kernel(linear_join_kernel<false, kGated>, grid, dim3(256), st, Timing{}, a);
 }
 
-// Tile shapes: every one as the wavefronts' arrangement and the depth of its
-// rings.
-template <bool kGated, bool kSplit>
-hipError_t run_shape(int shape, const TiledLinear &a, bool fp8, hipStream_t st) {
-  switch (shape) {
-    case 0: return run<4, 2, 2, 4, 2, 3, kGated, kSplit>(a, fp8, st);  // 256 x 256
-    case 1: return run<4, 2, 2, 2, 3, 3, kGated, kSplit>(a, fp8, st);  // 256 x 128
-    case 2: return run<2, 2, 3, 2, 4, 4, kGated, kSplit>(a, fp8, st);  // 192 x 128
-    case 3: return run<2, 2, 2, 2, 5, 5, kGated, kSplit>(a, fp8, st);  // 128 x 128
-    case 4: return run<2, 2, 1, 2, 6, 6, kGated, kSplit>(a, fp8, st);  // 64 x 128
-    case 5: return run<2, 4, 2, 2, 3, 3, kGated, kSplit>(a, fp8, st);  // 128 x 256
-    case 6: return run<4, 2, 1, 2, 5, 5, kGated, kSplit>(a, fp8, st);  // 128 x 128, 8 waves
-    case 7: return run<2, 2, 4, 4, 2, 3, kGated, kSplit>(a, fp8, st);  // 256 x 256, 4 waves
-    default: return run<4, 2, 2, 6, 2, 2, kGated, kSplit>(a, fp8, st); // 256 x 384
-  }
-}
-
+// Tile shape and split of K by estimated time. A stage of 128 k takes a full
+// chip 2.25 us with 256 x 256 tiles, 1.15 with 128 x 256 and 0.5 with 64 x 128
+// (one block per compute unit; two of the last take 0.9 together), measured at
+// K 4096 on MI355X: 69 us for 4096 x 4096 tokens x outputs in 256 tiles of
+// 256 x 256 (128 x 256: 79, 64 x 128: 100), 33 us for 1021 x 4999 in 160 tiles
+// of 128 x 256 (256 x 256: 53, 64 x 128: 40), 18 us for 512 x 4096 in 256 tiles
+// of 64 x 128 (128 x 256: 31). A launch that leaves most compute units idle
+// splits K where that saves more than the second launch (6 us) and the partial
+// sums (8 bytes each at 4 TB/s) cost: 128 x 4096 tokens x outputs, K 4096: 17.0
+// us in 64 tiles, 14.4 with K in three.
 template <bool kGated>
 hipError_t pick(TiledLinear a, bool fp8, hipStream_t st) {
-  int shape;
+  auto tiles = [&](int bm, int bn) {
+    return ((a.T + bm - 1) / bm) * (int64_t)((a.Np + bn - 1) / bn);
+  };
+  const int D = a.Kp >> 7;
+  const int64_t t0 = tiles(256, 256), t1 = tiles(128, 256), t2 = tiles(64, 128);
+  const double c0 = (double)((t0 + 255) / 256) * 2.25, c1 = (double)((t1 + 255) / 256) * 1.15;
+  const double c2 = t2 <= 256 ? 0.5 : (double)((t2 + 511) / 512) * 0.9;
   a.split = 1;
-  const int64_t t256 = ((a.T + 255) / 256) * ((a.Np + 255) / 256);
-  const int64_t t128 = ((a.T + 127) / 128) * ((a.Np + 127) / 128);
-  shape = t256 >= 192 ? 0 : t128 >= 128 ? 3 : 4;
-  if (a.split > 1) {
-    const hipError_t e = run_shape<kGated, true>(shape, a, fp8, st);
-    return e == hipSuccess ? join<kGated>(a, fp8, st) : e;
+  if (c0 <= c1 && c0 <= c2) return run<4, 2, 2, 4, 2, kGated, false>(a, fp8, st);
+  if (c1 <= c2) return run<2, 4, 2, 2, 2, kGated, false>(a, fp8, st);
+  double best = 0.0;
+  for (int s = 2; s <= 4 && t2 * s <= 256 && D >= 4 * s; ++s) {
+    const double sums = (double)s * (double)a.T * a.Np;
+    const double gain = 0.5 * D * (1.0 - 1.0 / s) - 6.0 - sums * 8.0 / 4e6;
+    if (gain > best && sums * 4.0 <= (double)kPartialBytes) {
+      best = gain;
+      a.split = s;
+    }
   }
-  return run_shape<kGated, false>(shape, a, fp8, st);
+  if (a.split == 1) return run<2, 2, 1, 2, 3, kGated, false>(a, fp8, st);
+  const hipError_t e = run<2, 2, 1, 2, 3, kGated, true>(a, fp8, st);
+  return e == hipSuccess ? join<kGated>(a, fp8, st) : e;
 }
 
 }  // namespace

@@ -43,8 +43,12 @@ __device__ __forceinline__ void load8(const float *p, int rem, float *o) {
     for (int i = 0; i < 8; ++i) o[i] = i < rem ? p[i] : 0.0f;
   }
 }
+// Two values rounded to bf16 (nearest, ties to even; NaN stays NaN) by the one
+// hardware instruction.
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
-  return (uint32_t)f32_to_bf16(a) | ((uint32_t)f32_to_bf16(b) << 16);
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2bf));
 }
 __device__ __forceinline__ void store8(uint16_t *p, int rem, const float *v) {
   if (rem >= 8) {
