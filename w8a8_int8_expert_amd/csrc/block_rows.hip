@@ -353,20 +353,29 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const void *__restrict__
   launch_kernel(kernel<TPR, NC>,                                                              \
                 dim3((unsigned)((T + RowGroup<TPR>::kRows - 1) / RowGroup<TPR>::kRows)),      \
                 dim3(RowGroup<TPR>::kThreads), st, Timing{}, __VA_ARGS__)
+// A thread per chunk up to 8192 columns: the shortest chain for a row alone (one
+// row of 4096: 3.4 us, against 4.2 with two chunks a thread and 9.3 with one
+// wavefront), and the most loads in flight for many (add_norm of 16384 rows of
+// 4096, bf16: 95 us = 5.6 TB/s, against 100 and 127). Two or four rows per
+// block, sharing the weights' loads, were no faster (98, 106).
 #define MOE_ROWS_BY_WIDTH(kernel, width, ...)                              \
   do {                                                                     \
     if ((width) <= 512) return MOE_ROWS(kernel, 64, 1, __VA_ARGS__);       \
-    if ((width) <= 1024) return MOE_ROWS(kernel, 64, 2, __VA_ARGS__);      \
     if ((width) <= 2048) return MOE_ROWS(kernel, 256, 1, __VA_ARGS__);     \
-    if ((width) <= 4096) return MOE_ROWS(kernel, 256, 2, __VA_ARGS__);     \
-    if ((width) <= 8192) return MOE_ROWS(kernel, 256, 4, __VA_ARGS__);     \
-    if ((width) <= 16384) return MOE_ROWS(kernel, 512, 4, __VA_ARGS__);    \
+    if ((width) <= 4096) return MOE_ROWS(kernel, 512, 1, __VA_ARGS__);     \
+    if ((width) <= 8192) return MOE_ROWS(kernel, 1024, 1, __VA_ARGS__);    \
     if ((width) <= 32768) return MOE_ROWS(kernel, 1024, 4, __VA_ARGS__);   \
     return MOE_ROWS(kernel, 1024, 8, __VA_ARGS__);                         \
   } while (0)
 
 hipError_t launch_act_rows(const uint16_t *x, int64_t ld, int64_t T, int K, const float *inv,
                            bool fp8, int8_t *q, float *s, uint32_t *clear, hipStream_t st) {
+  // Many rows and one reduction: two chunks a thread, half the barriers
+  // (16384 x 4096: 34.4 us against 40.6, 8192 x 8192: 35.2 against 43.8).
+  if (T > 2048 && K > 2048 && K <= 4096)
+    return MOE_ROWS(act_rows_kernel, 256, 2, x, ld, T, K, inv, fp8, q, s, clear);
+  if (T > 2048 && K > 4096 && K <= 8192)
+    return MOE_ROWS(act_rows_kernel, 512, 2, x, ld, T, K, inv, fp8, q, s, clear);
   MOE_ROWS_BY_WIDTH(act_rows_kernel, K, x, ld, T, K, inv, fp8, q, s, clear);
 }
 
