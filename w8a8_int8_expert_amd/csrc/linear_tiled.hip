@@ -22,6 +22,8 @@
 //
 // Few tiles: blockIdx.y cuts K into `split` parts; each writes its raw sums
 // and a second launch adds them in order and finishes the columns.
+#include <type_traits>
+
 #include "epilogue_device.h"
 
 namespace moe {
@@ -112,19 +114,16 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const Til
     p = p < (a.Np >> 4) ? p : (a.Np >> 4) - 1;  // columns past Np: never stored
     bsrc[t] = a.w + frag_tile(p, 2 * d0 + (j & 1), a.Kp) + lane * 16;
   }
-  auto issue_a = [&](int d, int slot) {
-    int8_t *st = lds + slot * kA;
-#pragma unroll
-    for (int t = 0; t < kALoads; ++t)
-      dma16(asrc[t] + (size_t)d * 128,
-            __builtin_amdgcn_readfirstlane(lds_addr(st + (kALoads * wave + t) * 1024)));
-  };
-  auto issue_b = [&](int d, int slot) {
-    int8_t *st = lds + S * kA + slot * kB;
-#pragma unroll
-    for (int t = 0; t < kBLoads; ++t)
-      dma16(bsrc[t] + (size_t)d * 2048,
-            __builtin_amdgcn_readfirstlane(lds_addr(st + (kBLoads * wave + t) * 1024)));
+  // The wavefront's loads of a stage are numbered: kALoads of tokens, then
+  // kBLoads of weights.
+  constexpr int kLoads = kALoads + kBLoads, kEarly = kLoads / 2;
+  auto load = [&](int d, int slot, int t) {
+    const bool tokens = t < kALoads;
+    const int u = tokens ? t : t - kALoads;
+    const int8_t *src = tokens ? asrc[u] + (size_t)d * 128 : bsrc[u] + (size_t)d * 2048;
+    int8_t *dst = tokens ? lds + slot * kA + (kALoads * wave + u) * 1024
+                         : lds + S * kA + slot * kB + (kBLoads * wave + u) * 1024;
+    dma16(src, __builtin_amdgcn_readfirstlane(lds_addr(dst)));
   };
 
   // What the epilogue needs of each row and column goes to LDS ahead of the
@@ -170,88 +169,103 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const Til
   // The operands of a step are read while the step before it multiplies, and
   // the first ones of a stage while the last step of the stage before does, so
   // that neither the reads nor the barrier between two stages leave the matrix
-  // cores idle.
+  // cores idle. Reads and loads go between the matrix instructions one by one:
+  // a wavefront that issues its loads in a row waits for the load queue with
+  // the matrix cores idle.
   constexpr int kSteps = kF8 ? 2 : 4, kH = kF8 ? 2 : 1;
+  constexpr int kReads = (MI + NJ) * kH, kM = MI * NJ;
   v4i af[2][MI][kH], bf[2][NJ][kH];
-  auto read = [&](int buf, int s, const int8_t *as, const int8_t *bs) {
-#pragma unroll
-    for (int h = 0; h < kH; ++h) {
-      const int k = s * kH + h;
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-        af[buf][i][h] = *reinterpret_cast<const v4i *>(as + aoff + i * 4096 + axor[k]);
-#pragma unroll
-      for (int c = 0; c < NJ; ++c)
-        bf[buf][c][h] = *reinterpret_cast<const v4i *>(bs + boff + c * 4096 + (k >> 1) * 1024 +
-                                                       (k & 1) * 512);
-    }
+  auto read = [&](int buf, int s, const int8_t *as, const int8_t *bs, int j) {
+    const int h = j % kH, i = j / kH, k = s * kH + h;
+    if (i < MI)
+      af[buf][i][h] = *reinterpret_cast<const v4i *>(as + aoff + i * 4096 + axor[k]);
+    else
+      bf[buf][i - MI][h] = *reinterpret_cast<const v4i *>(
+          bs + boff + (i - MI) * 4096 + (k >> 1) * 1024 + (k & 1) * 512);
   };
-  auto multiply = [&](int buf) {
+  // One step: the products of buffer s % 2, the reads of step `ns` into the
+  // other from a stage at as, bs (ns < 0: none), loads [t0, t1) of stage d.
+  auto step = [&](int s, int ns, const int8_t *as, const int8_t *bs, int t0, int t1, int d,
+                  int to) {
+    constexpr int kPer = (kReads + kM - 1) / kM;
+    const int buf = s & 1;
 #pragma unroll
-    for (int c = 0; c < NJ; ++c)
+    for (int m = 0; m < kM; ++m) {
+      const int c = m / MI, i = m % MI;
+      if constexpr (kF8)
+        acc[i][c] =
+            mfma32f8(af[buf][i][0], af[buf][i][1], bf[buf][c][0], bf[buf][c][1], acc[i][c]);
+      else
+        acc[i][c] = mfma32(af[buf][i][0], bf[buf][c][0], acc[i][c]);
+      if (ns >= 0) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        if constexpr (kF8)
-          acc[i][c] = mfma32f8(af[buf][i][0], af[buf][i][1], bf[buf][c][0], bf[buf][c][1],
-                               acc[i][c]);
-        else
-          acc[i][c] = mfma32(af[buf][i][0], bf[buf][c][0], acc[i][c]);
+        for (int j = m * kPer; j < (m + 1) * kPer; ++j)
+          if (j < kReads) read(buf ^ 1, ns, as, bs, j);
       }
-  };
-  // Each of the step's reads goes between its matrix instructions.
-  auto interleave = [&]() {
-    constexpr int kReads = (MI + NJ) * kH, kM = MI * NJ;
-    constexpr int kPer = kM > kReads ? kM / kReads : 1;
 #pragma unroll
-    for (int i = 0; i < kReads; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
+      for (int j = t0; j < t1; ++j)
+        if ((j - t0) % kM == m) load(d, to, j);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
-  // Stages 0 .. S-1 are issued first; at the end of stage d, once every
-  // wavefront has read the last of it, stage d + S goes to its slot. Loads
-  // return in order, so what may still be in flight when stage d+1 begins is
-  // what was issued after it: stages d+2 .. d+S-1.
+  // Stages 0 .. S-1 come first (the last of them, where all S exist, by its
+  // early loads only). Once every wavefront has read the last of stage d, stage
+  // d + S goes to its slot: the early loads during the last step of stage d,
+  // the others during the first of stage d + 1. Loads return in order, so what
+  // may still be in flight when stage d + 1 begins is what was issued after it:
+  // stages d + 2 .. d + S - 1.
+  const int8_t *const rings = lds;
 #pragma unroll
   for (int d = 0; d < S; ++d)
     if (d < D) {
-      issue_a(d, d);
-      issue_b(d, d);
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j)
+        if (d < S - 1 || j < kEarly) load(d, d, j);
     }
-  wait_stages<S - 1, kALoads + kBLoads>(D - 1);
+  if (D >= S) wait_barrier<(S - 2) * kLoads + kEarly>();
+  else wait_stages<S - 2, kLoads>(D - 1);
   const bool skip = wm * MI * 32 >= rows;  // no row of this wavefront exists
   int slot = 0;                            // of stage d
-  auto next_stage = [&](int d) {           // after stage d's last read
-    wait_stages<S - 2, kALoads + kBLoads>(D - 2 - d);
-    if (d + S < D) {
-      issue_a(d + S, slot);
-      issue_b(d + S, slot);
-    }
-    slot = slot + 1 == S ? 0 : slot + 1;
-  };
-  if (skip) {
-    for (int d = 0; d + 1 < D; ++d) next_stage(d);
-  } else {
-    read(0, 0, lds, lds + S * kA);
-    auto steps = [&]() {  // all but the last step of the stage in `slot`
-      const int8_t *as = lds + slot * kA, *bs = lds + S * kA + slot * kB;
+  auto after = [&](int s) { return s + 1 == S ? 0 : s + 1; };
+  auto before = [&](int s) { return s == 0 ? S - 1 : s - 1; };
+  auto stage = [&](auto late, auto early, auto last, int d) {
+    const int8_t *as = rings + slot * kA, *bs = rings + S * kA + slot * kB;
 #pragma unroll
-      for (int s = 0; s + 1 < kSteps; ++s) {
-        read((s + 1) & 1, s + 1, as, bs);
-        multiply(s & 1);
-        interleave();
-      }
-    };
-    for (int d = 0; d + 1 < D; ++d) {
-      steps();
-      next_stage(d);
-      read(0, 0, lds + slot * kA, lds + S * kA + slot * kB);
-      multiply((kSteps - 1) & 1);
-      interleave();
+    for (int s = 0; s + 1 < kSteps; ++s)
+      step(s, s + 1, as, bs, late && s == 0 ? kEarly : 0, late && s == 0 ? kLoads : 0, d + S - 1,
+           before(slot));
+    if constexpr (last) {
+      step(kSteps - 1, -1, as, bs, 0, 0, 0, 0);
+    } else {
+      wait_stages<S - 2, kLoads>(D - 2 - d);
+      const int next = after(slot);
+      step(kSteps - 1, 0, rings + next * kA, rings + S * kA + next * kB, 0, early ? kEarly : 0,
+           d + S, slot);
+      slot = next;
     }
-    steps();
-    multiply((kSteps - 1) & 1);
+  };
+  int d = 0;
+  if (skip) {
+    for (; d + 1 < D; ++d) {
+      if (d + S - 1 < D) {
+        for (int j = kEarly; j < kLoads; ++j) load(d + S - 1, before(slot), j);
+      }
+      wait_stages<S - 2, kLoads>(D - 2 - d);
+      if (d + S < D) {
+        for (int j = 0; j < kEarly; ++j) load(d + S, slot, j);
+      }
+      slot = after(slot);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kReads; ++j) read(0, 0, rings, rings + S * kA, j);
+    constexpr std::true_type yes;
+    constexpr std::false_type no;
+    for (; d + S < D; ++d) stage(yes, yes, no, d);
+    for (; d + S <= D && d + 1 < D; ++d) stage(yes, no, no, d);
+    for (; d + 1 < D; ++d) stage(no, no, no, d);
+    stage(no, no, yes, d);
   }
   wait_barrier<0>();  // every wavefront is done with the rings
 
