@@ -23,7 +23,7 @@ import torch
 import w8a8_int8_expert_amd as _m
 
 _BF16, _F32, _I8, _E4M3 = torch.bfloat16, torch.float32, torch.int8, torch.float8_e4m3fn
-_OUT_TYPES = (_BF16, _F32)
+_OUT_TYPES, _ONLY_BF16 = (_BF16, _F32), (_BF16,)
 _FORMATS = {"int8": 0, "fp8": 1}
 _NORMS = {None: 0, "none": 0, "rms": 1, "layer": 2}
 # A call of one token is a few microseconds of GPU work: what the binding does
@@ -109,7 +109,7 @@ def act_quant(x, inv_smooth=None, fp8: bool = False):
         _fail("x must be a [T][K] tensor")
     T, K = x.shape
     dev = x.device
-    px, ld = _rows(x, "x", (_BF16,), T, K, dev)
+    px, ld = _rows(x, "x", _ONLY_BF16, T, K, dev)
     inv = _vector(inv_smooth, "inv_smooth", K, dev)
     q, s = _empty_codes(T, K, fp8, dev)
     _call("moe_w8a8_act_quant", dev, K, int(bool(fp8)), px, ld, T, inv, q.data_ptr(), s.data_ptr())
@@ -166,7 +166,7 @@ class _Product:
         T = first.shape[0]
         act = _m.moe_w8a8_act()
         if codes is None:
-            act.x, act.ld_x = _rows(x, "x", (_BF16,), T, K, dev)
+            act.x, act.ld_x = _rows(x, "x", _ONLY_BF16, T, K, dev)
         else:
             pitch = (K + 127) // 128 * 128
             act.q, ld = _rows(first, "codes", _code_types(self.fp8), T, pitch, dev)
@@ -185,7 +185,7 @@ class _Product:
         if gate is not None:
             res.gate = _vector(gate, "gate", T, dev)
         if add is not None:
-            res.add, res.ld_add = _rows(add, "add", (_BF16,), T, N, dev)
+            res.add, res.ld_add = _rows(add, "add", _ONLY_BF16, T, N, dev)
         return T, act, res, out
 
 
@@ -302,66 +302,58 @@ def add_norm(y, residual=None, norm="rms", weight=None, bias=None, eps: float = 
         _fail("y must be a [T][H] tensor")
     T, H = y.shape
     dev = y.device
-    bf16 = (_BF16,)
     if post_norm is None and (post_weight is not None or post_bias is not None):
         post_norm = norm
     if norm not in _NORMS or post_norm not in _NORMS:
         _fail("norm must be 'rms', 'layer' or 'none'")
     if codes is not None and codes not in _FORMATS:
         _fail("codes must be 'int8' or 'fp8'")
-    a = _m.moe_w8a8_add_norm_args()
-    a.hidden, a.pre_norm, a.post_norm = H, _NORMS[norm], _NORMS[post_norm]
-    a.eps, a.residual_scale, a.block_scale = eps, residual_scale, block_scale
-    a.y, a.ld_y = _rows(y, "y", bf16, T, H, dev)
+    p_y, ld_y = _rows(y, "y", _ONLY_BF16, T, H, dev)
+    p_res = p_out = p_norm = p_token = p_rows = q = s = None
+    ld_res = ld_out = ld_norm = ld_gate = group = 0
     rtype = _BF16
     if residual is not None:
-        a.residual, a.ld_residual = _rows(residual, "residual", (_BF16, _F32),
-                                          T, H, dev)
+        p_res, ld_res = _rows(residual, "residual", _OUT_TYPES, T, H, dev)
         rtype = residual.dtype
     elif isinstance(residual_out, torch.Tensor):
         rtype = residual_out.dtype
     if residual_out is True:
         residual_out = torch.empty(T, H, dtype=rtype, device=dev)
-    elif residual_out is False:
+        p_out, ld_out = residual_out.data_ptr(), H
+    elif residual_out is False or residual_out is None:
         residual_out = None
-    if residual_out is not None:
-        a.residual_out, a.ld_residual_out = _rows(
-            residual_out, "residual_out",
-            (rtype,) if residual is not None else (_BF16, _F32), T, H, dev)
-    a.residual_type = 1 if rtype == _F32 else 0
+    else:
+        p_out, ld_out = _rows(residual_out, "residual_out",
+                              _OUT_TYPES if residual is None else (rtype,), T, H, dev)
     if normed is True:
         normed = torch.empty(T, H, dtype=_BF16, device=dev)
-    elif normed is False:
+        p_norm, ld_norm = normed.data_ptr(), H
+    elif normed is False or normed is None:
         normed = None
-    if normed is not None:
-        a.normed, a.ld_normed = _rows(normed, "normed", bf16, T, H, dev)
-    if weight is not None:
-        a.pre_weight = _vector(weight, "weight", H, dev)
-    if bias is not None:
-        a.pre_bias = _vector(bias, "bias", H, dev)
-    if post_weight is not None:
-        a.post_weight = _vector(post_weight, "post_weight", H, dev)
-    if post_bias is not None:
-        a.post_bias = _vector(post_bias, "post_bias", H, dev)
+    else:
+        p_norm, ld_norm = _rows(normed, "normed", _ONLY_BF16, T, H, dev)
     if gate is not None and T > 0:
         if isinstance(gate, torch.Tensor) and gate.dtype == _F32:
             if gate.shape not in ((T,), (T, 1)):
                 _fail("an fp32 gate must be [T] or [T][1]")
-            a.gate_token = _vector(gate, "gate", T, dev)
+            p_token = _vector(gate, "gate", T, dev)
         else:
             if not isinstance(gate, torch.Tensor) or gate.dim() != 2 or gate.shape[0] < 1:
                 _fail("gate must be fp32 [T] or bf16 [G][H]")
             G = gate.shape[0]
-            a.gate_rows, a.ld_gate = _rows(gate, "gate", bf16, G, H, dev)
-            a.gate_group = -(-T // G) if gate_group is None else int(gate_group)
-            if a.gate_group < 1 or -(-T // a.gate_group) > G:
-                _fail("gate has %d rows, too few for %d tokens in groups of %d" %
-                      (G, T, a.gate_group))
-    q = s = None
+            p_rows, ld_gate = _rows(gate, "gate", _ONLY_BF16, G, H, dev)
+            group = -(-T // G) if gate_group is None else int(gate_group)
+            if group < 1 or -(-T // group) > G:
+                _fail("gate has %d rows, too few for %d tokens in groups of %d" % (G, T, group))
     if codes is not None:
         q, s = _empty_codes(T, H, codes == "fp8", dev)
-        a.q, a.s, a.format = q.data_ptr(), s.data_ptr(), _FORMATS[codes]
-        if inv_smooth is not None:
-            a.inv_smooth = _vector(inv_smooth, "inv_smooth", H, dev)
+    a = _m.moe_w8a8_add_norm_args(
+        H, _NORMS[norm], _NORMS[post_norm], 1 if rtype == _F32 else 0, _FORMATS.get(codes, 0),
+        eps, residual_scale, block_scale, p_y, ld_y, p_res, ld_res, p_out, ld_out,
+        _vector(post_weight, "post_weight", H, dev), _vector(post_bias, "post_bias", H, dev),
+        _vector(weight, "weight", H, dev), _vector(bias, "bias", H, dev), p_token, p_rows,
+        ld_gate, group, p_norm, ld_norm,
+        None if codes is None else _vector(inv_smooth, "inv_smooth", H, dev),
+        None if q is None else q.data_ptr(), None if s is None else s.data_ptr())
     _call("moe_w8a8_add_norm", dev, ctypes.byref(a), T)
     return AddNorm(residual_out, normed, q, s)
