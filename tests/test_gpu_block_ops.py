@@ -151,7 +151,7 @@ def test_weights_packed(lib, N, K, fp8, gated):
 # ------------------------------------------------------------------- linear
 LINEAR = [
     # T, K, N
-    (1, 1, 1), (1, 64, 16), (1, 4096, 100), (2, 129, 17), (3, 1000, 33), (4, 12288, 40),
+    (1, 1, 1), (1, 64, 16), (1, 4096, 100), (2, 129, 17), (3, 1000, 33), (4, 12288, 40), (1, 48000, 33), (3, 16000, 35),
     (4, 300, 257), (5, 127, 15), (15, 512, 48), (16, 2048, 31), (17, 128, 16), (31, 640, 130),
     (33, 4097, 64), (48, 256, 333), (63, 1024, 5), (64, 1100, 96), (65, 128, 128), (65, 1, 1),
     (100, 2000, 300), (128, 512, 129), (129, 384, 255), (200, 4096, 500), (256, 1024, 1024),
@@ -458,6 +458,44 @@ def test_add_norm(lib, T, H, kind, post):
     assert torch.equal(outs["int8"].normed, outs["fp8"].normed)
 
 
+def test_rounding_to_bf16(lib):
+    """Every bf16 value passes add_norm without a norm unchanged, and fp32
+    residuals round to nearest, ties to even, subnormals and overflow included."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.uint16)
+    allv = torch.from_numpy(bits.numpy().copy().view("int16")).view(BF).reshape(256, 256)
+    o = lib.add_norm(allv.cuda(), None, norm="none")
+    for got in (o.residual.cpu(), o.normed.cpu()):
+        nan = torch.isnan(allv)
+        assert torch.equal(torch.isnan(got), nan)
+        assert torch.equal(got.view(torch.int16)[~nan], allv.view(torch.int16)[~nan])
+    g = torch.Generator().manual_seed(3)
+    raw = torch.randint(-(1 << 31), 1 << 31, (64, 1000), generator=g).to(torch.int32)
+    raw[:, ::3] = (raw[:, ::3] & -65536) | 0x8000                 # exact ties
+    f = raw.view(F32)
+    zero = torch.zeros(64, 1000, dtype=BF)
+    o = lib.add_norm(zero.cuda(), f.cuda(), norm="none")
+    keep = ~torch.isnan(f)
+    assert torch.equal(o.normed.cpu()[keep], f.to(BF)[keep])
+    assert torch.equal(o.residual.cpu()[keep], f[keep])
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_norm_of_the_largest_values(lib, kind):
+    """Rows whose squares pass the fp32 range still normalise; rows beside them
+    are what they are without them."""
+    T, H = 5, 900
+    y = tokens(T, H, 4).float()
+    y[1] *= 2.0 ** 100
+    y[3] = y[3].sign() * 2.0 ** 126
+    y = y.to(BF)
+    w = vec(H, 1)
+    o = lib.add_norm(y.cuda(), None, norm=kind, weight=w.cuda(), codes="int8")
+    c = dict(norm=kind, post="none", eps=1e-6, bs=1.0, rs=1.0, w=w)
+    _, _, n, en = add_norm64(y, None, c)
+    R.check(o.normed, n, en + R.half_step(BF) * (n.abs() + en) + 1e-44, kind)
+    assert bool(torch.isfinite(o.scales).all())
+
+
 def test_add_norm_in_place_and_parts(lib):
     """residual_out over residual and normed over y; outputs not asked for are
     not made; strided rows leave their neighbours alone."""
@@ -565,6 +603,31 @@ def test_block_runs_in_graphs_and_streams(lib, T, fp8):
         torch.cuda.synchronize()
         for k, (graph, x, g, out) in enumerate(graphs):
             assert all(torch.equal(u, v) for u, v in zip(eager[(i + k) % 4], out)), (i, k)
+
+
+def test_reloaded_weights_in_a_captured_call(lib):
+    """A captured call follows what is loaded into its operator later: codes,
+    scales, smoothing and bias keep their places."""
+    T, K, N = 3, 200, 60
+    x = tokens(T, K, 1).cuda()
+    lin = lib.W8A8Linear(K, N)
+    sets = [weight(N, K, False, s) + (vec(K, s), vec(N, s)) for s in (1, 2)]
+    load = lambda s: lin.load_quantized(s[0].cuda(), s[1].cuda(), inv_smooth=s[2].cuda(),  # noqa: E731
+                                        bias=s[3].cuda())
+    want = []
+    for s in sets:
+        load(s)
+        want.append(lin(x).clone())
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = lin(x)
+    for k in (0, 1, 0):
+        load(sets[k])
+        torch.cuda.empty_cache()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[k])
 
 
 def test_shared_expert_beside_the_layer(lib):

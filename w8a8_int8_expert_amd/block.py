@@ -128,19 +128,23 @@ class _Weights:
         self.codes = torch.empty(size, dtype=_I8, device=device)
         self.scale = torch.empty(_m.moe_w8a8_linear_scales(N, gated), dtype=_F32,
                                  device=device)
-        self.inv_smooth = self.bias = None
+        # The optional vectors have a place of their own for good: a captured
+        # call keeps their addresses, whatever is loaded later.
+        self.inv_smooth = torch.empty(K, dtype=_F32, device=device)
+        self.bias = torch.empty(N, dtype=_F32, device=device)
         self.struct = _m.moe_w8a8_linear_weights(K, N, int(fp8), int(gated),
                                                  self.codes.data_ptr(), self.scale.data_ptr(),
                                                  None, None)
         self.ref = ctypes.byref(self.struct)
 
     def vectors(self, inv_smooth, bias):
-        """Keep copies of the two optional vectors."""
+        """Copy the two optional vectors in; None turns one off."""
         for name, t, n in (("inv_smooth", inv_smooth, self.K), ("bias", bias, self.N)):
             _vector(t, name, n, self.device)
-            t = None if t is None else t.detach().reshape(n).clone()
-            setattr(self, name, t)
-            setattr(self.struct, name, None if t is None else t.data_ptr())
+            own = getattr(self, name)
+            if t is not None:
+                own.copy_(t.detach().reshape(n))
+            setattr(self.struct, name, None if t is None else own.data_ptr())
 
     def quantise(self, w, smooth):
         p, ld = _rows(w, "weight", (_BF16, _F32), self.N, self.K, self.device)

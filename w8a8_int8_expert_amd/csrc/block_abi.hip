@@ -86,10 +86,10 @@ Epilogue epilogue(const moe_w8a8_linear_weights &w, const moe_w8a8_result &r) {
   return e;
 }
 
-// The streaming product codes its tokens itself: few rows, and they fit LDS
-// beside its partial sums.
+// The streaming product codes its tokens itself: few rows, and they fit 64 KB
+// of LDS beside its partial sums (16 KB).
 bool fused_rows(int64_t T, int K) {
-  return T <= kFusedRows && T * (row_pitch(K) + 16) <= 48 * 1024;
+  return T <= kFusedRows && T * (row_pitch(K) + 16) <= 47 * 1024;
 }
 
 struct LinearLayout {

@@ -124,7 +124,8 @@ __global__ __launch_bounds__(256) void clear_kernel(uint32_t *__restrict__ p, in
 }
 
 // ----------------------------------------------------------------- add_norm
-// n = norm(v) for the row in v (elements past H are zero, and stay zero).
+// v = norm(v) for the row in v (elements past H are zero, and stay zero but for a
+// bias). Three cell rows.
 template <int TPR, int NC>
 __device__ __forceinline__ void norm_row(float (&v)[NC][8], int kind, const float *w,
                                          const float *b, int H, float eps, int lane,
@@ -133,24 +134,40 @@ __device__ __forceinline__ void norm_row(float (&v)[NC][8], int kind, const floa
   if (kind == MOE_W8A8_NORM_NONE) return;
   const float width = (float)H;
   if (kind == MOE_W8A8_NORM_LAYER) {
+    // (the mean as a sum of quotients: it stays in range where the sum would not)
+    const float inv = 1.0f / width;
     float a = 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a += v[i][j];
-    const float mean = G::sum(a, cells) / width;
+      for (int j = 0; j < 8; ++j) a = __builtin_fmaf(v[i][j], inv, a);
+    const float mean = G::sum(a, cells);
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         v[i][j] = (lane + i * TPR) * 8 + j < H ? v[i][j] - mean : 0.0f;
   }
-  float a = 0.0f;
+  auto squares = [&](float *slot) {
+    float a = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NC; ++i)
+    for (int i = 0; i < NC; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a = __builtin_fmaf(v[i][j], v[i][j], a);
-  const float rstd = 1.0f / __builtin_sqrtf(G::sum(a, cells + G::kWaves) / width + eps);
+      for (int j = 0; j < 8; ++j) a = __builtin_fmaf(v[i][j], v[i][j], a);
+    return G::sum(a, slot);
+  };
+  float ms = squares(cells + G::kWaves) / width;
+  // Values past 2^64 have squares past the fp32 range: such a row is taken down
+  // by 2^70 (exactly, but for what is too small to matter) and its eps with it.
+  if (ms > 0x1p127f) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= 0x1p-70f;
+    ms = squares(cells + 2 * G::kWaves) / width;
+    eps = eps * 0x1p-70f * 0x1p-70f;
+  }
+  const float rstd = 1.0f / __builtin_sqrtf(ms + eps);
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = (lane + i * TPR) * 8, rem = H - c;
@@ -175,7 +192,7 @@ template <int TPR, int NC>
 __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void add_norm_kernel(
     const moe_w8a8_add_norm_args a, int64_t T) {
   typedef RowGroup<TPR> G;
-  __shared__ float cells[5][G::kWaves];
+  __shared__ float cells[7][G::kWaves];
   const int lane = threadIdx.x % TPR;
   const int64_t t = (int64_t)blockIdx.x * G::kRows + threadIdx.x / TPR;
   if (t >= T) return;  // as in act_rows_kernel
@@ -223,7 +240,7 @@ __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void add_norm_kernel(
     }
   }
   if (!a.normed && !a.q) return;  // uniform over the grid
-  norm_row<TPR, NC>(v, a.pre_norm, a.pre_weight, a.pre_bias, H, a.eps, lane, cells[2]);
+  norm_row<TPR, NC>(v, a.pre_norm, a.pre_weight, a.pre_bias, H, a.eps, lane, cells[3]);
   if (a.normed) {
     uint16_t *n = a.normed + t * a.ld_normed;
 #pragma unroll
@@ -250,7 +267,7 @@ __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void add_norm_kernel(
       m = umax(m, abs_bits(v[i][j]));
     }
   }
-  m = G::max_bits(m, cells[4]);
+  m = G::max_bits(m, cells[6]);
   const int Kp = row_pitch(H);
   emit_codes<TPR, NC>(v, lane, Kp, m, a.format == MOE_W8A8_FORMAT_FP8, a.q + t * Kp, a.s + t);
 }
