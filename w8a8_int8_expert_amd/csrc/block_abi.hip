@@ -102,11 +102,11 @@ LinearLayout linear_layout(int K, int64_t T) {
   if (T == 0 || fused_rows(T, K)) return L;
   L.q = take((size_t)T * row_pitch(K));
   L.s = take((size_t)T * 4);
-  L.partial = take(T > kStreamRows ? kPartialBytes : 0);
+  L.partial = take(T > kAlwaysStream ? kPartialBytes : 0);
   L.total = o;
   return L;
 }
-// h holds gate and up values (T <= kStreamRows: fp32 [T][packed rows]) or
+// h holds gate and up values (of a streaming product: fp32 [T][packed rows]) or
 // hidden values (fp32 [T][Fp]).
 struct FfnLayout {
   size_t q, s, h, amax, qh, sh, partial, total;
@@ -130,7 +130,7 @@ FfnLayout ffn_layout(int H, int F, int64_t T) {
     L.qh = take((size_t)T * row_pitch(F));
     L.sh = take((size_t)T * 4);
   }
-  L.partial = take(T > kStreamRows ? kPartialBytes : 0);
+  L.partial = take(T > kAlwaysStream ? kPartialBytes : 0);
   L.total = o;
   return L;
 }
@@ -140,7 +140,7 @@ hipError_t product(const StreamIn &in, const int8_t *q, int64_t T,
                    hipStream_t st) {
   const bool gated = w.gated != 0, fp8 = w.format == MOE_W8A8_FORMAT_FP8;
   const int K = w.in_features, Np = packed_rows(w.out_features, gated);
-  if (T <= kStreamRows)
+  if (streams(T, K, Np))
     return launch_linear_stream(in, (int)T, w.w, K, Np, fp8, ep, st);
   return launch_linear_tiled(q, T, w.w, K, Np, gated, fp8, ep, partial, st);
 }
@@ -275,7 +275,7 @@ extern "C" int moe_w8a8_ffn(const moe_w8a8_linear_weights *gu, const moe_w8a8_li
   char *ws = (char *)workspace;
   float *h = (float *)(ws + L.h);
   uint32_t *amax = (uint32_t *)(ws + L.amax);
-  const bool few = T <= kStreamRows;  // else SwiGLU and row maxima in the first product
+  const bool few = streams(T, H, packed_rows(2 * F, true));  // else SwiGLU and row maxima in the first product
 
   Epilogue ep{};
   ep.scale = gu->scale; ep.out = h; ep.out_f32 = 1;

@@ -40,9 +40,23 @@ struct Epilogue {
   uint32_t *amax;  // gated: row max |h| (float bits), or NULL
 };
 
-// Largest batch of the streaming product, and of its form that codes the
-// tokens itself.
-constexpr int kStreamRows = 64;
+// Which product runs. Streaming reads the weights once and every block all
+// tokens; tiles read both several times, but the weights in larger panels, and
+// split K over blocks. Up to 32 tokens streaming is the faster almost
+// everywhere, beyond 64 never; between them it depends on how much there is to
+// read (us, streaming against tiles, INT8): 16 tokens, K 8192, 8192 outputs
+// 13.9, 15.9; 32 tokens, K 4096, 8192 outputs 10.0, 12.0; 64 tokens, K 2048,
+// 4096 outputs 6.2, 9.4; K 4096, 4096 outputs 11.6, 11.6; K 4096, 8192 outputs
+// 13.9, 12.5; K 8192, 4096 outputs 20.4, 13.1; 40 tokens, K 4096, 11000
+// outputs 20.3, 13.5.
+constexpr int kStreamRows = 64;   // most that stream
+constexpr int kAlwaysStream = 32; // fewer always do
+inline bool streams(int64_t T, int K, int Np) {
+  if (T <= kAlwaysStream) return true;
+  if (T > kStreamRows) return false;
+  return K <= 2048 || (K <= 4096 && Np <= 4096);
+}
+// Largest batch whose rows a streaming product codes itself.
 constexpr int kFusedRows = 4;
 // Partial sums of the products that split K over blocks.
 constexpr size_t kPartialBytes = (size_t)32 << 20;

@@ -423,7 +423,16 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const TiledLinear a) {
     float *h = static_cast<float *>(ep.out) + t * ep.ld_out + c8;
     *reinterpret_cast<v4f *>(h) = v4f{v[0], v[1], v[2], v[3]};
     *reinterpret_cast<v4f *>(h + 4) = v4f{v[4], v[5], v[6], v[7]};
-    atomicMax(ep.amax + t, m);
+    // One atomic for the lanes of a row: whole wavefronts of a wide row, runs of
+    // four lanes (a row has a multiple of four) where a wavefront holds several.
+    m = umax(m, (uint32_t)__shfl_xor((int)m, 1, 64));
+    m = umax(m, (uint32_t)__shfl_xor((int)m, 2, 64));
+    if (per % 64 == 0) {
+      m = wave_max_bits(m);
+      if ((threadIdx.x & 63) == 0) atomicMax(ep.amax + t, m);
+    } else if ((threadIdx.x & 3) == 0) {
+      atomicMax(ep.amax + t, m);
+    }
   } else {
     finish_columns<8>(ep, t, c8, v);
   }
@@ -460,15 +469,16 @@ hipError_t join(const TiledLinear &a, bool fp8, hipStream_t st) {
 }
 
 // Tile shape and split of K by estimated time. A stage of 128 k takes a full
-// chip 2.25 us with 256 x 256 tiles, 1.15 with 128 x 256 and 0.5 with 64 x 128
-// (one block per compute unit; two of the last take 0.9 together), measured at
-// K 4096 on MI355X: 69 us for 4096 x 4096 tokens x outputs in 256 tiles of
-// 256 x 256 (128 x 256: 79, 64 x 128: 100), 33 us for 1021 x 4999 in 160 tiles
-// of 128 x 256 (256 x 256: 53, 64 x 128: 40), 18 us for 512 x 4096 in 256 tiles
-// of 64 x 128 (128 x 256: 31). A launch that leaves most compute units idle
-// splits K where that saves more than the second launch (6 us) and the partial
-// sums (8 bytes each at 4 TB/s) cost: 128 x 4096 tokens x outputs, K 4096: 17.0
-// us in 64 tiles, 14.4 with K in three.
+// chip 2.1 us with 256 x 256 tiles, 1.1 with 128 x 256 and 0.4 with 64 x 128
+// (one block per compute unit, 0.28 while most are idle; two blocks a unit take
+// 0.8 together). Measured on MI355X, INT8 codes, us with 256 x 256, 128 x 256
+// and 64 x 128 tiles (tokens, K, outputs):
+//   512, 4096, 6144: 43, 30, 24     1500, 4096, 4096: 45, 35, 40
+//   3000, 4096, 4096: 55, 67, 74    8192, 512, 8192: 66, 75, 84
+// A launch that leaves compute units idle splits K where that saves more than
+// the second launch (1.5 us) and the partial sums (2.6 us a million) cost: 100,
+// 8192, 1024 takes 22 us in 16 tiles, 12 with K in four; 64, 8192, 4096: 12.8
+// with K in four, 16.0 in two, 14.4 in eight.
 template <bool kGated>
 hipError_t pick(TiledLinear a, bool fp8, hipStream_t st) {
   auto tiles = [&](int bm, int bn) {
@@ -476,17 +486,18 @@ hipError_t pick(TiledLinear a, bool fp8, hipStream_t st) {
   };
   const int D = a.Kp >> 7;
   const int64_t t0 = tiles(256, 256), t1 = tiles(128, 256), t2 = tiles(64, 128);
-  const double c0 = (double)((t0 + 255) / 256) * 2.25, c1 = (double)((t1 + 255) / 256) * 1.15;
-  const double c2 = t2 <= 256 ? 0.5 : (double)((t2 + 511) / 512) * 0.9;
+  const double c0 = (double)((t0 + 255) / 256) * 2.1, c1 = (double)((t1 + 255) / 256) * 1.1;
+  auto stage = [](int64_t n) { return 0.28 + 0.12 * (n < 192 ? (double)n / 192 : 1.0); };
+  const double c2 = t2 <= 256 ? stage(t2) : (double)((t2 + 511) / 512) * 0.8;
   a.split = 1;
   if (c0 <= c1 && c0 <= c2) return run<4, 2, 2, 4, 2, kGated, false>(a, fp8, st);
   if (c1 <= c2) return run<2, 4, 2, 2, 2, kGated, false>(a, fp8, st);
-  double best = 0.0;
-  for (int s = 2; s <= 4 && t2 * s <= 256 && D >= 4 * s; ++s) {
+  double best = D * c2;
+  for (int s = 2; s <= 8 && t2 * s <= 256 && D >= 2 * s; ++s) {
     const double sums = (double)s * (double)a.T * a.Np;
-    const double gain = 0.5 * D * (1.0 - 1.0 / s) - 6.0 - sums * 8.0 / 4e6;
-    if (gain > best && sums * 4.0 <= (double)kPartialBytes) {
-      best = gain;
+    const double us = (double)D / s * stage(t2 * s) + 1.5 + sums * 2.6e-6;
+    if (us < best && sums * 4.0 <= (double)kPartialBytes) {
+      best = us;
       a.split = s;
     }
   }
