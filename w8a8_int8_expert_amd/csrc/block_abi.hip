@@ -86,10 +86,15 @@ Epilogue epilogue(const moe_w8a8_linear_weights &w, const moe_w8a8_result &r) {
   return e;
 }
 
-// The streaming product codes its tokens itself: few rows, and they fit 64 KB
-// of LDS beside its partial sums (16 KB).
-bool fused_rows(int64_t T, int K) {
-  return T <= kFusedRows && T * (row_pitch(K) + 16) <= 47 * 1024;
+// Rows that a streaming product codes itself, every block over again: tokens,
+// and the hidden rows of a feed-forward block (twice the values to read, and
+// SwiGLU to compute).
+constexpr int kFusedTokens = 16384, kFusedHidden = 8192;
+bool fused_tokens(int64_t T, int K) {
+  return T <= kFusedRows && T * row_pitch(K) <= kFusedTokens;
+}
+bool fused_hidden(int64_t T, int F) {
+  return T <= kFusedRows && T * row_pitch(F) <= kFusedHidden;
 }
 
 struct LinearLayout {
@@ -99,7 +104,7 @@ LinearLayout linear_layout(int K, int64_t T) {
   LinearLayout L{};
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += up256(bytes); return at; };
-  if (T == 0 || fused_rows(T, K)) return L;
+  if (T == 0 || fused_tokens(T, K)) return L;
   L.q = take((size_t)T * row_pitch(K));
   L.s = take((size_t)T * 4);
   L.partial = take(T > kAlwaysStream ? kPartialBytes : 0);
@@ -121,11 +126,11 @@ FfnLayout ffn_layout(int H, int F, int64_t T) {
   const size_t gu = (size_t)few * packed_rows(2 * F, true) * 4;
   const size_t hid = (size_t)T * row_pitch(F) * 4;
   L.h = take(gu > hid ? gu : hid);
-  if (!fused_rows(T, H)) {
+  if (!fused_tokens(T, H)) {
     L.q = take((size_t)T * row_pitch(H));
     L.s = take((size_t)T * 4);
   }
-  if (!fused_rows(T, F)) {
+  if (!fused_hidden(T, F)) {
     L.amax = take((size_t)T * 4);
     L.qh = take((size_t)T * row_pitch(F));
     L.sh = take((size_t)T * 4);
@@ -234,7 +239,7 @@ extern "C" int moe_w8a8_linear(const moe_w8a8_linear_weights *w, const moe_w8a8_
   char *ws = (char *)workspace;
   Epilogue ep = epilogue(*w, *res);
   StreamIn in{};
-  if (act->x && fused_rows(T, K)) {
+  if (act->x && fused_tokens(T, K)) {
     in.x = act->x; in.ld = act->ld_x; in.inv = w->inv_smooth;
   } else if (act->x) {
     int8_t *q = (int8_t *)(ws + L.q);
@@ -284,7 +289,7 @@ extern "C" int moe_w8a8_ffn(const moe_w8a8_linear_weights *gu, const moe_w8a8_li
   ep.ld_out = few ? Np : row_pitch(F);
   ep.amax = amax;
   StreamIn in{};
-  if (act->x && fused_rows(T, H)) {
+  if (act->x && fused_tokens(T, H)) {
     in.x = act->x; in.ld = act->ld_x; in.inv = gu->inv_smooth;
   } else if (act->x) {
     int8_t *q = (int8_t *)(ws + L.q);
@@ -300,7 +305,7 @@ extern "C" int moe_w8a8_ffn(const moe_w8a8_linear_weights *gu, const moe_w8a8_li
 
   Epilogue ed = epilogue(*dn, *res);
   StreamIn hin{};
-  if (fused_rows(T, F)) {
+  if (fused_hidden(T, F)) {
     hin.h = h; hin.ld = Np;
   } else {
     int8_t *qh = (int8_t *)(ws + L.qh);

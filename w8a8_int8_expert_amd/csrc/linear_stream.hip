@@ -82,8 +82,13 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs 
     auto read = [&](int t, int c, float *o) {
       const int rem = a.K - c;
       if constexpr (kSrc == kTokens) {
+        if (rem <= 0) {  // most threads of a narrow row: no element loads to skip
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+          return;
+        }
         load8(a.in.x + t * a.in.ld + c, rem, o);
-        if (a.in.inv && rem > 0) {
+        if (a.in.inv) {
           float f[8];
           load8(a.in.inv + c, rem, f);
 #pragma unroll
@@ -99,6 +104,7 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs 
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < kKeep; ++i) {
+        if (i * kStep >= a.Kp) break;  // uniform
         read(t, threadIdx.x * 8 + i * kStep, v[t][i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = umax(m, abs_bits(v[t][i][j]));
@@ -128,7 +134,8 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs 
               v2i{(int)row_codes4(o, rc, kF8), (int)row_codes4(o + 4, rc, kF8)};
       };
 #pragma unroll
-      for (int i = 0; i < kKeep; ++i) put(threadIdx.x * 8 + i * kStep, v[t][i]);
+      for (int i = 0; i < kKeep; ++i)
+        if (i * kStep < a.Kp) put(threadIdx.x * 8 + i * kStep, v[t][i]);
       for (int c = threadIdx.x * 8 + kKeep * kStep; c < a.Kp; c += kStep) {
         float o[8];
         read(t, c, o);

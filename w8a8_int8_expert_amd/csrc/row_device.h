@@ -124,6 +124,11 @@ __device__ __forceinline__ uint32_t wave_max_bits(uint32_t m) {
 // them exist) from a row of gate and up values in packed order: alternating
 // runs of 32.
 __device__ __forceinline__ void hidden8(const float *gu, int c, int rem, float *o) {
+  if (rem <= 0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+    return;
+  }
   float u[8];
   const float *p = gu + c / 32 * 64 + c % 32;
   load8(p, rem, o);
