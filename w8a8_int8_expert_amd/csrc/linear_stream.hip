@@ -40,6 +40,16 @@ struct StreamArgs {
 template <bool kF8> struct Acc16v { typedef v4i T; };
 template <> struct Acc16v<true> { typedef v4f T; };
 
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+// Eight e4m3 codes as bf16 (exact: three mantissa bits, exponents of -9 to 8).
+__device__ __forceinline__ v8bf codes_bf16(int lo, int hi) {
+  const auto a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+  const auto b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  const auto c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+  const auto d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
 template <int RT, int NPW, int W, int U, bool kF8, int kSrc>
 __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs a) {
   typedef typename Acc16v<kF8>::T Acc;
@@ -171,18 +181,36 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs 
   for (int i = 0; i < NPW; ++i)
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) acc[i][rt] = Acc{0, 0, 0, 0};
+  // FP8 codes are multiplied as bf16, into which they convert exactly: the FP8
+  // instruction drops what lies 13 bits below the largest of eight products
+  // (sums 3e-5 off, against 1e-7), and the matrix cores wait for memory here.
   auto multiply = [&](int u) {
+    if constexpr (kF8) {
 #pragma unroll
-    for (int i = 0; i < NPW; ++i)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        if constexpr (kF8) {
-          acc[i][rt] = mfma16f8(af[u][i][0], af[u][i][1], bf[u][rt][0], bf[u][rt][1], acc[i][rt]);
-        } else {
-          acc[i][rt] = mfma16(af[u][i][0], bf[u][rt][0], acc[i][rt]);
-          acc[i][rt] = mfma16(af[u][i][1], bf[u][rt][1], acc[i][rt]);
+        for (int e = 0; e < 2; ++e) {
+          v8bf b[RT];
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+            b[rt] = codes_bf16(bf[u][rt][h][2 * e], bf[u][rt][h][2 * e + 1]);
+#pragma unroll
+          for (int i = 0; i < NPW; ++i) {
+            const v8bf w = codes_bf16(af[u][i][h][2 * e], af[u][i][h][2 * e + 1]);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+              acc[i][rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, b[rt], acc[i][rt], 0, 0, 0);
+          }
         }
-      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < NPW; ++i)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+            acc[i][rt] = mfma16(af[u][i][h], bf[u][rt][h], acc[i][rt]);
+    }
   };
   int s = 0;
   for (; s + 2 * U <= n; s += U) {
