@@ -208,3 +208,39 @@ def test_binding_refusals():
                                                                       inv_smooth=w[:3])):
         with pytest.raises(m.MoEW8A8Error):
             m.add_norm(**{"y": x, **kw})
+
+
+def test_header_from_c(tmp_path):
+    """The block operators' declarations link from a C99 program, which gets the
+    sizes the binding gets and the refusal of a NULL argument."""
+    import shutil
+    import subprocess
+    if shutil.which("gcc") is None:
+        pytest.skip("no gcc")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    libdir = os.path.dirname(m.LIB_PATH)
+    src = tmp_path / "client.c"
+    src.write_text(
+        "#include <stdio.h>\n#include \"moe_w8a8.h\"\n"
+        "int main(void) {\n"
+        "  printf(\"%lld %zu %lld %zu %zu\\n\", (long long)moe_w8a8_row_pitch(300),\n"
+        "         moe_w8a8_linear_codes_bytes(70, 300, 1),\n"
+        "         (long long)moe_w8a8_linear_scales(70, 1),\n"
+        "         moe_w8a8_linear_workspace_size(70, 300, 90),\n"
+        "         moe_w8a8_ffn_workspace_size(300, 35, 70, 90));\n"
+        "  printf(\"%d %d %d %d %d %d\\n\", moe_w8a8_linear_quantise(0, 0, 0, 0, 0, 0),\n"
+        "         moe_w8a8_linear_pack(0, 0, 0, 0, 0),\n"
+        "         moe_w8a8_act_quant(8, 0, 0, 8, 1, 0, 0, 0, 0),\n"
+        "         moe_w8a8_linear(0, 0, 1, 0, 0, 0, 0),\n"
+        "         moe_w8a8_ffn(0, 0, 0, 1, 0, 0, 0, 0), moe_w8a8_add_norm(0, 1, 0));\n"
+        "  return 0;\n}\n")
+    exe = tmp_path / "client"
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-pedantic", "-Werror",
+                    "-I", os.path.join(root, "include"), str(src), "-L", libdir, "-lmoe_w8a8",
+                    "-Wl,-rpath," + libdir, "-o", str(exe)], check=True, timeout=120)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, check=True, timeout=60)
+    sizes, codes = r.stdout.splitlines()
+    assert [int(v) for v in sizes.split()] == [
+        384, m.moe_w8a8_linear_codes_bytes(70, 300, 1), m.moe_w8a8_linear_scales(70, 1),
+        m.moe_w8a8_linear_workspace_size(70, 300, 90), m.moe_w8a8_ffn_workspace_size(300, 35, 70, 90)]
+    assert [int(v) for v in codes.split()] == [INV] * 6

@@ -158,7 +158,16 @@ class _Weights:
 
 
 class _Product:
-    """What the two products share: their operands and their result."""
+    """What the two products share: their operands, their workspace's size (a
+    function of the number of tokens, asked for once each) and their result."""
+
+    def _workspace(self, T):
+        n = self._sizes.get(T)
+        if n is None:
+            if len(self._sizes) >= 4096:
+                self._sizes.clear()
+            n = self._sizes[T] = self._size(T)
+        return n, torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
 
     def _operands(self, x, codes, K, N, add, gate, out, out_dtype):
         dev = self.device
@@ -203,6 +212,10 @@ class W8A8Linear(_Product):
         self.in_features, self.out_features = int(in_features), int(out_features)
         self.fp8, self.device = bool(fp8), _device(device)
         self._w = _Weights(self.in_features, self.out_features, self.fp8, False, self.device)
+        self._sizes = {}
+
+    def _size(self, T):
+        return _m.moe_w8a8_linear_workspace_size(self.out_features, self.in_features, T)
 
     def quantise(self, weight, smooth=None, bias=None):
         """weight: fp32 or bf16 [N][K]. smooth: SmoothQuant scales s fp32 [K]
@@ -223,8 +236,7 @@ class W8A8Linear(_Product):
         give them. gate fp32 [T]; add bf16 [T][N] (may be out itself)."""
         T, act, res, out = self._operands(x, codes, self.in_features, self.out_features, add,
                                           gate, out, out_dtype)
-        n = _m._lib.moe_w8a8_linear_workspace_size(self.out_features, self.in_features, T)
-        ws = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+        n, ws = self._workspace(T)
         _call("moe_w8a8_linear", self.device, self._w.ref, ctypes.byref(act), T,
               ctypes.byref(res), ws.data_ptr() if n else None, n)
         return out
@@ -244,6 +256,10 @@ class W8A8FFN(_Product):
         self.fp8, self.device = bool(fp8), _device(device)
         self._gu = _Weights(self.hidden, 2 * self.ffn, self.fp8, True, self.device)
         self._dn = _Weights(self.ffn, self.out_features, self.fp8, False, self.device)
+        self._sizes = {}
+
+    def _size(self, T):
+        return _m.moe_w8a8_ffn_workspace_size(self.hidden, self.ffn, self.out_features, T)
 
     def quantise(self, w_gate_up, w_down, smooth=None, bias=None):
         """w_gate_up: fp32 or bf16 [2F][H], gate rows then up rows; w_down
@@ -267,8 +283,7 @@ class W8A8FFN(_Product):
         As a shared expert: ffn.forward(x, add=moe.forward(x, ...), gate=g)."""
         T, act, res, out = self._operands(x, codes, self.hidden, self.out_features, add, gate,
                                           out, out_dtype)
-        n = _m._lib.moe_w8a8_ffn_workspace_size(self.hidden, self.ffn, self.out_features, T)
-        ws = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+        n, ws = self._workspace(T)
         _call("moe_w8a8_ffn", self.device, self._gu.ref, self._dn.ref, ctypes.byref(act), T,
               ctypes.byref(res), ws.data_ptr() if n else None, n)
         return out
@@ -354,10 +369,12 @@ def add_norm(y, residual=None, norm="rms", weight=None, bias=None, eps: float = 
     a = _m.moe_w8a8_add_norm_args(
         H, _NORMS[norm], _NORMS[post_norm], 1 if rtype == _F32 else 0, _FORMATS.get(codes, 0),
         eps, residual_scale, block_scale, p_y, ld_y, p_res, ld_res, p_out, ld_out,
-        _vector(post_weight, "post_weight", H, dev), _vector(post_bias, "post_bias", H, dev),
-        _vector(weight, "weight", H, dev), _vector(bias, "bias", H, dev), p_token, p_rows,
-        ld_gate, group, p_norm, ld_norm,
-        None if codes is None else _vector(inv_smooth, "inv_smooth", H, dev),
+        None if post_weight is None else _vector(post_weight, "post_weight", H, dev),
+        None if post_bias is None else _vector(post_bias, "post_bias", H, dev),
+        None if weight is None else _vector(weight, "weight", H, dev),
+        None if bias is None else _vector(bias, "bias", H, dev), p_token, p_rows, ld_gate, group,
+        p_norm, ld_norm,
+        None if codes is None or inv_smooth is None else _vector(inv_smooth, "inv_smooth", H, dev),
         None if q is None else q.data_ptr(), None if s is None else s.data_ptr())
     _call("moe_w8a8_add_norm", dev, ctypes.byref(a), T)
     return AddNorm(residual_out, normed, q, s)
