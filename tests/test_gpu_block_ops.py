@@ -151,7 +151,8 @@ def test_weights_packed(lib, N, K, fp8, gated):
 # ------------------------------------------------------------------- linear
 LINEAR = [
     # T, K, N
-    (1, 1, 1), (1, 64, 16), (1, 4096, 100), (2, 129, 17), (3, 1000, 33), (4, 12288, 40), (1, 48000, 33), (3, 16000, 35),
+    (1, 1, 1), (1, 64, 16), (1, 4096, 100), (2, 129, 17), (3, 1000, 33), (4, 12288, 40), (1, 16384, 33), (1, 48000, 33), (3, 5400, 35), (40, 5000, 64), (50, 2100, 4200),
+    (64, 4100, 1000), (2, 64, 1 << 20), (70, 9000, 30),
     (4, 300, 257), (5, 127, 15), (15, 512, 48), (16, 2048, 31), (17, 128, 16), (31, 640, 130),
     (33, 4097, 64), (48, 256, 333), (63, 1024, 5), (64, 1100, 96), (65, 128, 128), (65, 1, 1),
     (100, 2000, 300), (128, 512, 129), (129, 384, 255), (200, 4096, 500), (256, 1024, 1024),
@@ -185,7 +186,7 @@ def test_linear(lib, T, K, N, fp8):
 
 
 @pytest.mark.parametrize("T,K,N", [(1, 256, 70), (4, 100, 33), (20, 300, 130), (64, 128, 48),
-                                   (70, 256, 100), (300, 512, 257), (4100, 128, 4200)])
+                                   (70, 256, 100), (70, 2500, 100), (300, 512, 257), (4100, 128, 4200)])
 def test_linear_gate_add_strides(lib, T, K, N):
     """Row gate, add (also in place), strided x, add and out at odd offsets;
     what lies beside and behind the output's rows stays as it was."""
@@ -275,7 +276,8 @@ def test_linear_offsets_past_32_bits(lib):
 # ---------------------------------------------------------------------- ffn
 FFN = [(1, 64, 32), (1, 1, 1), (1, 4096, 512), (2, 300, 77), (4, 130, 33), (4, 8192, 100),
        (5, 128, 64), (16, 256, 100), (17, 512, 31), (33, 200, 130), (64, 1000, 96), (65, 128, 64),
-       (100, 300, 257), (256, 512, 500), (700, 256, 1000), (2100, 128, 2100)]
+       (100, 300, 257), (256, 512, 500), (700, 256, 1000), (2100, 128, 2100),
+       (40, 5000, 70), (70, 2500, 100), (66, 2500, 1000), (2, 64, 33000), (3, 100, 1300)]
 
 
 def ffn_weights(H, F, N, fp8, seed, small=False):
@@ -494,6 +496,21 @@ def test_norm_of_the_largest_values(lib, kind):
     _, _, n, en = add_norm64(y, None, c)
     R.check(o.normed, n, en + R.half_step(BF) * (n.abs() + en) + 1e-44, kind)
     assert bool(torch.isfinite(o.scales).all())
+
+
+def test_many_rows(lib):
+    """More rows than 2^16, each right: the first, the last and some between."""
+    T, H = 200003, 72
+    y = torch.randn(T, H, generator=torch.Generator().manual_seed(1)).to(BF)
+    w = vec(H, 2)
+    o = lib.add_norm(y.cuda(), y.cuda(), weight=w.cuda(), codes="int8")
+    pick = torch.tensor([0, 1, 65535, 65536, 131071, T - 2, T - 1])
+    c = dict(norm="rms", post="none", eps=1e-6, bs=1.0, rs=1.0, w=w)
+    _, _, n, en = add_norm64(y[pick], y[pick], c)
+    R.check(o.normed[pick.cuda()], n, en + R.half_step(BF) * (n.abs() + en) + 1e-44, "n")
+    q, s = lib.act_quant(y.cuda())
+    want, ws = R.row_codes(y.float(), False)
+    assert torch.equal(q.cpu().float()[:, :H], want) and torch.equal(s.cpu(), ws)
 
 
 def test_add_norm_in_place_and_parts(lib):
