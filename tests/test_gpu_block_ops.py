@@ -686,3 +686,25 @@ def test_empty_batches(lib):
     assert ffn(torch.empty(0, 64, dtype=BF, device="cuda")).shape == (0, 64)
     o = lib.add_norm(x, x, codes="fp8")
     assert o.normed.shape == (0, 70) and o.codes.shape == (0, 128)
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("H", [72, 900, 5000])
+def test_norm_of_the_smallest_values(lib, kind, H):
+    """Without an eps (or with one as small) a row whose squares fall below the
+    fp32 range normalises as any other; a row of zeros has no norm (0 / 0)."""
+    y = tokens(9, H, 5).float()
+    for t, p in ((1, -40), (2, -50), (3, -64), (4, -75), (5, -100), (6, -120)):
+        y[t] *= 2.0 ** p
+    y[7] = 0
+    y[7, 3] = 2.0 ** -133
+    y[8] = 0
+    y = y.to(BF)
+    for eps in (0.0, 2.0 ** -120):
+        o = lib.add_norm(y.cuda(), None, norm=kind, eps=eps, codes="int8")
+        c = dict(norm=kind, post="none", eps=eps, bs=1.0, rs=1.0)
+        _, _, n, en = add_norm64(y[:8], None, c)
+        R.check(o.normed[:8], n, en + R.half_step(BF) * (n.abs() + en) + 1e-44, kind)
+        assert bool(torch.isfinite(o.scales[:8]).all())
+        last = o.normed[8]
+        assert bool(torch.isnan(last).all()) if eps == 0.0 else not bool(last.any())

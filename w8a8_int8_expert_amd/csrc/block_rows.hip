@@ -133,7 +133,7 @@ __device__ __forceinline__ void norm_row(float (&v)[NC][8], int kind, const floa
   typedef RowGroup<TPR> G;
   if (kind == MOE_W8A8_NORM_NONE) return;
   const float width = (float)H;
-  if (kind == MOE_W8A8_NORM_LAYER) {
+  auto centre = [&]() {
     // (the mean as a sum of quotients: it stays in range where the sum would not)
     const float inv = 1.0f / width;
     float a = 0.0f;
@@ -147,7 +147,8 @@ __device__ __forceinline__ void norm_row(float (&v)[NC][8], int kind, const floa
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         v[i][j] = (lane + i * TPR) * 8 + j < H ? v[i][j] - mean : 0.0f;
-  }
+  };
+  if (kind == MOE_W8A8_NORM_LAYER) centre();
   auto squares = [&](float *slot) {
     float a = 0.0f;
 #pragma unroll
@@ -157,15 +158,21 @@ __device__ __forceinline__ void norm_row(float (&v)[NC][8], int kind, const floa
     return G::sum(a, slot);
   };
   float ms = squares(cells + G::kWaves) / width;
-  // Values past 2^64 have squares past the fp32 range: such a row is taken down
-  // by 2^70 (exactly, but for what is too small to matter) and its eps with it.
-  if (ms > 0x1p127f) {
+  // Squares that leave the fp32 range: a row of values past 2^64 is taken down by
+  // 2^70, one whose squares (and eps) lie below 2^-90 is taken up by 2^100, exactly
+  // but for what is too small to matter, and eps with it. The mean of such a small
+  // row may have lost bits to a subnormal: what that left is taken off again (its
+  // cells are free: every thread has read them before the barrier since).
+  const bool large = ms > 0x1p127f;
+  if (large || ms + eps < 0x1p-90f) {
+    const float f = large ? 0x1p-70f : 0x1p100f;
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= 0x1p-70f;
+      for (int j = 0; j < 8; ++j) v[i][j] *= f;
+    if (kind == MOE_W8A8_NORM_LAYER && !large) centre();
     ms = squares(cells + 2 * G::kWaves) / width;
-    eps = eps * 0x1p-70f * 0x1p-70f;
+    eps = eps * f * f;
   }
   const float rstd = 1.0f / __builtin_sqrtf(ms + eps);
 #pragma unroll
