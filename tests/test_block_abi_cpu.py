@@ -244,3 +244,19 @@ def test_header_from_c(tmp_path):
         384, m.moe_w8a8_linear_codes_bytes(70, 300, 1), m.moe_w8a8_linear_scales(70, 1),
         m.moe_w8a8_linear_workspace_size(70, 300, 90), m.moe_w8a8_ffn_workspace_size(300, 35, 70, 90)]
     assert [int(v) for v in codes.split()] == [INV] * 6
+
+
+def test_codes_of_the_other_format_are_refused():
+    """INT8 token codes given to an FP8 product would be read as e4m3 bytes."""
+    T = 5
+    s = torch.zeros(T)
+    i8 = torch.zeros(T, 128, dtype=torch.int8)
+    for fp8 in (False, True):
+        right, wrong = (i8.view(torch.float8_e4m3fn), i8) if fp8 else \
+            (i8, i8.view(torch.float8_e4m3fn))
+        for op in (m.W8A8Linear(70, 30, device="cpu", fp8=fp8),
+                   m.W8A8FFN(70, 30, device="cpu", fp8=fp8)):
+            with pytest.raises(m.MoEW8A8Error, match="codes must be"):
+                op.forward(codes=(wrong, s))
+            with pytest.raises(m.MoEW8A8Error, match="GPU"):   # nothing else is wrong
+                op.forward(codes=(right, s))

@@ -90,10 +90,6 @@ def _vector(t, name, n, device):
     return t.data_ptr()
 
 
-def _code_types(fp8):
-    return (_E4M3, _I8) if fp8 else (_I8,)
-
-
 def _empty_codes(T, K, fp8, device):
     if not 1 <= K <= 65536:
         _fail("unsupported width %d" % K)
@@ -152,7 +148,8 @@ class _Weights:
               ld, _vector(smooth, "smooth", self.K, self.device))
 
     def load(self, q, s):
-        p, ld = _rows(q, "codes", _code_types(self.fp8), self.N, self.K, self.device)
+        types = (_E4M3, _I8) if self.fp8 else (_I8,)  # int8: e4m3 bytes, as the layer takes them
+        p, ld = _rows(q, "codes", types, self.N, self.K, self.device)
         _call("moe_w8a8_linear_pack", self.device, self.ref, p, ld,
               _vector(s, "scales", self.N, self.device))
 
@@ -182,7 +179,7 @@ class _Product:
             act.x, act.ld_x = _rows(x, "x", _ONLY_BF16, T, K, dev)
         else:
             pitch = (K + 127) // 128 * 128
-            act.q, ld = _rows(first, "codes", _code_types(self.fp8), T, pitch, dev)
+            act.q, ld = _rows(first, "codes", (_E4M3,) if self.fp8 else (_I8,), T, pitch, dev)
             if ld != pitch:
                 _fail("codes must be contiguous")
             act.s = _vector(codes[1], "code scales", T, dev)
@@ -224,8 +221,9 @@ class W8A8Linear(_Product):
         self._w.vectors(None if smooth is None else 1.0 / smooth, bias)
 
     def load_quantized(self, q, s, inv_smooth=None, bias=None):
-        """Codes [N][K] (int8, or float8_e4m3fn) quantised elsewhere and their
-        scales fp32 [N]; inv_smooth fp32 [K] multiplies the tokens."""
+        """Codes [N][K] (int8; with fp8 float8_e4m3fn, or its bytes as int8)
+        quantised elsewhere and their scales fp32 [N]; inv_smooth fp32 [K]
+        multiplies the tokens."""
         self._w.load(q, s)
         self._w.vectors(inv_smooth, bias)
 
@@ -233,7 +231,7 @@ class W8A8Linear(_Product):
                 out_dtype: Optional["torch.dtype"] = None):  # noqa: F821
         """out = gate[:, None] * (x . W^T + bias) + add, rounded once to bf16
         (or fp32). x: bf16 [T][K], or codes=(q, s) as act_quant and add_norm
-        give them. gate fp32 [T]; add bf16 [T][N] (may be out itself)."""
+        give them in the weights' format. gate fp32 [T]; add bf16 [T][N] (may be out itself)."""
         T, act, res, out = self._operands(x, codes, self.in_features, self.out_features, add,
                                           gate, out, out_dtype)
         n, ws = self._workspace(T)
