@@ -708,3 +708,31 @@ def test_norm_of_the_smallest_values(lib, kind, H):
         assert bool(torch.isfinite(o.scales[:8]).all())
         last = o.normed[8]
         assert bool(torch.isnan(last).all()) if eps == 0.0 else not bool(last.any())
+
+
+def test_refused_weights_change_nothing(lib):
+    """A load that is refused for its last operand leaves what was loaded."""
+    H, F, N, T = 72, 40, 30, 3
+    x = tokens(T, H, 1).cuda()
+    r = lambda *s: torch.randn(*s, device="cuda")  # noqa: E731
+    lin = lib.W8A8Linear(H, N)
+    lin.quantise(r(N, H), vec(H, 1).cuda(), vec(N, 2).cuda())
+    ffn = lib.W8A8FFN(H, F, out_features=N)
+    ffn.quantise(r(2 * F, H), r(N, F), vec(H, 1).cuda(), vec(N, 2).cuda())
+    want = lin(x), ffn(x)
+    i8 = lambda *s: torch.ones(*s, dtype=torch.int8, device="cuda")  # noqa: E731
+    one = lambda n: torch.ones(n, device="cuda")  # noqa: E731
+    for call in (lambda: lin.quantise(r(N, H) * 2, bias=one(N + 1)),
+                 lambda: lin.quantise(r(N, H) * 2, smooth=one(H + 1)),
+                 lambda: lin.load_quantized(i8(N, H), one(N), bias=one(N + 1)),
+                 lambda: lin.load_quantized(i8(N, H), one(N), inv_smooth=one(H).double()),
+                 lambda: lin.load_quantized(i8(N, H), None),
+                 lambda: ffn.quantise(r(2 * F, H) * 2, r(N, F + 1)),
+                 lambda: ffn.quantise(r(2 * F, H) * 2, r(N, F), bias=one(N + 1)),
+                 lambda: ffn.load_quantized(i8(2 * F, H), one(2 * F), i8(N, F), one(N + 1)),
+                 lambda: ffn.load_quantized(i8(2 * F, H), one(2 * F), i8(N, F), None),
+                 lambda: ffn.load_quantized(i8(2 * F, H), one(2 * F), i8(N, F), one(N),
+                                            bias=one(N + 1))):
+        with pytest.raises(lib.MoEW8A8Error):
+            call()
+        assert torch.equal(lin(x), want[0]) and torch.equal(ffn(x), want[1])

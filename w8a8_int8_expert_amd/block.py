@@ -136,22 +136,38 @@ class _Weights:
     def vectors(self, inv_smooth, bias):
         """Copy the two optional vectors in; None turns one off."""
         for name, t, n in (("inv_smooth", inv_smooth, self.K), ("bias", bias, self.N)):
-            _vector(t, name, n, self.device)
             own = getattr(self, name)
             if t is not None:
                 own.copy_(t.detach().reshape(n))
             setattr(self.struct, name, None if t is None else own.data_ptr())
 
-    def quantise(self, w, smooth):
-        p, ld = _rows(w, "weight", (_BF16, _F32), self.N, self.K, self.device)
-        _call("moe_w8a8_linear_quantise", self.device, self.ref, p, 1 if w.dtype == _F32 else 0,
-              ld, _vector(smooth, "smooth", self.K, self.device))
+    # The checks stand apart, so that a call that has several things to load
+    # refuses before it has changed any of them.
+    def check_source(self, w, smooth, bias):
+        _vector(bias, "bias", self.N, self.device)
+        return (*_rows(w, "weight", (_BF16, _F32), self.N, self.K, self.device),
+                _vector(smooth, "smooth", self.K, self.device))
 
-    def load(self, q, s):
+    def quantise(self, w, smooth, bias=None):
+        p, ld, ps = self.check_source(w, smooth, bias)
+        _call("moe_w8a8_linear_quantise", self.device, self.ref, p, 1 if w.dtype == _F32 else 0,
+              ld, ps)
+        self.vectors(None if smooth is None else 1.0 / smooth, bias)
+
+    def check_codes(self, q, s, inv_smooth, bias):
+        _vector(bias, "bias", self.N, self.device)
+        _vector(inv_smooth, "inv_smooth", self.K, self.device)
         types = (_E4M3, _I8) if self.fp8 else (_I8,)  # int8: e4m3 bytes, as the layer takes them
         p, ld = _rows(q, "codes", types, self.N, self.K, self.device)
-        _call("moe_w8a8_linear_pack", self.device, self.ref, p, ld,
-              _vector(s, "scales", self.N, self.device))
+        ps = _vector(s, "scales", self.N, self.device)
+        if ps is None:
+            _fail("codes come with their scales")
+        return p, ld, ps
+
+    def load(self, q, s, inv_smooth=None, bias=None):
+        p, ld, ps = self.check_codes(q, s, inv_smooth, bias)
+        _call("moe_w8a8_linear_pack", self.device, self.ref, p, ld, ps)
+        self.vectors(inv_smooth, bias)
 
 
 class _Product:
@@ -217,15 +233,13 @@ class W8A8Linear(_Product):
     def quantise(self, weight, smooth=None, bias=None):
         """weight: fp32 or bf16 [N][K]. smooth: SmoothQuant scales s fp32 [K]
         (the weight's columns are multiplied by s, the tokens by 1/s)."""
-        self._w.quantise(weight, smooth)
-        self._w.vectors(None if smooth is None else 1.0 / smooth, bias)
+        self._w.quantise(weight, smooth, bias)
 
     def load_quantized(self, q, s, inv_smooth=None, bias=None):
         """Codes [N][K] (int8; with fp8 float8_e4m3fn, or its bytes as int8)
         quantised elsewhere and their scales fp32 [N]; inv_smooth fp32 [K]
         multiplies the tokens."""
-        self._w.load(q, s)
-        self._w.vectors(inv_smooth, bias)
+        self._w.load(q, s, inv_smooth, bias)
 
     def forward(self, x=None, codes=None, add=None, gate=None, out=None,
                 out_dtype: Optional["torch.dtype"] = None):  # noqa: F821
@@ -262,18 +276,16 @@ class W8A8FFN(_Product):
     def quantise(self, w_gate_up, w_down, smooth=None, bias=None):
         """w_gate_up: fp32 or bf16 [2F][H], gate rows then up rows; w_down
         [N][F]; smooth fp32 [H]; bias fp32 [N] of the down projection."""
+        self._dn.check_source(w_down, None, bias)
         self._gu.quantise(w_gate_up, smooth)
-        self._gu.vectors(None if smooth is None else 1.0 / smooth, None)
-        self._dn.quantise(w_down, None)
-        self._dn.vectors(None, bias)
+        self._dn.quantise(w_down, None, bias)
 
     def load_quantized(self, q_gate_up, s_gate_up, q_down, s_down, inv_smooth=None, bias=None):
         """Codes [2F][H] (gate rows, then up rows) and [N][F] quantised
         elsewhere, their scales fp32 [2F] and [N]."""
-        self._gu.load(q_gate_up, s_gate_up)
-        self._gu.vectors(inv_smooth, None)
-        self._dn.load(q_down, s_down)
-        self._dn.vectors(None, bias)
+        self._dn.check_codes(q_down, s_down, None, bias)
+        self._gu.load(q_gate_up, s_gate_up, inv_smooth)
+        self._dn.load(q_down, s_down, None, bias)
 
     def forward(self, x=None, codes=None, add=None, gate=None, out=None,
                 out_dtype: Optional["torch.dtype"] = None):  # noqa: F821
