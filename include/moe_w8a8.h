@@ -374,7 +374,8 @@ int moe_w8a8_pack(int64_t count, int32_t N, int32_t K, const int8_t *src, int8_t
  * in elements, at least the row's width and at most 2^26. bf16 and fp32 rows
  * need only the alignment of their element type. T is below 2^22.
  *
- * T == 0 is a successful no-op whatever the other pointers are. */
+ * T == 0 is a successful no-op whatever the pointers to tokens, results and
+ * workspace are. */
 
 /* Code rows' pitch in bytes for K columns; 0 for K outside [1, 65536]. */
 int64_t moe_w8a8_row_pitch(int32_t K);
