@@ -736,3 +736,56 @@ def test_refused_weights_change_nothing(lib):
         with pytest.raises(lib.MoEW8A8Error):
             call()
         assert torch.equal(lin(x), want[0]) and torch.equal(ffn(x), want[1])
+
+
+@pytest.mark.parametrize("H", list(range(1, 17)) + [509, 510, 2043, 2045])
+def test_row_ends(lib, H):
+    """Every remainder of eight, rows narrower than eight included: the values
+    are those of the same rows inside a wider matrix, NaN beside them is not
+    read, and what lies beside the outputs is left as it was."""
+    T, wide = 5, H + 9
+    pad = torch.full((T, wide), float("nan"))
+    for rd in (BF, F32):
+        y, res = pad.to(BF).cuda(), pad.to(rd).cuda()
+        y[:, 4:4 + H] = tokens(T, H, H).cuda()
+        res[:, 4:4 + H] = tokens(T, H, H + 1).to(rd).cuda()
+        w, b = vec(H, H).cuda(), vec(H, H + 1, -1, 1).cuda()
+        out, nrm = torch.full_like(res, 7), torch.full_like(y, 7)
+        o = lib.add_norm(y[:, 4:4 + H], res[:, 4:4 + H], weight=w, bias=b, codes="int8",
+                         inv_smooth=w, residual_out=out[:, 4:4 + H], normed=nrm[:, 4:4 + H])
+        c = dict(norm="rms", post="none", eps=1e-6, bs=1.0, rs=1.0, w=w.cpu(), b=b.cpu())
+        r, e, n, en = add_norm64(y[:, 4:4 + H].cpu(), res[:, 4:4 + H].cpu(), c)
+        R.check(o.residual, r, e * (1 + 4 * R.U) + R.half_step(rd) * (r.abs() + e) + 1e-44, "r")
+        R.check(o.normed, n, en + R.half_step(BF) * (n.abs() + en) + 1e-44, "n")
+        for t in (out, nrm):
+            assert bool((t[:, :4] == 7).all()) and bool((t[:, 4 + H:] == 7).all())
+        assert bool(torch.isfinite(o.scales).all()) and not bool(o.codes[:, H:].any())
+    q, s = lib.act_quant(y[:, 4:4 + H], w)
+    want, ws = R.row_codes(R.smoothed(y[:, 4:4 + H].cpu(), w.cpu()), False)
+    assert torch.equal(q.cpu().float()[:, :H], want) and torch.equal(s.cpu(), ws)
+
+
+@pytest.mark.parametrize("N", list(range(1, 17)) + [131])
+@pytest.mark.parametrize("T", [3, 70])
+def test_output_row_ends(lib, T, N):
+    """The same of a product's outputs and of what is added to them, in the
+    streaming and in the tiled kernel: with INT8 the fp32 result of exact sums,
+    then one rounding each."""
+    K = 130
+    qw = torch.randint(-127, 128, (N, K), generator=torch.Generator().manual_seed(N)).to(torch.int8)
+    sw, x = vec(N, N) / 100, tokens(T, K, N)
+    lin = lib.W8A8Linear(K, N)
+    lin.load_quantized(qw.cuda(), sw.cuda())
+    q, s = R.row_codes(x.float(), False)
+    y = (q.double() @ qw.double().t()) * s.double()[:, None] * sw.double()
+    add = torch.full((T, N + 9), float("nan")).to(BF)
+    add[:, 4:4 + N] = tokens(T, N, N + 1)
+    a = add[:, 4:4 + N].double()
+    for dt in (F32, BF):
+        out = torch.full((T, N + 9), 7.0, dtype=dt).cuda()
+        lin(x.cuda(), add=add.cuda()[:, 4:4 + N], out=out[:, 4:4 + N])
+        v = y + a
+        # sum to fp32, two products, one sum: four roundings
+        bound = 4 * R.U * (y.abs() + a.abs()) * (1 + 1e-3)
+        R.check(out[:, 4:4 + N], v, bound + R.half_step(dt) * (v.abs() + bound) + 1e-44, "out")
+        assert bool((out[:, :4] == 7).all()) and bool((out[:, 4 + N:] == 7).all())

@@ -63,7 +63,7 @@ __device__ __forceinline__ void emit_codes(const float (&v)[NC][8], int lane, in
   }
 }
 
-template <int TPR, int NC>
+template <int TPR, int NC, bool kOdd>
 __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void act_rows_kernel(
     const uint16_t *__restrict__ x, int64_t ld, int64_t T, int K, const float *__restrict__ inv,
     bool fp8, int8_t *__restrict__ q, float *__restrict__ s, uint32_t *__restrict__ clear) {
@@ -72,16 +72,18 @@ __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void act_rows_kernel(
   const int lane = threadIdx.x % TPR;
   const int64_t t = (int64_t)blockIdx.x * G::kRows + threadIdx.x / TPR;
   if (t >= T) return;  // whole wavefronts; a block of one row never has t >= T
-  const uint16_t *xr = x + t * ld;
-  float v[NC][8];
+  v4i raw[NC];
 #pragma unroll
-  for (int i = 0; i < NC; ++i) load8(xr + (lane + i * TPR) * 8, K - (lane + i * TPR) * 8, v[i]);
+  for (int i = 0; i < NC; ++i) raw[i] = fetch8<kOdd>(x + t * ld, (lane + i * TPR) * 8, K);
+  float v[NC][8];
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
+    const int c = (lane + i * TPR) * 8;
+    unpack8<kOdd>(raw[i], c, K, v[i]);
     if (inv) {
       float f[8];
-      load8(inv + (lane + i * TPR) * 8, K - (lane + i * TPR) * 8, f);
+      load8<kOdd>(inv, c, K, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] *= f[j];
     }
@@ -126,7 +128,7 @@ __global__ __launch_bounds__(256) void clear_kernel(uint32_t *__restrict__ p, in
 // ----------------------------------------------------------------- add_norm
 // v = norm(v) for the row in v (elements past H are zero, and stay zero but for a
 // bias). Three cell rows.
-template <int TPR, int NC>
+template <int TPR, int NC, bool kOdd>
 __device__ __forceinline__ void norm_row(float (&v)[NC][8], int kind, const float *w,
                                          const float *b, int H, float eps, int lane,
                                          float *cells) {
@@ -177,25 +179,25 @@ __device__ __forceinline__ void norm_row(float (&v)[NC][8], int kind, const floa
   const float rstd = 1.0f / __builtin_sqrtf(ms + eps);
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    const int c = (lane + i * TPR) * 8, rem = H - c;
+    const int c = (lane + i * TPR) * 8;
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[i][j] *= rstd;
     if (w) {
       float f[8];
-      load8(w + c, rem, f);
+      load8<kOdd>(w, c, H, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] *= f[j];
     }
     if (b) {
       float f[8];
-      load8(b + c, rem, f);
+      load8<kOdd>(b, c, H, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] += f[j];
     }
   }
 }
 
-template <int TPR, int NC>
+template <int TPR, int NC, bool kOdd>
 __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void add_norm_kernel(
     const moe_w8a8_add_norm_args a, int64_t T) {
   typedef RowGroup<TPR> G;
@@ -205,12 +207,9 @@ __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void add_norm_kernel(
   if (t >= T) return;  // as in act_rows_kernel
   const int H = a.hidden;
   float v[NC][8], r[NC][8];
-  const uint16_t *y = a.y + t * a.ld_y;
+  v4i raw[NC];
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int c = (lane + i * TPR) * 8;
-    load8(y + c, H - c, v[i]);
-  }
+  for (int i = 0; i < NC; ++i) raw[i] = fetch8<kOdd>(a.y + t * a.ld_y, (lane + i * TPR) * 8, H);
   // The residual is read before the reductions of the post norm, which would
   // otherwise hold its loads back.
   if (a.residual) {
@@ -218,19 +217,21 @@ __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void add_norm_kernel(
     for (int i = 0; i < NC; ++i) {
       const int c = (lane + i * TPR) * 8;
       if (a.residual_type == MOE_W8A8_F32)
-        load8(static_cast<const float *>(a.residual) + t * a.ld_residual + c, H - c, r[i]);
+        load8<kOdd>(static_cast<const float *>(a.residual) + t * a.ld_residual, c, H, r[i]);
       else
-        load8(static_cast<const uint16_t *>(a.residual) + t * a.ld_residual + c, H - c, r[i]);
+        load8<kOdd>(static_cast<const uint16_t *>(a.residual) + t * a.ld_residual, c, H, r[i]);
     }
   }
-  norm_row<TPR, NC>(v, a.post_norm, a.post_weight, a.post_bias, H, a.eps, lane, cells[0]);
+#pragma unroll
+  for (int i = 0; i < NC; ++i) unpack8<kOdd>(raw[i], (lane + i * TPR) * 8, H, v[i]);
+  norm_row<TPR, NC, kOdd>(v, a.post_norm, a.post_weight, a.post_bias, H, a.eps, lane, cells[0]);
   const float bs = a.block_scale * (a.gate_token ? a.gate_token[t] : 1.0f);
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    const int c = (lane + i * TPR) * 8, rem = H - c;
+    const int c = (lane + i * TPR) * 8;
     if (a.gate_rows) {
       float g[8];
-      load8(a.gate_rows + t / a.gate_group * a.ld_gate + c, rem, g);
+      load8<kOdd>(a.gate_rows + t / a.gate_group * a.ld_gate, c, H, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] *= g[j];
     }
@@ -241,20 +242,17 @@ __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void add_norm_kernel(
     }
     if (a.residual_out) {
       if (a.residual_type == MOE_W8A8_F32)
-        store8(static_cast<float *>(a.residual_out) + t * a.ld_residual_out + c, rem, v[i]);
+        store8<kOdd>(static_cast<float *>(a.residual_out) + t * a.ld_residual_out, c, H, v[i]);
       else
-        store8(static_cast<uint16_t *>(a.residual_out) + t * a.ld_residual_out + c, rem, v[i]);
+        store8<kOdd>(static_cast<uint16_t *>(a.residual_out) + t * a.ld_residual_out, c, H, v[i]);
     }
   }
   if (!a.normed && !a.q) return;  // uniform over the grid
-  norm_row<TPR, NC>(v, a.pre_norm, a.pre_weight, a.pre_bias, H, a.eps, lane, cells[3]);
+  norm_row<TPR, NC, kOdd>(v, a.pre_norm, a.pre_weight, a.pre_bias, H, a.eps, lane, cells[3]);
   if (a.normed) {
-    uint16_t *n = a.normed + t * a.ld_normed;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int c = (lane + i * TPR) * 8;
-      store8(n + c, H - c, v[i]);
-    }
+    for (int i = 0; i < NC; ++i)
+      store8<kOdd>(a.normed + t * a.ld_normed, (lane + i * TPR) * 8, H, v[i]);
   }
   if (!a.q) return;
   uint32_t m = 0;
@@ -263,7 +261,7 @@ __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void add_norm_kernel(
     const int c = (lane + i * TPR) * 8, rem = H - c;
     if (a.inv_smooth) {
       float f[8];
-      load8(a.inv_smooth + c, rem, f);
+      load8<kOdd>(a.inv_smooth, c, H, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] *= f[j];
     }
@@ -371,45 +369,63 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const void *__restrict__
 
 }  // namespace
 
-// Threads per row and chunks per thread: kernel<TPR, NC> holds rows of up to
+// Threads per row and chunks per thread: a kernel<TPR, NC> holds rows of up to
 // TPR * NC * 8 elements.
-#define MOE_ROWS(kernel, TPR, NC, ...)                                                        \
-  launch_kernel(kernel<TPR, NC>,                                                              \
-                dim3((unsigned)((T + RowGroup<TPR>::kRows - 1) / RowGroup<TPR>::kRows)),      \
-                dim3(RowGroup<TPR>::kThreads), st, Timing{}, __VA_ARGS__)
+template <int TPR, int NC>
+struct RowShape {
+  static constexpr int kTpr = TPR, kNc = NC;
+};
+template <int TPR, typename K, typename... A>
+static hipError_t launch_rows(K kernel, int64_t T, hipStream_t st, A... args) {
+  typedef RowGroup<TPR> G;
+  return launch_kernel(kernel, dim3((unsigned)((T + G::kRows - 1) / G::kRows)), dim3(G::kThreads),
+                       st, Timing{}, args...);
+}
 // A thread per chunk up to 8192 columns: the shortest chain for a row alone (one
 // row of 4096: 3.4 us, against 4.2 with two chunks a thread and 9.3 with one
 // wavefront), and the most loads in flight for many (add_norm of 16384 rows of
 // 4096, bf16: 95 us = 5.6 TB/s, against 100 and 127). Two or four rows per
 // block, sharing the weights' loads, were no faster (98, 106).
-#define MOE_ROWS_BY_WIDTH(kernel, width, ...)                              \
-  do {                                                                     \
-    if ((width) <= 512) return MOE_ROWS(kernel, 64, 1, __VA_ARGS__);       \
-    if ((width) <= 2048) return MOE_ROWS(kernel, 256, 1, __VA_ARGS__);     \
-    if ((width) <= 4096) return MOE_ROWS(kernel, 512, 1, __VA_ARGS__);     \
-    if ((width) <= 8192) return MOE_ROWS(kernel, 1024, 1, __VA_ARGS__);    \
-    if ((width) <= 32768) return MOE_ROWS(kernel, 1024, 4, __VA_ARGS__);   \
-    return MOE_ROWS(kernel, 1024, 8, __VA_ARGS__);                         \
-  } while (0)
+template <typename F>
+static hipError_t by_width(int width, F f) {
+  if (width <= 512) return f(RowShape<64, 1>{});
+  if (width <= 2048) return f(RowShape<256, 1>{});
+  if (width <= 4096) return f(RowShape<512, 1>{});
+  if (width <= 8192) return f(RowShape<1024, 1>{});
+  if (width <= 32768) return f(RowShape<1024, 4>{});
+  return f(RowShape<1024, 8>{});
+}
 
 hipError_t launch_act_rows(const uint16_t *x, int64_t ld, int64_t T, int K, const float *inv,
                            bool fp8, int8_t *q, float *s, uint32_t *clear, hipStream_t st) {
+  auto run = [&](auto shape) {
+    constexpr int TPR = decltype(shape)::kTpr, NC = decltype(shape)::kNc;
+    return launch_rows<TPR>(
+        K % 8 ? act_rows_kernel<TPR, NC, true> : act_rows_kernel<TPR, NC, false>, T, st, x, ld, T,
+        K, inv, fp8, q, s, clear);
+  };
   // Many rows and one reduction: two chunks a thread, half the barriers
   // (16384 x 4096: 34.4 us against 40.6, 8192 x 8192: 35.2 against 43.8).
-  if (T > 2048 && K > 2048 && K <= 4096)
-    return MOE_ROWS(act_rows_kernel, 256, 2, x, ld, T, K, inv, fp8, q, s, clear);
-  if (T > 2048 && K > 4096 && K <= 8192)
-    return MOE_ROWS(act_rows_kernel, 512, 2, x, ld, T, K, inv, fp8, q, s, clear);
-  MOE_ROWS_BY_WIDTH(act_rows_kernel, K, x, ld, T, K, inv, fp8, q, s, clear);
+  if (T > 2048 && K > 2048 && K <= 4096) return run(RowShape<256, 2>{});
+  if (T > 2048 && K > 4096 && K <= 8192) return run(RowShape<512, 2>{});
+  return by_width(K, run);
 }
 
 hipError_t launch_hidden_rows(const float *gu, int64_t ld, int64_t T, int F, bool fp8, int8_t *q,
                               float *s, hipStream_t st) {
-  MOE_ROWS_BY_WIDTH(hidden_rows_kernel, F, gu, ld, T, F, fp8, q, s);
+  return by_width(F, [&](auto shape) {
+    constexpr int TPR = decltype(shape)::kTpr, NC = decltype(shape)::kNc;
+    return launch_rows<TPR>(hidden_rows_kernel<TPR, NC>, T, st, gu, ld, T, F, fp8, q, s);
+  });
 }
 
 hipError_t launch_add_norm(const moe_w8a8_add_norm_args &a, int64_t T, hipStream_t st) {
-  MOE_ROWS_BY_WIDTH(add_norm_kernel, a.hidden, a, T);
+  return by_width(a.hidden, [&](auto shape) {
+    constexpr int TPR = decltype(shape)::kTpr, NC = decltype(shape)::kNc;
+    return launch_rows<TPR>(
+        a.hidden % 8 ? add_norm_kernel<TPR, NC, true> : add_norm_kernel<TPR, NC, false>, T, st, a,
+        T);
+  });
 }
 
 hipError_t launch_clear(uint32_t *p, int64_t n, hipStream_t st) {

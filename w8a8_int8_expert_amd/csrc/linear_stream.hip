@@ -97,10 +97,10 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs 
           for (int j = 0; j < 8; ++j) o[j] = 0.0f;
           return;
         }
-        load8(a.in.x + t * a.in.ld + c, rem, o);
+        load8(a.in.x + t * a.in.ld, c, a.K, o);
         if (a.in.inv) {
           float f[8];
-          load8(a.in.inv + c, rem, f);
+          load8(a.in.inv, c, a.K, f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) o[j] *= f[j];
         }

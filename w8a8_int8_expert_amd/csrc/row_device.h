@@ -15,33 +15,89 @@ typedef v4i v4i_a2 __attribute__((aligned(2)));
 typedef v2i v2i_a2 __attribute__((aligned(2)));
 typedef v4f v4f_a4 __attribute__((aligned(4)));
 
-// Eight elements from p, the first `rem` of which exist (the rest read as 0).
-__device__ __forceinline__ void load8(const uint16_t *p, int rem, float *o) {
-  if (rem >= 8) {
-    const v4i r = *reinterpret_cast<const v4i_a2 *>(p);
+// Eight elements c .. c+7 of a row of n (those past it are 0), in two steps: the
+// load, and what becomes of it. A chunk that ends past the row is loaded from
+// the row's last eight elements and moved down, so that a row's odd end costs one
+// load like any other chunk (element by element it held a whole block back:
+// add_norm of 8192 rows of 4095 took 93 us, 4096 columns 46). Only a row of
+// fewer than eight elements is loaded one by one. kOdd false: n is a multiple of
+// eight, and nothing of this is needed (8192 x 4096, both norms, codes: 80 us, 87
+// with it).
+template <bool kOdd = true>
+__device__ __forceinline__ v4i fetch8(const uint16_t *row, int c, int n) {
+  if constexpr (!kOdd)
+    return c < n ? *reinterpret_cast<const v4i_a2 *>(row + c) : v4i{0, 0, 0, 0};
+  if (n >= 8) return *reinterpret_cast<const v4i_a2 *>(row + (c < n - 8 ? c : n - 8));
+  v4i r = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[2 * i] = __uint_as_float((uint32_t)r[i] << 16);
-      o[2 * i + 1] = __uint_as_float((uint32_t)r[i] & 0xffff0000u);
+  for (int j = 0; j < 8; ++j)
+    if (c + j < n) r[j / 2] |= (int)((uint32_t)row[c + j] << (16 * (j & 1)));
+  return r;
+}
+template <bool kOdd = true>
+__device__ __forceinline__ void unpack8(v4i r, int c, int n, float *o) {
+  const int over = c + 8 - n;  // elements past the row
+  if (kOdd && over > 0 && n >= 8) {
+    if (over & 4) r = v4i{r[2], r[3], 0, 0};
+    if (over & 2) r = v4i{r[1], r[2], r[3], 0};
+    if (over & 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r[i] = (int)(((uint32_t)r[i] >> 16) | (i < 3 ? (uint32_t)r[i + 1] << 16 : 0u));
     }
-  } else {
+    if (over >= 8) r = v4i{0, 0, 0, 0};
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = i < rem ? bf16_to_f32(p[i]) : 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = __uint_as_float((uint32_t)r[i] << 16);
+    o[2 * i + 1] = __uint_as_float((uint32_t)r[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void load8(const float *p, int rem, float *o) {
-  if (rem >= 8) {
-    const v4f a = *reinterpret_cast<const v4f_a4 *>(p);
-    const v4f b = *reinterpret_cast<const v4f_a4 *>(p + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[i] = a[i];
-      o[4 + i] = b[i];
+struct Floats8 {
+  v4f a, b;
+};
+template <bool kOdd = true>
+__device__ __forceinline__ Floats8 fetch8(const float *row, int c, int n) {
+  Floats8 r;
+  if constexpr (!kOdd) {
+    r = Floats8{v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
+    if (c < n) {
+      r.a = *reinterpret_cast<const v4f_a4 *>(row + c);
+      r.b = *reinterpret_cast<const v4f_a4 *>(row + c + 4);
     }
+    return r;
+  }
+  if (n >= 8) {
+    const float *p = row + (c < n - 8 ? c : n - 8);
+    r.a = *reinterpret_cast<const v4f_a4 *>(p);
+    r.b = *reinterpret_cast<const v4f_a4 *>(p + 4);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = i < rem ? p[i] : 0.0f;
+    for (int j = 0; j < 4; ++j) {
+      r.a[j] = c + j < n ? row[c + j] : 0.0f;
+      r.b[j] = c + 4 + j < n ? row[c + 4 + j] : 0.0f;
+    }
   }
+  return r;
+}
+template <bool kOdd = true>
+__device__ __forceinline__ void unpack8(Floats8 r, int c, int n, float *o) {
+  const int over = c + 8 - n;
+  if (kOdd && over > 0 && n >= 8) {
+    if (over & 4) r = Floats8{r.b, v4f{0, 0, 0, 0}};
+    if (over & 2) r = Floats8{v4f{r.a[2], r.a[3], r.b[0], r.b[1]}, v4f{r.b[2], r.b[3], 0, 0}};
+    if (over & 1) r = Floats8{v4f{r.a[1], r.a[2], r.a[3], r.b[0]}, v4f{r.b[1], r.b[2], r.b[3], 0}};
+    if (over >= 8) r = Floats8{v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    o[j] = r.a[j];
+    o[4 + j] = r.b[j];
+  }
+}
+template <bool kOdd = true, typename T>
+__device__ __forceinline__ void load8(const T *row, int c, int n, float *o) {
+  unpack8<kOdd>(fetch8<kOdd>(row, c, n), c, n, o);
 }
 // Two values rounded to bf16 (nearest, ties to even; NaN stays NaN) by the one
 // hardware instruction.
@@ -50,26 +106,50 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2bf));
 }
-__device__ __forceinline__ void store8(uint16_t *p, int rem, const float *v) {
+// Elements c .. c+7 of a row of n; a row's odd end in pieces of 4, 2 and 1.
+template <bool kOdd = true>
+__device__ __forceinline__ void store8(uint16_t *row, int c, int n, const float *v) {
+  typedef uint32_t u32_a2 __attribute__((aligned(2)));
+  uint16_t *p = row + c;
+  const int rem = n - c;
+  int w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (int)bf16x2(v[2 * i], v[2 * i + 1]);
   if (rem >= 8) {
-    v4i r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = (int)bf16x2(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<v4i_a2 *>(p) = r;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < rem) p[i] = f32_to_bf16(v[i]);
+    *reinterpret_cast<v4i_a2 *>(p) = v4i{w[0], w[1], w[2], w[3]};
+  } else if (kOdd && rem > 0) {
+    if (rem & 4) {
+      *reinterpret_cast<v2i_a2 *>(p) = v2i{w[0], w[1]};
+      p += 4; w[0] = w[2]; w[1] = w[3];
+    }
+    if (rem & 2) {
+      *reinterpret_cast<u32_a2 *>(p) = (uint32_t)w[0];
+      p += 2; w[0] = w[1];
+    }
+    if (rem & 1) *p = (uint16_t)w[0];
   }
 }
-__device__ __forceinline__ void store8(float *p, int rem, const float *v) {
+template <bool kOdd = true>
+__device__ __forceinline__ void store8(float *row, int c, int n, const float *v) {
+  typedef float v2f_a4 __attribute__((ext_vector_type(2), aligned(4)));
+  float *p = row + c;
+  const int rem = n - c;
   if (rem >= 8) {
     *reinterpret_cast<v4f_a4 *>(p) = v4f{v[0], v[1], v[2], v[3]};
     *reinterpret_cast<v4f_a4 *>(p + 4) = v4f{v[4], v[5], v[6], v[7]};
-  } else {
+  } else if (kOdd && rem > 0) {
+    float w[4] = {v[0], v[1], v[2], v[3]};
+    if (rem & 4) {
+      *reinterpret_cast<v4f_a4 *>(p) = v4f{v[0], v[1], v[2], v[3]};
+      p += 4;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < rem) p[i] = v[i];
+      for (int i = 0; i < 4; ++i) w[i] = v[4 + i];
+    }
+    if (rem & 2) {
+      *reinterpret_cast<v2f_a4 *>(p) = v2f_a4{w[0], w[1]};
+      p += 2; w[0] = w[2];
+    }
+    if (rem & 1) *p = w[0];
   }
 }
 
@@ -121,20 +201,18 @@ __device__ __forceinline__ uint32_t wave_max_bits(uint32_t m) {
 }
 
 // Hidden values h = silu(g) u of columns c .. c+7 (c a multiple of 8, `rem` of
-// them exist) from a row of gate and up values in packed order: alternating
-// runs of 32.
+// them exist, 0 past them) from a row of gate and up values in packed order:
+// alternating runs of 32, whole ones also at the end.
 __device__ __forceinline__ void hidden8(const float *gu, int c, int rem, float *o) {
   if (rem <= 0) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = 0.0f;
     return;
   }
-  float u[8];
-  const float *p = gu + c / 32 * 64 + c % 32;
-  load8(p, rem, o);
-  load8(p + 32, rem, u);
+  const v4f *p = reinterpret_cast<const v4f *>(gu + c / 32 * 64 + c % 32);
+  const v4f g[2] = {p[0], p[1]}, u[2] = {p[8], p[9]};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = swiglu(o[j], u[j]);
+  for (int j = 0; j < 8; ++j) o[j] = j < rem ? swiglu(g[j / 4][j % 4], u[j / 4][j % 4]) : 0.0f;
 }
 
 }  // namespace moe
