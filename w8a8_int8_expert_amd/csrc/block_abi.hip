@@ -97,6 +97,9 @@ bool fused_hidden(int64_t T, int F) {
   return T <= kFusedRows && T * row_pitch(F) <= kFusedHidden;
 }
 
+// Room for codes of T rows, row-major or in tiles.
+size_t codes_bytes(int64_t T, int K) { return (size_t)((T + 15) / 16 * 16) * row_pitch(K); }
+
 struct LinearLayout {
   size_t q, s, partial, total;
 };
@@ -105,7 +108,7 @@ LinearLayout linear_layout(int K, int64_t T) {
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += up256(bytes); return at; };
   if (T == 0 || fused_tokens(T, K)) return L;
-  L.q = take((size_t)T * row_pitch(K));
+  L.q = take(codes_bytes(T, K));
   L.s = take((size_t)T * 4);
   L.partial = take(T > kAlwaysStream ? kPartialBytes : 0);
   L.total = o;
@@ -127,12 +130,12 @@ FfnLayout ffn_layout(int H, int F, int64_t T) {
   const size_t hid = (size_t)T * row_pitch(F) * 4;
   L.h = take(gu > hid ? gu : hid);
   if (!fused_tokens(T, H)) {
-    L.q = take((size_t)T * row_pitch(H));
+    L.q = take(codes_bytes(T, H));
     L.s = take((size_t)T * 4);
   }
   if (!fused_hidden(T, F)) {
     L.amax = take((size_t)T * 4);
-    L.qh = take((size_t)T * row_pitch(F));
+    L.qh = take(codes_bytes(T, F));
     L.sh = take((size_t)T * 4);
   }
   L.partial = take(T > kAlwaysStream ? kPartialBytes : 0);
@@ -212,7 +215,7 @@ extern "C" int moe_w8a8_act_quant(int32_t K, int32_t format, const uint16_t *x, 
             sm = flat(s, (size_t)T * 4);
   if (overlap(xm, qm) || overlap(xm, sm) || overlap(qm, sm))
     return MOE_W8A8_ERR_INVALID;
-  MOE_CHECK(launch_act_rows(x, ld_x, T, K, inv_smooth, format == MOE_W8A8_FORMAT_FP8, q, s,
+  MOE_CHECK(launch_act_rows(x, ld_x, T, K, inv_smooth, format == MOE_W8A8_FORMAT_FP8, false, q, s,
                             nullptr, (hipStream_t)stream));
   return MOE_W8A8_OK;
 }
@@ -244,9 +247,10 @@ extern "C" int moe_w8a8_linear(const moe_w8a8_linear_weights *w, const moe_w8a8_
   } else if (act->x) {
     int8_t *q = (int8_t *)(ws + L.q);
     float *s = (float *)(ws + L.s);
-    MOE_CHECK(launch_act_rows(act->x, act->ld_x, T, K, w->inv_smooth,
-                              w->format == MOE_W8A8_FORMAT_FP8, q, s, nullptr, st));
     in.q = q; ep.row_scale = s;
+    in.tiles = streams(T, K, packed_rows(w->out_features, false));
+    MOE_CHECK(launch_act_rows(act->x, act->ld_x, T, K, w->inv_smooth,
+                              w->format == MOE_W8A8_FORMAT_FP8, in.tiles, q, s, nullptr, st));
   } else {
     in.q = act->q; ep.row_scale = act->s;
   }
@@ -294,7 +298,8 @@ extern "C" int moe_w8a8_ffn(const moe_w8a8_linear_weights *gu, const moe_w8a8_li
   } else if (act->x) {
     int8_t *q = (int8_t *)(ws + L.q);
     float *s = (float *)(ws + L.s);
-    MOE_CHECK(launch_act_rows(act->x, act->ld_x, T, H, gu->inv_smooth, fp8, q, s,
+    in.tiles = few;
+    MOE_CHECK(launch_act_rows(act->x, act->ld_x, T, H, gu->inv_smooth, fp8, few, q, s,
                               few ? nullptr : amax, st));
     in.q = q; ep.row_scale = s;
   } else {
@@ -310,10 +315,12 @@ extern "C" int moe_w8a8_ffn(const moe_w8a8_linear_weights *gu, const moe_w8a8_li
   } else {
     int8_t *qh = (int8_t *)(ws + L.qh);
     float *sh = (float *)(ws + L.sh);
-    if (few)
-      MOE_CHECK(launch_hidden_rows(h, Np, T, F, fp8, qh, sh, st));
-    else
+    if (few) {
+      hin.tiles = streams(T, F, packed_rows(dn->out_features, false));
+      MOE_CHECK(launch_hidden_rows(h, Np, T, F, fp8, hin.tiles, qh, sh, st));
+    } else {
       MOE_CHECK(launch_requant_rows(h, amax, T, F, fp8, qh, sh, st));
+    }
     hin.q = qh; ed.row_scale = sh;
   }
   MOE_CHECK(product(hin, hin.q, T, *dn, ed, ws + L.partial, st));

@@ -25,6 +25,16 @@ inline __host__ __device__ int source_row(int p, int N, bool gated) {
   return f < F ? (p / 32 % 2) * F + f : -1;
 }
 
+// Where code k of row t is. Codes that only a streaming product reads lie in
+// tiles of 16 rows x 64 k, as the weights do: an operand load then takes whole
+// cache lines, against half a line of each of 16 rows (and the lines in flight are
+// what bounds it). The row count is rounded up to whole tiles.
+inline __host__ __device__ size_t code_at(bool tiles, int64_t t, int k, int Kp) {
+  return tiles ? ((size_t)(t >> 4) * (size_t)(Kp >> 6) + (size_t)(k >> 6)) * 1024 +
+                     (size_t)((((k >> 4) & 3) * 16 + (int)(t & 15)) * 16 + (k & 15))
+               : (size_t)t * (size_t)Kp + (size_t)k;
+}
+
 // What a product does with its sums.
 struct Epilogue {
   const float *row_scale;  // [T]
@@ -62,12 +72,13 @@ constexpr int kFusedRows = 4;
 constexpr size_t kPartialBytes = (size_t)32 << 20;
 
 hipError_t launch_act_rows(const uint16_t *x, int64_t ld_x, int64_t T, int K, const float *inv,
-                           bool fp8, int8_t *q, float *s, uint32_t *clear, hipStream_t st);
+                           bool fp8, bool tiles, int8_t *q, float *s, uint32_t *clear,
+                           hipStream_t st);
 hipError_t launch_clear(uint32_t *p, int64_t n, hipStream_t st);
 // Gate and up values fp32 [T][ld] in packed order (a streaming product's plain
 // output) -> codes [T][Fp] and scales of h = silu(g) u
-hipError_t launch_hidden_rows(const float *gu, int64_t ld, int64_t T, int F, bool fp8, int8_t *q,
-                              float *s, hipStream_t st);
+hipError_t launch_hidden_rows(const float *gu, int64_t ld, int64_t T, int F, bool fp8, bool tiles,
+                              int8_t *q, float *s, hipStream_t st);
 // h fp32 [T][Fp] with row max |h| -> codes [T][Fp], scales
 hipError_t launch_requant_rows(const float *h, const uint32_t *amax, int64_t T, int F, bool fp8,
                                int8_t *q, float *s, hipStream_t st);
@@ -80,7 +91,8 @@ hipError_t launch_pack_rows(const moe_w8a8_linear_weights &w, const void *src, i
 // that the kernel codes itself: bf16 tokens x, or the hidden rows of gate and
 // up values h in packed order.
 struct StreamIn {
-  const int8_t *q;  // codes [T][Kp], or NULL
+  const int8_t *q;  // codes, or NULL
+  bool tiles;       // codes in tiles of 16 rows x 64 k (code_at), not [T][Kp]
   const uint16_t *x;
   const float *h;
   int64_t ld;        // of x or h

@@ -47,18 +47,19 @@ struct RowGroup {
   }
 };
 
-// Codes of a row whose scaled values v are in registers; columns past the
+// Codes of row t, whose scaled values v are in registers; columns past the
 // width hold zeros and give zero codes, up to the pitch Kp.
 template <int TPR, int NC>
-__device__ __forceinline__ void emit_codes(const float (&v)[NC][8], int lane, int Kp, uint32_t amax,
-                                           bool fp8, int8_t *q, float *s) {
+__device__ __forceinline__ void emit_codes(const float (&v)[NC][8], int lane, int64_t t, int Kp,
+                                           uint32_t amax, bool fp8, bool tiles, int8_t *q,
+                                           float *s) {
   const RowCode rc = row_code(amax, fp8);
-  if (lane == 0) *s = rc.scale;
+  if (lane == 0) s[t] = rc.scale;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    const int c = lane + i * TPR;
-    if (c * 8 < Kp)
-      *reinterpret_cast<v2i *>(q + c * 8) =
+    const int c = (lane + i * TPR) * 8;
+    if (c < Kp)
+      *reinterpret_cast<v2i *>(q + code_at(tiles, t, c, Kp)) =
           v2i{(int)row_codes4(v[i], rc, fp8), (int)row_codes4(v[i] + 4, rc, fp8)};
   }
 }
@@ -66,7 +67,8 @@ __device__ __forceinline__ void emit_codes(const float (&v)[NC][8], int lane, in
 template <int TPR, int NC, bool kOdd>
 __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void act_rows_kernel(
     const uint16_t *__restrict__ x, int64_t ld, int64_t T, int K, const float *__restrict__ inv,
-    bool fp8, int8_t *__restrict__ q, float *__restrict__ s, uint32_t *__restrict__ clear) {
+    bool fp8, bool tiles, int8_t *__restrict__ q, float *__restrict__ s,
+    uint32_t *__restrict__ clear) {
   typedef RowGroup<TPR> G;
   __shared__ float cells[G::kWaves];
   const int lane = threadIdx.x % TPR;
@@ -92,15 +94,14 @@ __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void act_rows_kernel(
   }
   m = G::max_bits(m, cells);
   if (clear && lane == 0) clear[t] = 0u;
-  const int Kp = row_pitch(K);
-  emit_codes<TPR, NC>(v, lane, Kp, m, fp8, q + t * Kp, s + t);
+  emit_codes<TPR, NC>(v, lane, t, row_pitch(K), m, fp8, tiles, q, s);
 }
 
 // Codes of the hidden rows of a streaming gate/up product.
 template <int TPR, int NC>
 __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void hidden_rows_kernel(
-    const float *__restrict__ gu, int64_t ld, int64_t T, int F, bool fp8, int8_t *__restrict__ q,
-    float *__restrict__ s) {
+    const float *__restrict__ gu, int64_t ld, int64_t T, int F, bool fp8, bool tiles,
+    int8_t *__restrict__ q, float *__restrict__ s) {
   typedef RowGroup<TPR> G;
   __shared__ float cells[G::kWaves];
   const int lane = threadIdx.x % TPR;
@@ -116,8 +117,7 @@ __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void hidden_rows_kernel(
     for (int j = 0; j < 8; ++j) m = umax(m, abs_bits(v[i][j]));
   }
   m = G::max_bits(m, cells);
-  const int Fp = row_pitch(F);
-  emit_codes<TPR, NC>(v, lane, Fp, m, fp8, q + t * Fp, s + t);
+  emit_codes<TPR, NC>(v, lane, t, row_pitch(F), m, fp8, tiles, q, s);
 }
 
 __global__ __launch_bounds__(256) void clear_kernel(uint32_t *__restrict__ p, int64_t n) {
@@ -273,8 +273,8 @@ __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void add_norm_kernel(
     }
   }
   m = G::max_bits(m, cells[6]);
-  const int Kp = row_pitch(H);
-  emit_codes<TPR, NC>(v, lane, Kp, m, a.format == MOE_W8A8_FORMAT_FP8, a.q + t * Kp, a.s + t);
+  emit_codes<TPR, NC>(v, lane, t, row_pitch(H), m, a.format == MOE_W8A8_FORMAT_FP8, false, a.q,
+                      a.s);
 }
 
 // ------------------------------------------------------------------- requant
@@ -397,12 +397,13 @@ static hipError_t by_width(int width, F f) {
 }
 
 hipError_t launch_act_rows(const uint16_t *x, int64_t ld, int64_t T, int K, const float *inv,
-                           bool fp8, int8_t *q, float *s, uint32_t *clear, hipStream_t st) {
+                           bool fp8, bool tiles, int8_t *q, float *s, uint32_t *clear,
+                           hipStream_t st) {
   auto run = [&](auto shape) {
     constexpr int TPR = decltype(shape)::kTpr, NC = decltype(shape)::kNc;
     return launch_rows<TPR>(
         K % 8 ? act_rows_kernel<TPR, NC, true> : act_rows_kernel<TPR, NC, false>, T, st, x, ld, T,
-        K, inv, fp8, q, s, clear);
+        K, inv, fp8, tiles, q, s, clear);
   };
   // Many rows and one reduction: two chunks a thread, half the barriers
   // (16384 x 4096: 34.4 us against 40.6, 8192 x 8192: 35.2 against 43.8).
@@ -411,11 +412,11 @@ hipError_t launch_act_rows(const uint16_t *x, int64_t ld, int64_t T, int K, cons
   return by_width(K, run);
 }
 
-hipError_t launch_hidden_rows(const float *gu, int64_t ld, int64_t T, int F, bool fp8, int8_t *q,
-                              float *s, hipStream_t st) {
+hipError_t launch_hidden_rows(const float *gu, int64_t ld, int64_t T, int F, bool fp8, bool tiles,
+                              int8_t *q, float *s, hipStream_t st) {
   return by_width(F, [&](auto shape) {
     constexpr int TPR = decltype(shape)::kTpr, NC = decltype(shape)::kNc;
-    return launch_rows<TPR>(hidden_rows_kernel<TPR, NC>, T, st, gu, ld, T, F, fp8, q, s);
+    return launch_rows<TPR>(hidden_rows_kernel<TPR, NC>, T, st, gu, ld, T, F, fp8, tiles, q, s);
   });
 }
 

@@ -27,7 +27,8 @@
 namespace moe {
 namespace {
 
-enum { kCodes, kTokens, kHidden };
+// Row-major codes, codes in tiles, bf16 tokens, the hidden rows' gate and up values.
+enum { kCodes, kTiles, kTokens, kHidden };
 
 struct StreamArgs {
   StreamIn in;
@@ -53,7 +54,8 @@ __device__ __forceinline__ v8bf codes_bf16(int lo, int hi) {
 template <int RT, int NPW, int W, int U, bool kF8, int kSrc>
 __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs a) {
   typedef typename Acc16v<kF8>::T Acc;
-  static_assert(kSrc == kCodes || RT == 1, "rows coded by the block");
+  constexpr bool kFused = kSrc == kTokens || kSrc == kHidden;
+  static_assert(!kFused || RT == 1, "rows coded by the block");
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int pairs = a.Kp >> 7;
 
@@ -81,10 +83,10 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs 
   for (int u = 0; u < U; ++u)
     if (u < n) load_w(u, u);
 
-  extern __shared__ __attribute__((aligned(16))) int8_t codes[];  // kSrc != kCodes: [T][Kp + 16]
+  extern __shared__ __attribute__((aligned(16))) int8_t codes[];  // kFused: [T][Kp + 16]
   __shared__ float rscale[kFusedRows];
   __shared__ uint32_t rmax[kFusedRows][W];
-  if constexpr (kSrc != kCodes) {
+  if constexpr (kFused) {
     // Rows of up to 64 W * 8 * kKeep elements stay in registers between their
     // maximum and their codes; wider ones are read again.
     constexpr int kKeep = 2, kStep = 64 * W * 8;
@@ -163,15 +165,18 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs 
     int r = rt * 16 + (lane & 15);
     r = r < a.T ? r : a.T - 1;
     if constexpr (kSrc == kCodes) bp[rt] = a.in.q + (size_t)r * a.Kp + (lane >> 4) * 16;
+    else if constexpr (kSrc == kTiles)
+      bp[rt] = a.in.q + frag_tile(r >> 4, 0, a.Kp) + ((lane & 48) + (r & 15)) * 16;
     else bp[rt] = codes + r * (a.Kp + 16) + (lane >> 4) * 16;
   }
   auto load_x = [&](int u, int s) {
-    const size_t at = (size_t)(wave + s * W) * 128;
+    constexpr int kHalf = kSrc == kTiles ? 1024 : 64;  // 64 k further
+    const size_t at = (size_t)(wave + s * W) * (2 * kHalf);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        bf[u][rt][h] = *reinterpret_cast<const v4i *>(bp[rt] + at + h * 64);
+        bf[u][rt][h] = *reinterpret_cast<const v4i *>(bp[rt] + at + h * kHalf);
   };
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -253,7 +258,7 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs 
     const int p = (int)blockIdx.x * NPW + c / RT;
     const Acc sum = total(c);
     if (r < a.T && p < (a.Np >> 4)) {
-      const float rs = kSrc == kCodes ? ep.row_scale[r] : rscale[r];
+      const float rs = kFused ? rscale[r] : ep.row_scale[r];
       const v4f sc = *reinterpret_cast<const v4f_a4 *>(ep.scale + p * 16 + ch0);
       float v[4];
 #pragma unroll
@@ -266,7 +271,8 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs 
 template <int RT, int NPW, int W, int U, int kSrc>
 hipError_t run(const StreamArgs &a, bool fp8, hipStream_t st) {
   const dim3 grid((unsigned)((a.Np / 16 + NPW - 1) / NPW));
-  const size_t lds = kSrc == kCodes ? 0 : (size_t)a.T * (a.Kp + 16);
+  const bool fused = kSrc == kTokens || kSrc == kHidden;
+  const size_t lds = fused ? (size_t)a.T * (a.Kp + 16) : 0;
   (void)hipGetLastError();
   if (fp8)
     hipLaunchKernelGGL((linear_stream_kernel<RT, NPW, W, U, true, kSrc>), grid,
@@ -291,11 +297,11 @@ hipError_t pick(const StreamArgs &a, bool fp8, hipStream_t st) {
   if (panels <= 256) {
     // Rows coded by the block: more wavefronts share that work (one token,
     // 4096 outputs, K 4096: 5.6 with 16 wavefronts, 6.1 with 8).
-    if constexpr (kSrc != kCodes)
+    if constexpr (kSrc == kTokens || kSrc == kHidden)
       if (a.Kp >= 4096) return run<RT, 1, 16, 2, kSrc>(a, fp8, st);
     return run<RT, 1, 8, 2, kSrc>(a, fp8, st);
   }
-  if constexpr (kSrc == kCodes && RT == 1) return run<RT, 2, 8, 2, kSrc>(a, fp8, st);
+  if constexpr ((kSrc == kCodes || kSrc == kTiles) && RT == 1) return run<RT, 2, 8, 2, kSrc>(a, fp8, st);
   if (panels < 1024) return run<RT, 2, 8, 2, kSrc>(a, fp8, st);
   return run<RT, 4, 4, 2, kSrc>(a, fp8, st);
 }
@@ -308,6 +314,11 @@ hipError_t launch_linear_stream(const StreamIn &in, int T, const int8_t *w, int 
   a.in = in; a.T = T; a.K = K; a.Kp = row_pitch(K); a.w = w; a.Np = Np; a.ep = ep;
   if (in.x) return pick<1, kTokens>(a, fp8, st);
   if (in.h) return pick<1, kHidden>(a, fp8, st);
+  if (in.tiles) {
+    if (T <= 16) return pick<1, kTiles>(a, fp8, st);
+    if (T <= 32) return pick<2, kTiles>(a, fp8, st);
+    return pick<4, kTiles>(a, fp8, st);
+  }
   if (T <= 16) return pick<1, kCodes>(a, fp8, st);
   if (T <= 32) return pick<2, kCodes>(a, fp8, st);
   return pick<4, kCodes>(a, fp8, st);
