@@ -284,7 +284,8 @@ extern "C" int moe_w8a8_ffn(const moe_w8a8_linear_weights *gu, const moe_w8a8_li
   char *ws = (char *)workspace;
   float *h = (float *)(ws + L.h);
   uint32_t *amax = (uint32_t *)(ws + L.amax);
-  const bool few = streams(T, H, packed_rows(2 * F, true));  // else SwiGLU and row maxima in the first product
+  // Few tokens stream; of more, the first product applies SwiGLU and takes row maxima.
+  const bool few = streams(T, H, packed_rows(2 * F, true));
 
   Epilogue ep{};
   ep.scale = gu->scale; ep.out = h; ep.out_f32 = 1;

@@ -54,17 +54,18 @@ struct Epilogue {
 // tokens; tiles read both several times, but the weights in larger panels, and
 // split K over blocks. Up to 32 tokens streaming is the faster almost
 // everywhere, beyond 64 never; between them it depends on how much there is to
-// read (us, streaming against tiles, INT8): 16 tokens, K 8192, 8192 outputs
-// 13.9, 15.9; 32 tokens, K 4096, 8192 outputs 10.0, 12.0; 64 tokens, K 2048,
-// 4096 outputs 6.2, 9.4; K 4096, 4096 outputs 11.6, 11.6; K 4096, 8192 outputs
-// 13.9, 12.5; K 8192, 4096 outputs 20.4, 13.1; 40 tokens, K 4096, 11000
-// outputs 20.3, 13.5.
+// read (us, streaming against tiles, INT8, from bf16 tokens): 32 tokens, K 4096,
+// 8192 outputs 11.9, 14.7; 40 tokens, K 4096, 8192 outputs 12.8, 15.6; 64 tokens,
+// K 4096, 4096 outputs 10.7, 14.4, 8192 outputs 14.2, 15.8, 11000 outputs 21.0,
+// 17.6; K 8192, 4096 outputs 17.7, 16.7; K 2048, 16384 outputs 14.1, 13.2, 32003
+// outputs 25.2, 18.0. (Row-major codes cost streaming up to 2.2 more at 64 tokens;
+// the choice is the same for both, so that a sum's order is.)
 constexpr int kStreamRows = 64;   // most that stream
 constexpr int kAlwaysStream = 32; // fewer always do
 inline bool streams(int64_t T, int K, int Np) {
   if (T <= kAlwaysStream) return true;
   if (T > kStreamRows) return false;
-  return K <= 2048 || (K <= 4096 && Np <= 4096);
+  return K <= 4096 && Np <= 8192;
 }
 // Largest batch whose rows a streaming product codes itself.
 constexpr int kFusedRows = 4;

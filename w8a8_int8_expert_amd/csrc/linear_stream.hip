@@ -285,12 +285,16 @@ hipError_t run(const StreamArgs &a, bool fp8, hipStream_t st) {
 
 // Panels a block owns: one while a launch has at most a block per compute unit
 // then, more where that leaves enough blocks, so that the tokens are read a
-// half or a quarter as often. Measured on MI355X (codes, INT8, K 4096; us with
-// 1, 2 and 4 panels a block):
-//   4096 outputs:  16 tokens 5.7, 6.7, 9.1   64 tokens 11.7, 12.6, 16.6
-//   8192 outputs:  16 tokens 9.9, 8.3, 10.5  64 tokens 21.9, 14.0, 17.2
-//   16384 outputs: 16 tokens 14.9, 12.7, 12.9  64 tokens 41.4, 25.9, 19.7
-//   32003 outputs: 32 tokens 42.9, 30.5, 25.3 (131 MB of weights: 5.2 TB/s)
+// half or a quarter as often. Measured on MI355X (INT8, K 4096, the codes' launch
+// of 2.5 included; us with 1, 2 and 4 panels a block):
+//   4096 outputs:  16 tokens 8.0, 9.0, 11.3    64 tokens 10.8, 12.1, 15.8
+//   8192 outputs:  16 tokens 11.7, 10.7, 12.6  64 tokens 17.0, 14.1, 17.2
+//   11000 outputs: 16 tokens 14.7, 14.0, 13.5  32 tokens 18.3, 16.4, 15.4
+//   16384 outputs: 16 tokens 18.2, 15.9, 16.3  32 tokens 22.8, 17.9, 17.7
+//   32003 outputs: 32 tokens 38.7, 30.0, 27.6
+// Between 512 and 1024 panels, blocks of two would be more than one a unit and
+// fewer than two: with K from 4096 on, blocks of four take 3 to 9 % less time (32
+// tokens, K 8192, 12800 outputs: 28.9, 25.9), below it 2 % more.
 template <int RT, int kSrc>
 hipError_t pick(const StreamArgs &a, bool fp8, hipStream_t st) {
   const int panels = a.Np / 16;
@@ -301,8 +305,9 @@ hipError_t pick(const StreamArgs &a, bool fp8, hipStream_t st) {
       if (a.Kp >= 4096) return run<RT, 1, 16, 2, kSrc>(a, fp8, st);
     return run<RT, 1, 8, 2, kSrc>(a, fp8, st);
   }
-  if constexpr ((kSrc == kCodes || kSrc == kTiles) && RT == 1) return run<RT, 2, 8, 2, kSrc>(a, fp8, st);
-  if (panels < 1024) return run<RT, 2, 8, 2, kSrc>(a, fp8, st);
+  constexpr bool codes = kSrc == kCodes || kSrc == kTiles;
+  const bool four = codes && a.Kp >= 4096 ? panels > 512 : (!codes || RT > 1) && panels >= 1024;
+  if (!four) return run<RT, 2, 8, 2, kSrc>(a, fp8, st);
   return run<RT, 4, 4, 2, kSrc>(a, fp8, st);
 }
 
