@@ -789,3 +789,19 @@ def test_output_row_ends(lib, T, N):
         bound = 4 * R.U * (y.abs() + a.abs()) * (1 + 1e-3)
         R.check(out[:, 4:4 + N], v, bound + R.half_step(dt) * (v.abs() + bound) + 1e-44, "out")
         assert bool((out[:, :4] == 7).all()) and bool((out[:, 4 + N:] == 7).all())
+
+
+# Each tile shape of the tiled product, with ragged last tiles both ways: 256 x 256,
+# 256 x 192, 128 x 256, 128 x 192, 128 x 128, 64 x 128 (one and two blocks a unit).
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,K,N", [(2990, 200, 4090), (1999, 130, 6130), (990, 300, 8187),
+                                   (1021, 200, 6001), (500, 400, 6099), (250, 300, 6143),
+                                   (251, 1, 11007), (130, 130, 32003)])
+def test_linear_tiles(lib, T, K, N, fp8):
+    test_linear(lib, T, K, N, fp8)
+
+
+@pytest.mark.parametrize("T,H,F", [(500, 200, 3007), (990, 130, 4091), (120, 300, 8200)])
+def test_ffn_tiles(lib, T, H, F):
+    test_ffn_int8(lib, T, H, F)
+    test_ffn_fp8(lib, T, H, F)

@@ -73,9 +73,11 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const Til
   // words so that the two 32-lane halves (rows r and r + 4) use other banks.
   constexpr int kPitch = NJ * 32 + 8, kSlice = 16 * kPitch * 4;
   static_assert(W * kSlice <= kRing, "epilogue staging");
+  constexpr int kCols = (BN + 63) / 64 * 64;  // whole wavefronts fetch scales
+  static_assert(BM % 64 == 0, "scales");
   __shared__ __attribute__((aligned(1024))) int8_t lds[kRing];
-  __shared__ __attribute__((aligned(16))) float row_scale[BM], row_gate[BM], col_scale[BN],
-      col_bias[BN];
+  __shared__ __attribute__((aligned(16))) float row_scale[BM], row_gate[BM], col_scale[kCols],
+      col_bias[kCols];
 
   const int64_t tiles = (int64_t)a.mt * a.nt, chunk = (tiles + 7) >> 3;
   const int64_t L = (int64_t)(blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
@@ -137,7 +139,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tiled_kernel(const Til
       const int64_t i = at + lane;
       dma4(src + (i < last ? i : last), __builtin_amdgcn_readfirstlane(lds_addr(dst)));
     };
-    for (int i = wave; i < (BM + BN) / 64; i += W) {
+    for (int i = wave; i < (BM + kCols) / 64; i += W) {
       const int r = i * 64, c = r - BM;
       if (r < BM) {
         fetch(ep.row_scale, m0 + r, a.T - 1, row_scale + r);
@@ -438,8 +440,8 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const TiledLinear a) {
   }
 }
 
-template <int WM, int WN, int MI, int NJ, int S, bool kGated, bool kSplit>
-hipError_t run(TiledLinear a, bool fp8, hipStream_t st) {
+template <int WM, int WN, int MI, int NJ, int S, bool kF8, bool kGated, bool kSplit>
+hipError_t run_as(TiledLinear a, hipStream_t st) {
   constexpr int BM = WM * MI * 32, BN = WN * NJ * 32;
   a.mt = (int)((a.T + BM - 1) / BM);
   a.nt = (a.Np + BN - 1) / BN;
@@ -450,13 +452,13 @@ hipError_t run(TiledLinear a, bool fp8, hipStream_t st) {
   a.gn = (int)(a.mt >= 8 ? 4 : (share + a.mt - 1) / a.mt);
   if (a.gn > a.nt) a.gn = a.nt;
   const dim3 grid((unsigned)((tiles + 7) / 8 * 8), (unsigned)a.split);
-  const dim3 block(64 * WM * WN);
-  const Timing tm{};
-  if (fp8)
-    return launch_kernel(linear_tiled_kernel<WM, WN, MI, NJ, S, true, kGated, kSplit>, grid,
-                         block, st, tm, a);
-  return launch_kernel(linear_tiled_kernel<WM, WN, MI, NJ, S, false, kGated, kSplit>, grid,
-                       block, st, tm, a);
+  return launch_kernel(linear_tiled_kernel<WM, WN, MI, NJ, S, kF8, kGated, kSplit>, grid,
+                       dim3(64 * WM * WN), st, Timing{}, a);
+}
+template <int WM, int WN, int MI, int NJ, int S, bool kGated, bool kSplit = false>
+hipError_t run(const TiledLinear &a, bool fp8, hipStream_t st) {
+  return fp8 ? run_as<WM, WN, MI, NJ, S, true, kGated, kSplit>(a, st)
+             : run_as<WM, WN, MI, NJ, S, false, kGated, kSplit>(a, st);
 }
 
 template <bool kGated>
@@ -468,42 +470,78 @@ hipError_t join(const TiledLinear &a, bool fp8, hipStream_t st) {
   return launch_kernel(linear_join_kernel<false, kGated>, grid, dim3(256), st, Timing{}, a);
 }
 
-// Tile shape and split of K by estimated time. A stage of 128 k takes a full
-// chip 2.1 us with 256 x 256 tiles, 1.1 with 128 x 256 and 0.4 with 64 x 128
-// (one block per compute unit, 0.28 while most are idle; two blocks a unit take
-// 0.8 together). Measured on MI355X, INT8 codes, us with 256 x 256, 128 x 256
-// and 64 x 128 tiles (tokens, K, outputs):
-//   512, 4096, 6144: 43, 30, 24     1500, 4096, 4096: 45, 35, 40
-//   3000, 4096, 4096: 55, 67, 74    8192, 512, 8192: 66, 75, 84
+// Tile shape and split of K by estimated time: what a stage of 128 k takes with
+// every compute unit at work (`full`), and in a last round of fewer tiles (from
+// `a` for one to a + b). Fitted to 36 shapes of 70 to 8192 tokens, K 512 to 8192,
+// 2048 to 32003 outputs, of which it misses the fastest tile by 0.2 % on average
+// (at most 4 %). Measured on MI355X, INT8 / FP8 codes, us at K 4096:
+//   tokens, outputs  256x256  256x192  128x256  128x192  128x128  64x128
+//     256,  6144      45 / 44  38 / 39  30 / 30  23 / 20  19 / 17  16 / 15
+//     512,  6144      45 / 45  38 / 39  31 / 31  25 / 22  20 / 19  24 / 23
+//    1024,  6144      48 / 45  40 / 40  34 / 33  32 / 28  39 / 36  39 / 36
+//    1000,  8192      51 / 48  44 / 43  39 / 38  51 / 45  45 / 40  48 / 45
+//    1400,  6144      49 / 43  43 / 41  65 / 62  51 / 45  58 / 53  57 / 52
+//    3000,  4096      55 / 52  83 / 81  67 / 64  75 / 67  63 / 58  72 / 65
+// (64x128 fits twice on a unit.) FP8 products of one round of 64x128 take eight
+// wavefronts and five stages: 14.5 against 15.9, INT8 16.8 against 16.3.
+//
 // A launch that leaves compute units idle splits K where that saves more than
 // the second launch (1.5 us) and the partial sums (2.6 us a million) cost: 100,
 // 8192, 1024 takes 22 us in 16 tiles, 12 with K in four; 64, 8192, 4096: 12.8
 // with K in four, 16.0 in two, 14.4 in eight.
+//
+// The gated product has no tiles of 192 columns: a wavefront holds whole pairs
+// of gate and up runs, and there is no split of 192 columns into such.
 template <bool kGated>
 hipError_t pick(TiledLinear a, bool fp8, hipStream_t st) {
   auto tiles = [&](int bm, int bn) {
     return ((a.T + bm - 1) / bm) * (int64_t)((a.Np + bn - 1) / bn);
   };
+  auto rounds = [](int64_t n, double full, double lone, double more) {
+    const int64_t rest = n % 256;
+    return (double)(n / 256) * full + (rest ? lone + more * (double)rest / 256 : 0.0);
+  };
+  auto one = [](int64_t n) { return 0.28 + 0.12 * (n < 192 ? (double)n / 192 : 1.0); };
   const int D = a.Kp >> 7;
-  const int64_t t0 = tiles(256, 256), t1 = tiles(128, 256), t2 = tiles(64, 128);
-  const double c0 = (double)((t0 + 255) / 256) * 2.1, c1 = (double)((t1 + 255) / 256) * 1.1;
-  auto stage = [](int64_t n) { return 0.28 + 0.12 * (n < 192 ? (double)n / 192 : 1.0); };
-  const double c2 = t2 <= 256 ? stage(t2) : (double)((t2 + 511) / 512) * 0.8;
+  const int64_t t = tiles(64, 128), rest = t % 512;  // two tiles a compute unit
+  const double small =
+      (double)(t / 512) * 0.75 +
+      (rest > 256 ? 0.57 + 0.18 * (double)(rest - 256) / 256 : rest ? one(rest) : 0.0);
+  const double c0 = rounds(tiles(256, 256), 2.0, 1.25, 0.6);
+  const double c1 = kGated ? 1e30 : rounds(tiles(256, 192), 1.6, 1.0, 0.4);
+  const double c2 = rounds(tiles(128, 256), 1.15, 0.75, 0.35);
+  const double c3 = kGated ? 1e30 : rounds(tiles(128, 192), 0.9, 0.52, 0.34);
+  const double c4 = rounds(tiles(128, 128), 0.66, 0.36, 0.26);
+  auto least = [&](double c) {
+    return c <= c0 && c <= c1 && c <= c2 && c <= c3 && c <= c4 && c <= small;
+  };
   a.split = 1;
-  if (c0 <= c1 && c0 <= c2) return run<4, 2, 2, 4, 2, kGated, false>(a, fp8, st);
-  if (c1 <= c2) return run<2, 4, 2, 2, 2, kGated, false>(a, fp8, st);
-  double best = D * c2;
-  for (int s = 2; s <= 8 && t2 * s <= 256 && D >= 2 * s; ++s) {
+  if (least(c0)) return run<4, 2, 2, 4, 2, kGated>(a, fp8, st);
+  if (least(c2)) return run<2, 4, 2, 2, 2, kGated>(a, fp8, st);
+  if constexpr (kGated) {
+    if (least(c4)) return run<4, 2, 1, 2, 4, kGated>(a, fp8, st);
+  } else {
+    if (least(c1)) return run<4, 2, 2, 3, 2, kGated>(a, fp8, st);
+    if (least(c3)) return run<4, 2, 1, 3, 3, kGated>(a, fp8, st);
+    if (least(c4)) return run<2, 4, 2, 1, 3, kGated>(a, fp8, st);
+  }
+  double best = D * small;
+  for (int s = 2; s <= 8 && t * s <= 256 && D >= 2 * s; ++s) {
     const double sums = (double)s * (double)a.T * a.Np;
-    const double us = (double)D / s * stage(t2 * s) + 1.5 + sums * 2.6e-6;
+    const double us = (double)D / s * one(t * s) + 1.5 + sums * 2.6e-6;
     if (us < best && sums * 4.0 <= (double)kPartialBytes) {
       best = us;
       a.split = s;
     }
   }
-  if (a.split == 1) return run<2, 2, 1, 2, 3, kGated, false>(a, fp8, st);
-  const hipError_t e = run<2, 2, 1, 2, 3, kGated, true>(a, fp8, st);
-  return e == hipSuccess ? join<kGated>(a, fp8, st) : e;
+  if (a.split > 1) {
+    const hipError_t e = run<2, 2, 1, 2, 3, kGated, true>(a, fp8, st);
+    return e == hipSuccess ? join<kGated>(a, fp8, st) : e;
+  }
+  if constexpr (!kGated) {
+    if (fp8 && t <= 256) return run_as<2, 4, 1, 1, 5, true, false, false>(a, st);
+  }
+  return run<2, 2, 1, 2, 3, kGated>(a, fp8, st);
 }
 
 }  // namespace
