@@ -201,12 +201,16 @@ class _Product:
             act.s = _vector(codes[1], "code scales", T, dev)
             if act.s is None and T > 0:
                 _fail("codes come with their scales")
-        if out is None:
-            out = torch.empty(T, N, dtype=out_dtype or _BF16, device=dev)
-        elif out_dtype is not None and out.dtype != out_dtype:
-            _fail("out must be %s, got %s" % (out_dtype, out.dtype))
         res = _m.moe_w8a8_result()
-        res.out, res.ld_out = _rows(out, "out", _OUT_TYPES, T, N, dev)
+        if out is None:
+            if out_dtype is not None and out_dtype not in _OUT_TYPES:
+                _fail("out_dtype must be bfloat16 or float32, got %s" % out_dtype)
+            out = torch.empty(T, N, dtype=out_dtype or _BF16, device=dev)
+            res.out, res.ld_out = out.data_ptr(), N
+        else:
+            res.out, res.ld_out = _rows(out, "out", _OUT_TYPES, T, N, dev)
+            if out_dtype is not None and out.dtype != out_dtype:
+                _fail("out must be %s, got %s" % (out_dtype, out.dtype))
         res.out_type = 1 if out.dtype == _F32 else 0
         if gate is not None:
             res.gate = _vector(gate, "gate", T, dev)
