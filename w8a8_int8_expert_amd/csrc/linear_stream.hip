@@ -14,7 +14,7 @@
 // meet in LDS, and the wavefronts share the epilogue. INT8 sums are exact; FP8
 // sums are added in wavefront order.
 //
-// Up to four tokens the kernel codes the rows itself (kSrc 1: bf16 tokens, 2:
+// Up to four tokens the kernel codes the rows itself (kTokens: bf16 tokens, kHidden:
 // the feed-forward's hidden rows, from its gate and up values): every block
 // does it over again, which costs less than a launch of its own, and the
 // weights' first loads are in flight meanwhile.
