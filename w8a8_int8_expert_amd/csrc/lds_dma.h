@@ -1,6 +1,6 @@
 // lds_dma.h -- device building blocks shared by the tiled matrix products: direct
-// global -> LDS loads, the wait that goes with them, and the epilogue's SwiGLU
-// and row maximum. Included by the HIP sources only.
+// global -> LDS loads, the wait that goes with them, the epilogue's SwiGLU and
+// row maximum, and the conversion of e4m3 codes. Included by the HIP sources only.
 #pragma once
 
 #include "moe_internal.h"
@@ -56,6 +56,16 @@ __device__ __forceinline__ uint32_t half_wave_max(uint32_t m) {
 // silu(g) * u with the hardware exponential and reciprocal.
 __device__ __forceinline__ float swiglu(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+// Eight e4m3 codes as bf16 (exact: three mantissa bits, exponents of -9 to 8).
+__device__ __forceinline__ v8bf codes_bf16(int lo, int hi) {
+  const auto a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+  const auto b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  const auto c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+  const auto d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
 // Accumulators: INT32 for INT8 codes, fp32 for FP8 codes.

@@ -41,16 +41,6 @@ struct StreamArgs {
 template <bool kF8> struct Acc16v { typedef v4i T; };
 template <> struct Acc16v<true> { typedef v4f T; };
 
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-// Eight e4m3 codes as bf16 (exact: three mantissa bits, exponents of -9 to 8).
-__device__ __forceinline__ v8bf codes_bf16(int lo, int hi) {
-  const auto a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-  const auto b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-  const auto c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-  const auto d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
-  return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
 template <int RT, int NPW, int W, int U, bool kF8, int kSrc>
 __global__ __launch_bounds__(64 * W) void linear_stream_kernel(const StreamArgs a) {
   typedef typename Acc16v<kF8>::T Acc;
