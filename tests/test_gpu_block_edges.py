@@ -79,3 +79,55 @@ def test_ffn_fp8_hidden_codes(lib, T, H, F):
     err = err + 2 * R.U * R.pitch(F) * (qh.abs() @ qd.double().abs().t()) * scale
     err = err + (flip @ qd.double().abs().t()) * scale + y.abs() * rel[:, None]
     R.check(out, *R.finish(y, err, F32), "ffn")
+
+
+# ------------------------------------------------------------------- norms
+@pytest.mark.parametrize("kind", ["rms"])
+@pytest.mark.parametrize("H", [7, 900, 4096, 5000, 8191, 20001, 40000, 65536])
+def test_norm_of_the_largest_values_at_every_width(lib, kind, H):
+    """Rows of values near the largest bf16, of one sign or both, and of powers of
+    two up to 2^127, normalise as any other: their squares do not leave
+    the range."""
+    T = 7
+    g = torch.Generator().manual_seed(H)
+    sign = (torch.randint(0, 2, (T, H), generator=g) * 2 - 1).float()
+    y = 3.38e38 * (1 - 0.2 * torch.rand(T, H, generator=g)) * sign
+    y[1] = 2.0 ** 127 * sign[1]
+    y[2] = 2.0 ** 110 * torch.randn(H, generator=g)
+    y[3] = 3.38e38 * torch.where(torch.arange(H) % 10 == 0, -1.0, 1.0)  # far from its mean
+    y[4] = tokens(1, H, H)[0].float()
+    y[5] = y[5].abs() * torch.where(torch.arange(H) == H // 2, -1.0, 1.0)
+    y[6] = 2.0 ** 64 * torch.randn(H, generator=g)
+    y = y.to(BF)
+    w = vec(H, 1)
+    o = lib.add_norm(y.cuda(), None, norm=kind, weight=w.cuda(), codes="int8")
+    c = dict(norm=kind, post="none", eps=1e-6, bs=1.0, rs=1.0, w=w)
+    _, _, n, en = add_norm64(y, None, c)
+    R.check(o.normed, n, en + R.half_step(BF) * (n.abs() + en) + 1e-44, kind)
+    assert bool(torch.isfinite(o.scales).all()) and bool((o.scales > 0).all())
+    # an fp32 residual up to the last fp32 value, and the post norm
+    res = torch.full((T, H), torch.finfo(F32).max) * sign
+    o = lib.add_norm(torch.zeros_like(y).cuda(), res.cuda(), norm=kind, weight=w.cuda())
+    _, _, n, en = add_norm64(torch.zeros_like(y), res, c)
+    R.check(o.normed, n, en + R.half_step(BF) * (n.abs() + en) + 1e-44, kind + " fp32")
+    o = lib.add_norm(y.cuda(), None, norm="none", post_norm=kind, post_weight=w.cuda())
+    c = dict(norm="none", post=kind, eps=1e-6, bs=1.0, rs=1.0, pw=w)
+    _, _, n, en = add_norm64(y, None, c)
+    R.check(o.normed, n, en + R.half_step(BF) * (n.abs() + en) + 1e-44, kind + " post")
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_norm_with_the_largest_eps(lib, kind):
+    """eps beside which a row is small, up to the last fp32 value."""
+    T, H = 3, 700
+    y = tokens(T, H, 1).float()
+    y[1] *= 2.0 ** 60
+    y[2] *= 2.0 ** 100
+    y = y.to(BF)
+    w = torch.full((H,), 2.0 ** 60)
+    for eps in (1.0, 1e30, 2.0 ** 127, torch.finfo(F32).max):
+        o = lib.add_norm(y.cuda(), None, norm=kind, weight=w.cuda(), eps=eps)
+        c = dict(norm=kind, post="none", eps=eps, bs=1.0, rs=1.0, w=w)
+        _, _, n, en = add_norm64(y, None, c)
+        # (below the bf16 range a rounding is half of 2^-133)
+        R.check(o.normed, n, en + R.half_step(BF) * (n.abs() + en) + 2.0 ** -134, str(eps))

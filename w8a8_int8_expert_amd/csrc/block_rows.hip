@@ -127,7 +127,7 @@ __global__ __launch_bounds__(256) void clear_kernel(uint32_t *__restrict__ p, in
 
 // ----------------------------------------------------------------- add_norm
 // v = norm(v) for the row in v (elements past H are zero, and stay zero but for a
-// bias). Three cell rows.
+// bias). Four cell rows; a second use of one lies behind the barrier of another.
 template <int TPR, int NC, bool kOdd>
 __device__ __forceinline__ void norm_row(float (&v)[NC][8], int kind, const float *w,
                                          const float *b, int H, float eps, int lane,
@@ -135,46 +135,54 @@ __device__ __forceinline__ void norm_row(float (&v)[NC][8], int kind, const floa
   typedef RowGroup<TPR> G;
   if (kind == MOE_W8A8_NORM_NONE) return;
   const float width = (float)H;
-  auto centre = [&]() {
-    // (the mean as a sum of quotients: it stays in range where the sum would not)
+  const bool layer = kind == MOE_W8A8_NORM_LAYER;
+  // (the mean as a sum of quotients: it stays in range where the sum would not)
+  auto mean_of = [&](float *slot) {
     const float inv = 1.0f / width;
     float a = 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) a = __builtin_fmaf(v[i][j], inv, a);
-    const float mean = G::sum(a, cells);
+    return G::sum(a, slot);
+  };
+  auto centre = [&](float mean) {
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         v[i][j] = (lane + i * TPR) * 8 + j < H ? v[i][j] - mean : 0.0f;
   };
-  if (kind == MOE_W8A8_NORM_LAYER) centre();
   auto squares = [&](float *slot) {
     float a = 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) a = __builtin_fmaf(v[i][j], v[i][j], a);
-    return G::sum(a, slot);
+    return G::sum(a, slot) / width;
   };
-  float ms = squares(cells + G::kWaves) / width;
-  // Squares that leave the fp32 range: a row of values past 2^64 is taken down by
-  // 2^70, one whose squares (and eps) lie below 2^-90 is taken up by 2^100, exactly
-  // but for what is too small to matter, and eps with it. The mean of such a small
-  // row may have lost bits to a subnormal: what that left is taken off again (its
-  // cells are free: every thread has read them before the barrier since).
-  const bool large = ms > 0x1p127f;
-  if (large || ms + eps < 0x1p-90f) {
-    const float f = large ? 0x1p-70f : 0x1p100f;
+  // Rows at the ends of the fp32 range are scaled by a power of two, exactly but for
+  // what is too small to matter, and eps with the square of it (an eps stays one:
+  // zeros keep their norm). Down by 2^80: 65536 squares of 2^48 stay below 2^113.
+  auto scale = [&](float f) {
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] *= f;
-    if (kind == MOE_W8A8_NORM_LAYER && !large) centre();
-    ms = squares(cells + 2 * G::kWaves) / width;
-    eps = eps * f * f;
+    if (eps > 0.0f) eps = __builtin_fmaxf(eps * f * f, 0x1p-126f);
+  };
+  const float mean = layer ? mean_of(cells) : 0.0f;
+  if (layer) centre(mean);
+  float ms = squares(cells + 2 * G::kWaves);
+  // Squares that leave the range: down as above, or, where they (and eps) lie below
+  // 2^-90, up by 2^100. The mean of such a small row may have lost bits to a
+  // subnormal: what that left is taken off again.
+  const bool large = ms + eps > 0x1p127f, small = ms + eps < 0x1p-90f;
+  const bool again = layer && small;
+  if (large || small) {
+    scale(large ? 0x1p-80f : 0x1p100f);
+    if (again) centre(mean_of(cells + 3 * G::kWaves));
+    ms = squares(cells + G::kWaves);
   }
   const float rstd = 1.0f / __builtin_sqrtf(ms + eps);
 #pragma unroll
@@ -201,7 +209,7 @@ template <int TPR, int NC, bool kOdd>
 __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void add_norm_kernel(
     const moe_w8a8_add_norm_args a, int64_t T) {
   typedef RowGroup<TPR> G;
-  __shared__ float cells[7][G::kWaves];
+  __shared__ float cells[9][G::kWaves];
   const int lane = threadIdx.x % TPR;
   const int64_t t = (int64_t)blockIdx.x * G::kRows + threadIdx.x / TPR;
   if (t >= T) return;  // as in act_rows_kernel
@@ -248,7 +256,7 @@ __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void add_norm_kernel(
     }
   }
   if (!a.normed && !a.q) return;  // uniform over the grid
-  norm_row<TPR, NC, kOdd>(v, a.pre_norm, a.pre_weight, a.pre_bias, H, a.eps, lane, cells[3]);
+  norm_row<TPR, NC, kOdd>(v, a.pre_norm, a.pre_weight, a.pre_bias, H, a.eps, lane, cells[4]);
   if (a.normed) {
 #pragma unroll
     for (int i = 0; i < NC; ++i)
@@ -272,7 +280,7 @@ __global__ __launch_bounds__(RowGroup<TPR>::kThreads) void add_norm_kernel(
       m = umax(m, abs_bits(v[i][j]));
     }
   }
-  m = G::max_bits(m, cells[6]);
+  m = G::max_bits(m, cells[8]);
   emit_codes<TPR, NC>(v, lane, t, row_pitch(H), m, a.format == MOE_W8A8_FORMAT_FP8, false, a.q,
                       a.s);
 }
