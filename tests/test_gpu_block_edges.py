@@ -82,12 +82,12 @@ def test_ffn_fp8_hidden_codes(lib, T, H, F):
 
 
 # ------------------------------------------------------------------- norms
-@pytest.mark.parametrize("kind", ["rms"])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
 @pytest.mark.parametrize("H", [7, 900, 4096, 5000, 8191, 20001, 40000, 65536])
 def test_norm_of_the_largest_values_at_every_width(lib, kind, H):
     """Rows of values near the largest bf16, of one sign or both, and of powers of
-    two up to 2^127, normalise as any other: their squares do not leave
-    the range."""
+    two up to 2^127, normalise as any other: neither their squares nor their
+    differences from the mean leave the range."""
     T = 7
     g = torch.Generator().manual_seed(H)
     sign = (torch.randint(0, 2, (T, H), generator=g) * 2 - 1).float()

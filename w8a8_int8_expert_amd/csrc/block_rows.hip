@@ -163,7 +163,8 @@ __device__ __forceinline__ void norm_row(float (&v)[NC][8], int kind, const floa
   };
   // Rows at the ends of the fp32 range are scaled by a power of two, exactly but for
   // what is too small to matter, and eps with the square of it (an eps stays one:
-  // zeros keep their norm). Down by 2^80: 65536 squares of 2^48 stay below 2^113.
+  // zeros keep their norm). Down by 2^80: 65536 squares of 2^49 (a difference from
+  // the mean at most) stay below 2^114.
   auto scale = [&](float f) {
 #pragma unroll
     for (int i = 0; i < NC; ++i)
@@ -171,13 +172,18 @@ __device__ __forceinline__ void norm_row(float (&v)[NC][8], int kind, const floa
       for (int j = 0; j < 8; ++j) v[i][j] *= f;
     if (eps > 0.0f) eps = __builtin_fmaxf(eps * f * f, 0x1p-126f);
   };
-  const float mean = layer ? mean_of(cells) : 0.0f;
+  float mean = layer ? mean_of(cells) : 0.0f;
+  const bool far = __builtin_fabsf(mean) > 0x1p100f;  // a difference may pass the range
+  if (far) {
+    scale(0x1p-80f);
+    mean = mean_of(cells + G::kWaves);
+  }
   if (layer) centre(mean);
   float ms = squares(cells + 2 * G::kWaves);
   // Squares that leave the range: down as above, or, where they (and eps) lie below
   // 2^-90, up by 2^100. The mean of such a small row may have lost bits to a
   // subnormal: what that left is taken off again.
-  const bool large = ms + eps > 0x1p127f, small = ms + eps < 0x1p-90f;
+  const bool large = !far && ms + eps > 0x1p127f, small = !far && ms + eps < 0x1p-90f;
   const bool again = layer && small;
   if (large || small) {
     scale(large ? 0x1p-80f : 0x1p100f);
