@@ -131,3 +131,19 @@ def test_norm_with_the_largest_eps(lib, kind):
         _, _, n, en = add_norm64(y, None, c)
         # (below the bf16 range a rounding is half of 2^-133)
         R.check(o.normed, n, en + R.half_step(BF) * (n.abs() + en) + 2.0 ** -134, str(eps))
+
+
+@pytest.mark.parametrize("H", [1, 5, 700, 2047, 4099, 20001])
+def test_layer_norm_of_constant_rows(lib, H):
+    """A row of one value has a layer norm of zero whatever the value. The mean's
+    rounding (92 u of it, by the chains of its sum) is taken off with the mean of
+    what it leaves: 92 u of 92 u |c| remain, and the rounding of that difference."""
+    cs = torch.tensor([0.0, 1.0, -3.3, 1000.7, 30001.0, -123456.7, 1e-3, 7e6])
+    res = cs[:, None].expand(8, H).contiguous()
+    b, eps = vec(H, 3), 1e-6
+    zero = torch.zeros(8, H, dtype=BF)
+    for r in (res, res.to(BF)):
+        o = lib.add_norm(zero.cuda(), r.cuda(), norm="layer", bias=b.cuda(), eps=eps)
+        left = (93 * 92 * R.U ** 2 * cs.double().abs() / eps ** 0.5)[:, None]
+        want = b.double()[None, :].expand(8, H)
+        R.check(o.normed, want, left + (R.half_step(BF) + R.U) * (want + left), "constant")

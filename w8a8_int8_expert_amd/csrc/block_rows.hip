@@ -181,12 +181,13 @@ __device__ __forceinline__ void norm_row(float (&v)[NC][8], int kind, const floa
   if (layer) centre(mean);
   float ms = squares(cells + 2 * G::kWaves);
   // Squares that leave the range: down as above, or, where they (and eps) lie below
-  // 2^-90, up by 2^100. The mean of such a small row may have lost bits to a
-  // subnormal: what that left is taken off again.
+  // 2^-90, up by 2^100. The mean is off by its rounding, which is no small part of a
+  // row that spreads over less than 2^-10 of it, or lies that low: the mean of what
+  // is left is taken off again.
   const bool large = !far && ms + eps > 0x1p127f, small = !far && ms + eps < 0x1p-90f;
-  const bool again = layer && small;
-  if (large || small) {
-    scale(large ? 0x1p-80f : 0x1p100f);
+  const bool again = layer && !large && (small || ms < mean * mean * 0x1p-20f);
+  if (large || small || again) {
+    if (large || small) scale(large ? 0x1p-80f : 0x1p100f);
     if (again) centre(mean_of(cells + 3 * G::kWaves));
     ms = squares(cells + G::kWaves);
   }
