@@ -147,3 +147,77 @@ def test_layer_norm_of_constant_rows(lib, H):
         left = (93 * 92 * R.U ** 2 * cs.double().abs() / eps ** 0.5)[:, None]
         want = b.double()[None, :].expand(8, H)
         R.check(o.normed, want, left + (R.half_step(BF) + R.U) * (want + left), "constant")
+
+
+# ---------------------------------------------------------------- captured calls
+@pytest.mark.parametrize("T", [3, 20, 50, 90])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_captured_calls_follow_reloads_with_and_without_vectors(lib, T, fp8):
+    """A captured product or feed-forward block gives what an eager call of the
+    weights loaded now gives, whichever of smoothing and bias they have; what a
+    captured call went without can no longer be loaded, and the refusal changes
+    nothing."""
+    K, F, N = 300, 70, 60
+    say("[reloads]", T, fp8)
+    x = tokens(T, K, 1).cuda()
+
+    def build():
+        return lib.W8A8Linear(K, N, fp8=fp8), lib.W8A8FFN(K, F, out_features=N, fp8=fp8)
+
+    def load(ops, s):
+        w, inv, bias = s
+        ops[0].load_quantized(w[0], w[1], inv_smooth=inv, bias=bias)
+        ops[1].load_quantized(*w[2:], inv_smooth=inv, bias=bias)
+    sets, want = [], []
+    for i, (smooth, bias) in enumerate([(1, 1), (0, 0), (1, 0), (0, 1)]):
+        w = [cu(t) for j, shape in enumerate([(N, K), (2 * F, K), (N, F)])
+             for t in weight(*shape, fp8, 10 * i + j)]
+        sets.append((w, cu(vec(K, i)) if smooth else None, cu(vec(N, i)) if bias else None))
+        ops = build()
+        load(ops, sets[-1])
+        want.append([op(x) for op in ops])
+    for first, s in enumerate(sets):
+        ops = build()
+        load(ops, s)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = [op(x) for op in ops]
+        last = first
+        for k in (0, 1, 2, 3, 1, 0):
+            fits = all(now is None or then is not None for now, then in zip(sets[k][1:], s[1:]))
+            if fits:
+                load(ops, sets[k])
+                last = k
+            else:
+                for i, op in enumerate(ops):
+                    w = sets[k][0]
+                    with pytest.raises(lib.MoEW8A8Error, match="captured"):
+                        op.load_quantized(*(w[2:] if i else w[:2]), inv_smooth=sets[k][1],
+                                          bias=sets[k][2])
+            graph.replay()
+            torch.cuda.synchronize()
+            for op, got, right in zip(ops, out, want[last]):
+                assert torch.equal(got, right) and torch.equal(op(x), right)
+
+
+def test_smoothing_loaded_after_a_capture_from_codes(lib):
+    """A captured call that was given codes does not use the smoothing: it may
+    come later."""
+    K, N = 200, 40
+    lin = lib.W8A8Linear(K, N)
+    w, s = weight(N, K, False, 1)
+    lin.load_quantized(w.cuda(), s.cuda())
+    codes = lib.act_quant(tokens(5, K, 2).cuda())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = lin(codes=codes)
+    w2, s2 = weight(N, K, False, 3)
+    lin.load_quantized(w2.cuda(), s2.cuda(), inv_smooth=vec(K, 1).cuda())
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, lin(codes=codes))
+    with pytest.raises(lib.MoEW8A8Error, match="captured"):
+        lin.load_quantized(w.cuda(), s.cuda(), bias=vec(N, 1).cuda())

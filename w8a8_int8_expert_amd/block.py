@@ -32,6 +32,8 @@ _NORMS = {None: 0, "none": 0, "rms": 1, "layer": 2}
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
     torch._C, "_cuda_getCurrentRawStream") else \
     (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing",
+                     torch.cuda.is_current_stream_capturing)
 
 
 def _fail(msg):
@@ -45,17 +47,20 @@ def _device(device):
     return device
 
 
-def _call(name, device, *args):
-    """One library call with `device` current, on torch's current stream of it."""
+def _call(name, device, *args, captured=None):
+    """One library call with `device` current, on torch's current stream of it;
+    `captured` is called after it where the call was captured into a graph."""
     if device.type != "cuda":
         _fail("the operands must be on a GPU")
     f = getattr(_m._lib or _m.load_library(), name)
     i = device.index
     if torch.cuda.current_device() == i:
         rc = f(*args, _raw_stream(i))
+        if captured is not None and _capturing():
+            captured()
     else:
         with torch.cuda.device(i):
-            rc = f(*args, _raw_stream(i))
+            return _call(name, device, *args, captured=captured)
     if rc != 0:
         _m._check(rc, name)
 
@@ -114,7 +119,13 @@ def act_quant(x, inv_smooth=None, fp8: bool = False):
 
 class _Weights:
     """Packed codes and scales of one weight matrix, and the struct that names
-    them."""
+    them.
+
+    Its buffers have their places for good: a captured call follows what is loaded
+    later. Of the two optional vectors (the tokens' inv_smooth and the bias) it
+    keeps the places of those there were: one that a later load leaves out holds
+    ones or zeros from then on, and one that the captured call went without can no
+    longer be loaded."""
 
     def __init__(self, K, N, fp8, gated, device):
         size = _m.moe_w8a8_linear_codes_bytes(N, K, gated)
@@ -124,26 +135,41 @@ class _Weights:
         self.codes = torch.empty(size, dtype=_I8, device=device)
         self.scale = torch.empty(_m.moe_w8a8_linear_scales(N, gated), dtype=_F32,
                                  device=device)
-        # The optional vectors have a place of their own for good: a captured
-        # call keeps their addresses, whatever is loaded later.
         self.inv_smooth = torch.empty(K, dtype=_F32, device=device)
         self.bias = torch.empty(N, dtype=_F32, device=device)
         self.struct = _m.moe_w8a8_linear_weights(K, N, int(fp8), int(gated),
                                                  self.codes.data_ptr(), self.scale.data_ptr(),
                                                  None, None)
         self.ref = ctypes.byref(self.struct)
+        self.without = set()  # what a captured call went without
+
+    def captured(self, coded):
+        """A call was captured (`coded`: of tokens that it codes itself)."""
+        if self.struct.bias is None:
+            self.without.add("bias")
+        if coded and self.struct.inv_smooth is None:
+            self.without.add("smoothing")
+
+    def _check_vectors(self, smoothing, bias):
+        for name, t in (("smoothing", smoothing), ("bias", bias)):
+            if t is not None and name in self.without:
+                _fail("a call of this operator without %s was captured into a graph, which would "
+                      "go on without: load these weights into a new operator" % name)
 
     def vectors(self, inv_smooth, bias):
         """Copy the two optional vectors in; None turns one off."""
-        for name, t, n in (("inv_smooth", inv_smooth, self.K), ("bias", bias, self.N)):
+        for name, t, none in (("inv_smooth", inv_smooth, 1.0), ("bias", bias, 0.0)):
             own = getattr(self, name)
-            if t is not None:
-                own.copy_(t.detach().reshape(n))
+            if t is None:
+                own.fill_(none)
+            else:
+                own.copy_(t.detach().reshape(own.shape))
             setattr(self.struct, name, None if t is None else own.data_ptr())
 
     # The checks stand apart, so that a call that has several things to load
     # refuses before it has changed any of them.
     def check_source(self, w, smooth, bias):
+        self._check_vectors(smooth, bias)
         _vector(bias, "bias", self.N, self.device)
         return (*_rows(w, "weight", (_BF16, _F32), self.N, self.K, self.device),
                 _vector(smooth, "smooth", self.K, self.device))
@@ -155,6 +181,7 @@ class _Weights:
         self.vectors(None if smooth is None else 1.0 / smooth, bias)
 
     def check_codes(self, q, s, inv_smooth, bias):
+        self._check_vectors(inv_smooth, bias)
         _vector(bias, "bias", self.N, self.device)
         _vector(inv_smooth, "inv_smooth", self.K, self.device)
         types = (_E4M3, _I8) if self.fp8 else (_I8,)  # int8: e4m3 bytes, as the layer takes them
@@ -181,6 +208,14 @@ class _Product:
                 self._sizes.clear()
             n = self._sizes[T] = self._size(T)
         return n, torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+
+    def _captured(self):
+        for w in self._all:
+            w.captured(True)
+
+    def _captured_codes(self):
+        for w in self._all:
+            w.captured(False)
 
     def _operands(self, x, codes, K, N, add, gate, out, out_dtype):
         dev = self.device
@@ -222,13 +257,16 @@ class _Product:
 class W8A8Linear(_Product):
     """y = x . W^T in W8A8: INT8 (or, with fp8=True, e4m3) codes with a scale
     per token and per output channel. Fill it with quantise() or
-    load_quantized(), then call forward()."""
+    load_quantized(), then call forward(). Captured calls follow later loads; a
+    load that brings smoothing or a bias which a captured call went without is
+    refused."""
 
     def __init__(self, in_features: int, out_features: int, device="cuda", fp8: bool = False):
         _m.load_library()
         self.in_features, self.out_features = int(in_features), int(out_features)
         self.fp8, self.device = bool(fp8), _device(device)
         self._w = _Weights(self.in_features, self.out_features, self.fp8, False, self.device)
+        self._all = (self._w,)
         self._sizes = {}
 
     def _size(self, T):
@@ -254,7 +292,8 @@ class W8A8Linear(_Product):
                                           gate, out, out_dtype)
         n, ws = self._workspace(T)
         _call("moe_w8a8_linear", self.device, self._w.ref, ctypes.byref(act), T,
-              ctypes.byref(res), ws.data_ptr() if n else None, n)
+              ctypes.byref(res), ws.data_ptr() if n else None, n,
+              captured=self._captured if codes is None else self._captured_codes)
         return out
 
     __call__ = forward
@@ -262,7 +301,7 @@ class W8A8Linear(_Product):
 
 class W8A8FFN(_Product):
     """Gated feed-forward block in W8A8: down(silu(gate(x)) * up(x)), the hidden
-    rows requantised per token."""
+    rows requantised per token. Loads and captured calls as W8A8Linear."""
 
     def __init__(self, hidden: int, ffn: int, device="cuda", fp8: bool = False,
                  out_features: Optional[int] = None):
@@ -272,6 +311,7 @@ class W8A8FFN(_Product):
         self.fp8, self.device = bool(fp8), _device(device)
         self._gu = _Weights(self.hidden, 2 * self.ffn, self.fp8, True, self.device)
         self._dn = _Weights(self.ffn, self.out_features, self.fp8, False, self.device)
+        self._all = (self._gu, self._dn)
         self._sizes = {}
 
     def _size(self, T):
@@ -299,7 +339,8 @@ class W8A8FFN(_Product):
                                           out, out_dtype)
         n, ws = self._workspace(T)
         _call("moe_w8a8_ffn", self.device, self._gu.ref, self._dn.ref, ctypes.byref(act), T,
-              ctypes.byref(res), ws.data_ptr() if n else None, n)
+              ctypes.byref(res), ws.data_ptr() if n else None, n,
+              captured=self._captured if codes is None else self._captured_codes)
         return out
 
     __call__ = forward
