@@ -51,6 +51,28 @@ def test_fp8_sums_kept_in_fp32(lib, T, K, N):
         R.check(y, want, R.fp8_sum_bound(q, w) + R.half_step(BF) * want.abs() * (1 + 1e-3), "bf16")
 
 
+@pytest.mark.parametrize("T,K,N", [(1, 4096, 4096), (1, 8192, 100), (4, 4096, 300), (2, 8192, 48),
+                                   (1, 4100, 8000), (1, 4096, 16500), (3, 1000, 20000),
+                                   (4, 300, 70), (4, 8192, 70), (5, 4096, 9000), (16, 4096, 300),
+                                   (32, 4096, 9000), (40, 4096, 5000), (64, 4200, 500),
+                                   (70, 2000, 300), (300, 512, 1000)])
+def test_fp8_sums_from_tokens_and_from_codes(lib, T, K, N):
+    """The order of a sum depends on the sizes only: a product of tokens and one of
+    their codes give the same bits, FP8 included, and so do feed-forward blocks."""
+    say("[same sums]", T, K, N)
+    x, (w, sw) = tokens(T, K, seed_of(T, K)).cuda(), weight(N, K, True, seed_of(T, K, N))
+    lin = lib.W8A8Linear(K, N, fp8=True)
+    lin.load_quantized(w.cuda(), sw.cuda())
+    codes = lib.act_quant(x, fp8=True)
+    assert torch.equal(lin(x, out_dtype=F32), lin(codes=codes, out_dtype=F32))
+    assert torch.equal(lin(x), lin(codes=codes))
+    F = N // 2
+    ffn = lib.W8A8FFN(K, F, out_features=33, fp8=True)
+    wd, sd = weight(33, F, True, N)
+    ffn.load_quantized(w[:2 * F].cuda(), sw[:2 * F].cuda(), wd.cuda(), sd.cuda())
+    assert torch.equal(ffn(x, out_dtype=F32), ffn(codes=codes, out_dtype=F32))
+
+
 @pytest.mark.parametrize("T,H,F", [(3, 256, 100), (24, 512, 2100), (64, 300, 130), (65, 128, 64),
                                    (70, 2500, 300), (100, 1024, 1000), (300, 300, 257),
                                    (700, 256, 1000), (2100, 128, 2100)])

@@ -86,17 +86,6 @@ Epilogue epilogue(const moe_w8a8_linear_weights &w, const moe_w8a8_result &r) {
   return e;
 }
 
-// Rows that a streaming product codes itself, every block over again: tokens,
-// and the hidden rows of a feed-forward block (twice the values to read, and
-// SwiGLU to compute).
-constexpr int kFusedTokens = 16384, kFusedHidden = 8192;
-bool fused_tokens(int64_t T, int K) {
-  return T <= kFusedRows && T * row_pitch(K) <= kFusedTokens;
-}
-bool fused_hidden(int64_t T, int F) {
-  return T <= kFusedRows && T * row_pitch(F) <= kFusedHidden;
-}
-
 // Room for codes of T rows, row-major or in tiles.
 size_t codes_bytes(int64_t T, int K) { return (size_t)((T + 15) / 16 * 16) * row_pitch(K); }
 

@@ -67,8 +67,17 @@ inline bool streams(int64_t T, int K, int Np) {
   if (T > kStreamRows) return false;
   return K <= 4096 && Np <= 8192;
 }
-// Largest batch whose rows a streaming product codes itself.
+// Rows that a streaming product codes itself, every block over again: tokens,
+// and the hidden rows of a feed-forward block (twice the values to read, and
+// SwiGLU to compute).
 constexpr int kFusedRows = 4;
+constexpr int kFusedTokens = 16384, kFusedHidden = 8192;
+inline bool fused_tokens(int64_t T, int K) {
+  return T <= kFusedRows && T * row_pitch(K) <= kFusedTokens;
+}
+inline bool fused_hidden(int64_t T, int F) {
+  return T <= kFusedRows && T * row_pitch(F) <= kFusedHidden;
+}
 // Partial sums of the products that split K over blocks.
 constexpr size_t kPartialBytes = (size_t)32 << 20;
 

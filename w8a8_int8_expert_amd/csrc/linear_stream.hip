@@ -288,15 +288,19 @@ hipError_t run(const StreamArgs &a, bool fp8, hipStream_t st) {
 template <int RT, int kSrc>
 hipError_t pick(const StreamArgs &a, bool fp8, hipStream_t st) {
   const int panels = a.Np / 16;
+  // A call that is given the codes of such few tokens takes the same number of
+  // wavefronts as one that codes them: it cuts K the same way, and FP8 sums are
+  // the same to the last bit.
+  bool fused = kSrc == kTokens || kSrc == kHidden;
+  if constexpr (kSrc == kCodes && RT == 1) fused = fused_tokens(a.T, a.K);
   if (panels <= 256) {
     // Rows coded by the block: more wavefronts share that work (one token,
     // 4096 outputs, K 4096: 5.6 with 16 wavefronts, 6.1 with 8).
-    if constexpr (kSrc == kTokens || kSrc == kHidden)
-      if (a.Kp >= 4096) return run<RT, 1, 16, 2, kSrc>(a, fp8, st);
+    if constexpr (kSrc != kTiles && RT == 1)
+      if (fused && a.Kp >= 4096) return run<RT, 1, 16, 2, kSrc>(a, fp8, st);
     return run<RT, 1, 8, 2, kSrc>(a, fp8, st);
   }
-  constexpr bool codes = kSrc == kCodes || kSrc == kTiles;
-  const bool four = codes && a.Kp >= 4096 ? panels > 512 : (!codes || RT > 1) && panels >= 1024;
+  const bool four = !fused && a.Kp >= 4096 ? panels > 512 : (fused || RT > 1) && panels >= 1024;
   if (!four) return run<RT, 2, 8, 2, kSrc>(a, fp8, st);
   return run<RT, 4, 4, 2, kSrc>(a, fp8, st);
 }
