@@ -301,8 +301,9 @@ hipError_t pick(const StreamArgs &a, bool fp8, hipStream_t st) {
     return run<RT, 1, 8, 2, kSrc>(a, fp8, st);
   }
   const bool four = !fused && a.Kp >= 4096 ? panels > 512 : (fused || RT > 1) && panels >= 1024;
-  if (!four) return run<RT, 2, 8, 2, kSrc>(a, fp8, st);
-  return run<RT, 4, 4, 2, kSrc>(a, fp8, st);
+  if constexpr (RT < 4)  // (33 tokens and more stream to 512 panels at most)
+    if (four) return run<RT, 4, 4, 2, kSrc>(a, fp8, st);
+  return run<RT, 2, 8, 2, kSrc>(a, fp8, st);
 }
 
 }  // namespace
