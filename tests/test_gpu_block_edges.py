@@ -5,10 +5,12 @@ import pytest
 import torch
 
 import block_ref as R
-from test_gpu_block_ops import (BF, E4, F32, add_norm64, cu, lib, say, seed_of, tokens,  # noqa: F401
-                                vec, weight)
+from test_gpu_block_ops import (BF, E4, F32, add_norm64, cu, lib, say,  # noqa: F401
+                                seed_of, test_linear, tokens, vec, weight)
 
 pytestmark = pytest.mark.gpu
+linear_case = test_linear
+del test_linear  # (its own cases run where it stands)
 
 
 # ----------------------------------------------------------------- FP8 sums
@@ -101,6 +103,82 @@ def test_ffn_fp8_hidden_codes(lib, T, H, F):
     err = err + 2 * R.U * R.pitch(F) * (qh.abs() @ qd.double().abs().t()) * scale
     err = err + (flip @ qd.double().abs().t()) * scale + y.abs() * rel[:, None]
     R.check(out, *R.finish(y, err, F32), "ffn")
+
+
+# ------------------------------------------------------- every streaming kernel
+# By rows (up to 16, 32, 64), wavefronts of one panel (16, 8), panels a block (1, 2,
+# 4) and source; each shape runs from tokens (coded by the kernel, or in tiles)
+# and from row-major codes.
+STREAM = [(1, 4096, 300), (1, 1000, 300), (1, 4096, 6000), (3, 1000, 9000), (2, 4096, 17000),
+          (3, 300, 20000),                                               # rows coded by the kernel
+          (4, 5000, 300), (4, 5000, 6000), (4, 5000, 9000),              # too wide for that
+          (9, 4096, 3000), (9, 4096, 6000), (16, 4200, 9000), (12, 600, 17000),
+          (20, 4096, 3000), (20, 4096, 6000), (32, 4200, 9000), (25, 2000, 9000), (32, 600, 17000),
+          (33, 4096, 3000), (40, 4096, 6000), (64, 1000, 8190)]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,K,N", STREAM)
+def test_streaming_kernels(lib, T, K, N, fp8):
+    linear_case(lib, T, K, N, fp8)
+
+
+@pytest.mark.parametrize("T,K,N", STREAM)
+def test_streaming_kernels_fp8_sums(lib, T, K, N):
+    test_fp8_sums_kept_in_fp32(lib, T, K, N)
+    q, w = wide_codes(T, K, 5), wide_codes(N, K, 6)
+    lin = lib.W8A8Linear(K, N, fp8=True)
+    lin.load_quantized(w.to(E4).cuda(), torch.ones(N).cuda())
+    y = lin(q.to(BF).cuda(), out_dtype=F32)  # (a row's largest is 448: its codes are itself)
+    assert torch.equal(y.cpu().double(), q.double() @ w.double().t())
+
+
+def ffn64(x, inv, qg, sg, qd, sd, fp8, loose_down):
+    """(y, bound) of a feed-forward block in 64 bits. FP8 sums add whole products:
+    K additions, each within one fp32 step of a partial sum; loose_down: those of the
+    down product by the FP8 instructions instead."""
+    F = qd.shape[1]
+    q, s = R.row_codes(R.smoothed(x, inv), fp8)
+
+    def product(q, s, w, sw, loose):
+        y, err = R.product(q, s, w, sw, fp8 and loose)
+        if fp8 and not loose:
+            sums = q.double().abs() @ w.double().abs().t()
+            err = err + 2 * R.U * R.pitch(w.shape[1]) * sums * (
+                s.double()[:, None] * sw.double()[None, :])
+        return y, err
+    gu, e = product(q, s, qg, sg, False)
+    h, herr = R.hidden(gu[:, :F], gu[:, F:], e[:, :F], e[:, F:])
+    qh, sh, flip, rel = R.requantised(h, herr, fp8)
+    y, err = product(qh, sh, qd, sd, loose_down)
+    moved = (flip @ qd.double().abs().t()) * (sh[:, None] * sd.double()[None, :])
+    return y, err + moved + y.abs() * rel[:, None]
+
+
+# Hidden rows coded by the down product's kernel: 8 and 16 wavefronts, one, two and
+# four panels; by a launch of their own, in streaming and tiled products.
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,H,F,N", [(1, 300, 700, 200), (1, 200, 5000, 100), (2, 128, 4000, 5000),
+                                     (1, 64, 8000, 17000), (3, 100, 300, 16400), (4, 64, 90, 6000),
+                                     (1, 300, 9000, 200), (7, 300, 2300, 90), (20, 256, 2300, 4200),
+                                     (32, 300, 130, 9000), (40, 300, 257, 130), (70, 300, 257, 66),
+                                     (300, 200, 300, 257), (700, 256, 500, 130)])
+def test_ffn_streaming_kernels_and_ordinary_codes(lib, T, H, F, N, fp8):
+    say("[ffn]", T, H, F, N, fp8)
+    seed = seed_of(T, H, F, N)
+    x, inv = tokens(T, H, seed), vec(H, seed)
+    (qg, sg), (qd, sd) = weight(2 * F, H, fp8, seed), weight(N, F, fp8, seed + 1)
+    ffn = lib.W8A8FFN(H, F, out_features=N, fp8=fp8)
+    bias, gate, add = vec(N, seed, -1, 1), vec(T, seed, -1, 1), tokens(T, N, seed + 9)
+    ffn.load_quantized(qg.cuda(), sg.cuda(), qd.cuda(), sd.cuda(), inv_smooth=inv.cuda(),
+                       bias=bias.cuda())
+    f = ffn(x.cuda(), out_dtype=F32)
+    out = ffn(x.cuda(), add=add.cuda(), gate=gate.cuda())
+    for got, loose, dt, kw in ((f, False, F32, {}), (out, T > 32, BF, dict(gate=gate, add=add))):
+        y, err = ffn64(x, inv, qg.float(), sg, qd.float(), sd, fp8, loose)
+        y = y + bias.double()
+        err = err + R.U * y.abs()
+        R.check(got, *R.finish(y, err, dt, **kw), str(dt))
 
 
 # ------------------------------------------------------------------- norms
