@@ -321,3 +321,39 @@ def test_smoothing_loaded_after_a_capture_from_codes(lib):
         assert torch.equal(out, lin(codes=codes))
     with pytest.raises(lib.MoEW8A8Error, match="captured"):
         lin.load_quantized(w.cuda(), s.cuda(), bias=vec(N, 1).cuda())
+
+
+# ------------------------------------------------- kernels that the rest passes by
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,K", [(2049, 4096), (2050, 2051), (2049, 8192), (2100, 4103), (2, 33001),
+                                 (1, 65533)])
+def test_act_quant_many_rows(lib, T, K, fp8):
+    """More than 2048 rows of 2049 to 8192 columns take two chunks a thread."""
+    x, inv = tokens(T, K, seed_of(T, K)), vec(K, K)
+    q, s = lib.act_quant(x.cuda(), inv.cuda(), fp8=fp8)
+    want, ws = R.row_codes(R.smoothed(x, inv), fp8)
+    got = q.cpu().float()
+    assert torch.equal(got[:, :K], want) and torch.equal(s.cpu(), ws) and not got[:, K:].any()
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("T,H", [(3, 2051), (5, 4095), (2, 32769), (1, 40001), (1, 65535)])
+def test_add_norm_odd_wide_rows(lib, T, H, kind):
+    y, res = tokens(T, H, H), tokens(T, H, H + 1)
+    w, b = vec(H, 1), vec(H, 2, -1, 1)
+    o = lib.add_norm(y.cuda(), res.cuda(), norm=kind, weight=w.cuda(), bias=b.cuda(), eps=1e-5)
+    c = dict(norm=kind, post="none", eps=1e-5, bs=1.0, rs=1.0, w=w, b=b)
+    r, e, n, en = add_norm64(y, res, c)
+    R.check(o.residual, r, e * (1 + 4 * R.U) + R.half_step(BF) * (r.abs() + e) + 1e-44, "r")
+    R.check(o.normed, n, en + R.half_step(BF) * (n.abs() + en) + 1e-44, "n")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_small_tiles_two_a_unit(lib, fp8):
+    """64 x 128 tiles, more than one a compute unit."""
+    linear_case(lib, 393, 200, 8873, fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_ffn_hidden_rows_of_middle_width(lib, fp8):
+    test_ffn_streaming_kernels_and_ordinary_codes(lib, 20, 256, 1000, 90, fp8)
