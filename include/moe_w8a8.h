@@ -413,7 +413,8 @@ int64_t moe_w8a8_linear_scales(int32_t N, int32_t gated);
 /* Fill out->w and out->scale from unquantised weights: src fp32 (src_type
  * MOE_W8A8_F32) or bf16 (MOE_W8A8_BF16) [N][K] with row pitch ld_src. Rows are
  * multiplied by smooth (fp32 [K], or NULL) in fp32, then coded per row by the
- * rule above (a row with a NaN or an infinity gets codes 0 and scale NaN). */
+ * rule above (a row with a NaN or an infinity gets codes 0 and scale NaN). The
+ * buffers filled overlap neither src nor smooth (nor, below, src_scale). */
 #define MOE_W8A8_BF16 0
 #define MOE_W8A8_F32 1
 int moe_w8a8_linear_quantise(const moe_w8a8_linear_weights *out, const void *src,

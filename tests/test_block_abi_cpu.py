@@ -260,3 +260,22 @@ def test_codes_of_the_other_format_are_refused():
                 op.forward(codes=(wrong, s))
             with pytest.raises(m.MoEW8A8Error, match="GPU"):   # nothing else is wrong
                 op.forward(codes=(right, s))
+
+
+def test_weight_sources_over_their_destination_are_refused():
+    """Filling a weight matrix reads its source twice and in another order than it
+    writes: no source may share a byte with the codes or the scales filled."""
+    N, K = 70, 300
+    w = weights(w=FAR, scale=2 * FAR)
+    codes, scales = m.moe_w8a8_linear_codes_bytes(N, K), 4 * m.moe_w8a8_linear_scales(N)
+    for t, size in ((0, 2), (1, 4)):
+        span = N * K * size
+        for src in (FAR, FAR + codes - size, FAR - span + size, 2 * FAR, 2 * FAR + scales - size,
+                    2 * FAR - span + size):
+            assert m.moe_w8a8_linear_quantise(w, src, t, K, None, stream=0) == INV
+    for sm in (FAR, FAR + codes - 4, 2 * FAR - K * 4 + 4):
+        assert m.moe_w8a8_linear_quantise(w, 3 * FAR, 1, K, sm, stream=0) == INV
+    for src in (FAR, FAR + codes - 1, 2 * FAR - N * K + 1, 2 * FAR + scales - 1):
+        assert m.moe_w8a8_linear_pack(w, src, K, 3 * FAR, stream=0) == INV
+    for s in (FAR, FAR + codes - 4, 2 * FAR + scales - 4):
+        assert m.moe_w8a8_linear_pack(w, 3 * FAR, K, s, stream=0) == INV

@@ -52,6 +52,12 @@ int weights_check(const moe_w8a8_linear_weights *w) {
   if (!width_ok(w->in_features) || !outputs_ok(w->out_features)) return MOE_W8A8_ERR_UNSUPPORTED;
   return MOE_W8A8_OK;
 }
+// Whether m shares a byte with packed codes or scales.
+bool over_weights(const moe_w8a8_linear_weights &w, const Mat &m) {
+  const size_t rows = (size_t)packed_rows(w.out_features, w.gated != 0);
+  return overlap(m, flat(w.w, rows * row_pitch(w.in_features))) ||
+         overlap(m, flat(w.scale, rows * 4));
+}
 int act_check(const moe_w8a8_act *a, int64_t K) {
   if (!a) return MOE_W8A8_ERR_INVALID;
   const bool x = a->x != nullptr, q = a->q != nullptr || a->s != nullptr;
@@ -172,6 +178,10 @@ extern "C" int moe_w8a8_linear_quantise(const moe_w8a8_linear_weights *out, cons
   if (!src || !type_ok(src_type) || !al(src, src_type == MOE_W8A8_F32 ? 4 : 2) ||
       !al(smooth, 4) || !pitch_ok(ld_src, out->in_features))
     return MOE_W8A8_ERR_INVALID;
+  if (over_weights(*out, mat(src, out->out_features, ld_src, out->in_features,
+                             src_type == MOE_W8A8_F32 ? 4 : 2)) ||
+      over_weights(*out, flat(smooth, (size_t)out->in_features * 4)))
+    return MOE_W8A8_ERR_INVALID;
   MOE_CHECK(launch_pack_rows(*out, src, src_type, ld_src, smooth, nullptr, (hipStream_t)stream));
   return MOE_W8A8_OK;
 }
@@ -181,11 +191,8 @@ extern "C" int moe_w8a8_linear_pack(const moe_w8a8_linear_weights *out, const in
   MOE_TRY(weights_check(out));
   if (!src || !src_scale || !al(src_scale, 4) || !pitch_ok(ld_src, out->in_features))
     return MOE_W8A8_ERR_INVALID;
-  const int N = out->out_features;
-  const size_t scales = (size_t)packed_rows(N, out->gated != 0);
-  if (overlap(mat(src, N, ld_src, out->in_features, 1),
-              flat(out->w, scales * row_pitch(out->in_features))) ||
-      overlap(flat(src_scale, (size_t)N * 4), flat(out->scale, scales * 4)))
+  if (over_weights(*out, mat(src, out->out_features, ld_src, out->in_features, 1)) ||
+      over_weights(*out, flat(src_scale, (size_t)out->out_features * 4)))
     return MOE_W8A8_ERR_INVALID;
   MOE_CHECK(launch_pack_rows(*out, src, -1, ld_src, nullptr, src_scale, (hipStream_t)stream));
   return MOE_W8A8_OK;
