@@ -443,8 +443,8 @@ typedef struct {
  *   gate  fp32 [T], or NULL (1);
  *   add   bf16 [T][N], row pitch ld_add, or NULL (0). May be `out` itself
  *         (out_type MOE_W8A8_BF16 and ld_add == ld_out); otherwise it must not
- *         overlap it. `out` overlaps no other input (column blocks of one
- *         buffer with one pitch do not overlap). */
+ *         overlap it. `out` overlaps no other input, the weights' buffers
+ *         included (column blocks of one buffer with one pitch do not overlap). */
 typedef struct {
   void *out;
   int64_t ld_out;
@@ -455,8 +455,8 @@ typedef struct {
 } moe_w8a8_result;
 
 /* Per-token codes of bf16 rows x[T][K] (row pitch ld_x) in `format`, after
- * multiplying by inv_smooth (fp32 [K], or NULL): q [T][Kp], s fp32 [T]. One
- * launch, no workspace. Errors: MOE_W8A8_ERR_INVALID, MOE_W8A8_ERR_UNSUPPORTED
+ * multiplying by inv_smooth (fp32 [K], or NULL): q [T][Kp], s fp32 [T], which
+ * overlap neither an input nor each other. One launch, no workspace. Errors: MOE_W8A8_ERR_INVALID, MOE_W8A8_ERR_UNSUPPORTED
  * (K outside [1, 65536]), MOE_W8A8_ERR_HIP. */
 int moe_w8a8_act_quant(int32_t K, int32_t format, const uint16_t *x, int64_t ld_x, int64_t T,
                        const float *inv_smooth, int8_t *q, float *s, void *stream);

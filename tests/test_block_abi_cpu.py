@@ -279,3 +279,25 @@ def test_weight_sources_over_their_destination_are_refused():
         assert m.moe_w8a8_linear_pack(w, src, K, 3 * FAR, stream=0) == INV
     for s in (FAR, FAR + codes - 4, 2 * FAR + scales - 4):
         assert m.moe_w8a8_linear_pack(w, 3 * FAR, K, s, stream=0) == INV
+
+
+def test_results_over_the_weights_are_refused():
+    """A result that shares a byte with a buffer of the weights would change the
+    weights while other blocks still read them."""
+    N, K = 70, 300
+    codes, scales = m.moe_w8a8_linear_codes_bytes(N, K), 4 * m.moe_w8a8_linear_scales(N)
+    at = [(8 + i) * FAR for i in range(4)]
+    w = weights(w=at[0], scale=at[1], inv=at[2], bias=at[3])
+    ends = [(at[0], codes), (at[1], scales), (at[2], 4 * K), (at[3], 4 * N)]
+    out_bytes = 4 * N * 2                                   # T = 4 rows of bf16
+    for p, size in ends:
+        for o in (p, p + size - 2, p - out_bytes + 2):
+            assert linear(w=w, r=result(out=o)) == INV
+    gu, dn = weights(K=K, N=64, gated=1), weights(K=32, N=N, w=at[0], scale=at[1], bias=at[3])
+    gu2 = weights(K=K, N=64, gated=1, w=at[0], scale=at[1], inv=at[2])
+    plain = weights(K=32, N=N)
+    for g, d, ps in ((gu, dn, (at[0], at[1], at[3])), (gu2, plain, (at[0], at[1], at[2]))):
+        for p in ps:
+            assert m.moe_w8a8_ffn(g, d, act(), 4, result(out=p), 2 * FAR, 1 << 40, stream=0) == INV
+    for q, s in ((FAR, 2 * FAR), (FAR - 4 * 384 + 16, 2 * FAR), (3 * FAR, FAR + 4 * K - 4)):
+        assert m.moe_w8a8_act_quant(K, 0, FAKE, K, 4, FAR, q, s, stream=0) == INV

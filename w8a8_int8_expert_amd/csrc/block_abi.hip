@@ -52,11 +52,15 @@ int weights_check(const moe_w8a8_linear_weights *w) {
   if (!width_ok(w->in_features) || !outputs_ok(w->out_features)) return MOE_W8A8_ERR_UNSUPPORTED;
   return MOE_W8A8_OK;
 }
-// Whether m shares a byte with packed codes or scales.
+// Whether m shares a byte with packed codes or scales; with anything of the weights.
 bool over_weights(const moe_w8a8_linear_weights &w, const Mat &m) {
   const size_t rows = (size_t)packed_rows(w.out_features, w.gated != 0);
   return overlap(m, flat(w.w, rows * row_pitch(w.in_features))) ||
          overlap(m, flat(w.scale, rows * 4));
+}
+bool over_any(const moe_w8a8_linear_weights &w, const Mat &m) {
+  return over_weights(w, m) || overlap(m, flat(w.inv_smooth, (size_t)w.in_features * 4)) ||
+         overlap(m, flat(w.bias, (size_t)w.out_features * 4));
 }
 int act_check(const moe_w8a8_act *a, int64_t K) {
   if (!a) return MOE_W8A8_ERR_INVALID;
@@ -69,7 +73,10 @@ int act_check(const moe_w8a8_act *a, int64_t K) {
 Mat act_mat(const moe_w8a8_act *a, int64_t T, int K) {
   return a->x ? mat(a->x, T, a->ld_x, K, 2) : mat(a->q, T, row_pitch(K), row_pitch(K), 1);
 }
-int result_check(const moe_w8a8_result *r, const moe_w8a8_act *act, int64_t T, int K, int64_t N) {
+int result_check(const moe_w8a8_result *r, const moe_w8a8_act *act, int64_t T,
+                 const moe_w8a8_linear_weights &in, const moe_w8a8_linear_weights &last) {
+  const int K = in.in_features;
+  const int64_t N = last.out_features;
   if (!r || !r->out || !type_ok(r->out_type)) return MOE_W8A8_ERR_INVALID;
   const size_t size = r->out_type == MOE_W8A8_F32 ? 4 : 2;
   if (!al(r->out, size) || !pitch_ok(r->ld_out, N) || !al(r->gate, 4)) return MOE_W8A8_ERR_INVALID;
@@ -80,7 +87,8 @@ int result_check(const moe_w8a8_result *r, const moe_w8a8_act *act, int64_t T, i
     if (!same && overlap(out, mat(r->add, T, r->ld_add, N, 2))) return MOE_W8A8_ERR_INVALID;
   }
   if (overlap(out, act_mat(act, T, K)) || overlap(out, flat(act->s, (size_t)T * 4)) ||
-      overlap(out, flat(r->gate, (size_t)T * 4)))
+      overlap(out, flat(r->gate, (size_t)T * 4)) || over_any(in, out) ||
+      (&last != &in && over_any(last, out)))
     return MOE_W8A8_ERR_INVALID;
   return MOE_W8A8_OK;
 }
@@ -209,7 +217,8 @@ extern "C" int moe_w8a8_act_quant(int32_t K, int32_t format, const uint16_t *x, 
     return MOE_W8A8_ERR_INVALID;
   const Mat xm = mat(x, T, ld_x, K, 2), qm = flat(q, (size_t)T * row_pitch(K)),
             sm = flat(s, (size_t)T * 4);
-  if (overlap(xm, qm) || overlap(xm, sm) || overlap(qm, sm))
+  const Mat im = flat(inv_smooth, (size_t)K * 4);
+  if (overlap(xm, qm) || overlap(xm, sm) || overlap(qm, sm) || overlap(im, qm) || overlap(im, sm))
     return MOE_W8A8_ERR_INVALID;
   MOE_CHECK(launch_act_rows(x, ld_x, T, K, inv_smooth, format == MOE_W8A8_FORMAT_FP8, false, q, s,
                             nullptr, (hipStream_t)stream));
@@ -230,7 +239,7 @@ extern "C" int moe_w8a8_linear(const moe_w8a8_linear_weights *w, const moe_w8a8_
   if (T == 0) return MOE_W8A8_OK;
   const int K = w->in_features;
   MOE_TRY(act_check(act, K));
-  MOE_TRY(result_check(res, act, T, K, w->out_features));
+  MOE_TRY(result_check(res, act, T, *w, *w));
   const LinearLayout L = linear_layout(K, T);
   if (!al(workspace, 256)) return MOE_W8A8_ERR_INVALID;
   if (L.total > 0 && (!workspace || workspace_bytes < L.total)) return MOE_W8A8_ERR_WORKSPACE;
@@ -271,7 +280,7 @@ extern "C" int moe_w8a8_ffn(const moe_w8a8_linear_weights *gu, const moe_w8a8_li
   if (T == 0) return MOE_W8A8_OK;
   const int H = gu->in_features, F = dn->in_features;
   MOE_TRY(act_check(act, H));
-  MOE_TRY(result_check(res, act, T, H, dn->out_features));
+  MOE_TRY(result_check(res, act, T, *gu, *dn));
   const FfnLayout L = ffn_layout(H, F, T);
   if (!al(workspace, 256)) return MOE_W8A8_ERR_INVALID;
   if (!workspace || workspace_bytes < L.total) return MOE_W8A8_ERR_WORKSPACE;
