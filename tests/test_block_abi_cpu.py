@@ -301,3 +301,36 @@ def test_results_over_the_weights_are_refused():
             assert m.moe_w8a8_ffn(g, d, act(), 4, result(out=p), 2 * FAR, 1 << 40, stream=0) == INV
     for q, s in ((FAR, 2 * FAR), (FAR - 4 * 384 + 16, 2 * FAR), (3 * FAR, FAR + 4 * K - 4)):
         assert m.moe_w8a8_act_quant(K, 0, FAKE, K, 4, FAR, q, s, stream=0) == INV
+
+
+def far_rows(rows, width, dtype=torch.float32):
+    """A matrix whose rows lie further apart than the library takes (a view of a
+    storage that is never touched)."""
+    store = torch.empty(0, dtype=dtype, device="meta")
+    return store.new_empty((1,)).as_strided((rows, width), ((1 << 26) + 1, 1))
+
+
+def test_every_operand_is_checked_before_weights_change(monkeypatch):
+    """A pitch past the library's limit is refused with the other checks, before a
+    call that loads two matrices has filled the first."""
+    from w8a8_int8_expert_amd import block
+    called = []
+    monkeypatch.setattr(block, "_call", lambda name, *a, **k: called.append(name))
+    H, F, N = 64, 32, 5
+    meta = torch.device("meta")
+    lin, ffn = m.W8A8Linear(H, N, device=meta), m.W8A8FFN(H, F, device=meta, out_features=N)
+    z = lambda *s, d=torch.float32: torch.empty(*s, dtype=d, device=meta)  # noqa: E731
+    i8 = torch.int8
+    for call in (lambda: lin.quantise(far_rows(N, H)),
+                 lambda: lin.load_quantized(far_rows(N, H, i8), z(N)),
+                 lambda: ffn.quantise(z(2 * F, H), far_rows(N, F)),
+                 lambda: ffn.quantise(far_rows(2 * F, H), z(N, F)),
+                 lambda: ffn.load_quantized(z(2 * F, H, d=i8), z(2 * F), far_rows(N, F, i8), z(N)),
+                 lambda: lin(far_rows(3, H, BF)),
+                 lambda: ffn(z(3, H, d=BF), out=far_rows(3, N, BF)),
+                 lambda: m.add_norm(z(3, H, d=BF), far_rows(3, H, BF))):
+        with pytest.raises(m.MoEW8A8Error, match="too far apart"):
+            call()
+        assert not called
+    ffn.quantise(z(2 * F, H), z(N, F))
+    assert called == ["moe_w8a8_linear_quantise"] * 2

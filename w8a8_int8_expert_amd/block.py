@@ -26,6 +26,7 @@ _BF16, _F32, _I8, _E4M3 = torch.bfloat16, torch.float32, torch.int8, torch.float
 _OUT_TYPES, _ONLY_BF16 = (_BF16, _F32), (_BF16,)
 _FORMATS = {"int8": 0, "fp8": 1}
 _NORMS = {None: 0, "none": 0, "rms": 1, "layer": 2}
+_MAX_PITCH = 1 << 26  # elements, the library's limit
 # A call of one token is a few microseconds of GPU work: what the binding does
 # per call is kept as small. The stream's handle comes from the same function
 # that torch.cuda.current_stream wraps in an object.
@@ -82,6 +83,8 @@ def _rows(t, name, dtypes, T, width, device):
         ld = width
     elif ld < width:
         _fail("the rows of %s overlap (row stride %d for %d columns)" % (name, ld, width))
+    elif ld > _MAX_PITCH:
+        _fail("the rows of %s lie too far apart (row stride %d)" % (name, ld))
     return t.data_ptr(), ld
 
 
