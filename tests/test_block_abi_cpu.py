@@ -334,3 +334,16 @@ def test_every_operand_is_checked_before_weights_change(monkeypatch):
         assert not called
     ffn.quantise(z(2 * F, H), z(N, F))
     assert called == ["moe_w8a8_linear_quantise"] * 2
+
+
+def test_gate_group_of_any_size(monkeypatch):
+    """The group that reaches the library needs no more gate rows than there are,
+    whatever number was given: one past 64 bits does not wrap to a small one."""
+    from w8a8_int8_expert_amd import block
+    seen = []
+    monkeypatch.setattr(block, "_call", lambda name, dev, a, T, **k: seen.append(a._obj.gate_group))
+    T = 5
+    y, gate = torch.zeros(T, 70, dtype=BF), torch.zeros(1, 70, dtype=BF)
+    for group in (None, T, T + 1, 1 << 40, (1 << 64) + 1, (1 << 65) + 2):
+        m.add_norm(y, gate=gate, gate_group=group)
+        assert -(-T // seen[-1]) == 1, group

@@ -422,6 +422,7 @@ def add_norm(y, residual=None, norm="rms", weight=None, bias=None, eps: float = 
             group = -(-T // G) if gate_group is None else int(gate_group)
             if group < 1 or -(-T // group) > G:
                 _fail("gate has %d rows, too few for %d tokens in groups of %d" % (G, T, group))
+            group = min(group, T)  # (a number past 64 bits would wrap to another)
     if codes is not None:
         q, s = _empty_codes(T, H, codes == "fp8", dev)
     a = _m.moe_w8a8_add_norm_args(
