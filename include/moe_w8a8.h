@@ -456,8 +456,9 @@ typedef struct {
 
 /* Per-token codes of bf16 rows x[T][K] (row pitch ld_x) in `format`, after
  * multiplying by inv_smooth (fp32 [K], or NULL): q [T][Kp], s fp32 [T], which
- * overlap neither an input nor each other. One launch, no workspace. Errors: MOE_W8A8_ERR_INVALID, MOE_W8A8_ERR_UNSUPPORTED
- * (K outside [1, 65536]), MOE_W8A8_ERR_HIP. */
+ * overlap neither an input nor each other. One launch, no workspace. Errors:
+ * MOE_W8A8_ERR_INVALID, MOE_W8A8_ERR_UNSUPPORTED (K outside [1, 65536]),
+ * MOE_W8A8_ERR_HIP. */
 int moe_w8a8_act_quant(int32_t K, int32_t format, const uint16_t *x, int64_t ld_x, int64_t T,
                        const float *inv_smooth, int8_t *q, float *s, void *stream);
 

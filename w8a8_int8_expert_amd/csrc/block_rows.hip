@@ -420,8 +420,10 @@ hipError_t launch_act_rows(const uint16_t *x, int64_t ld, int64_t T, int K, cons
         K % 8 ? act_rows_kernel<TPR, NC, true> : act_rows_kernel<TPR, NC, false>, T, st, x, ld, T,
         K, inv, fp8, tiles, q, s, clear);
   };
-  // Many rows and one reduction: two chunks a thread, half the barriers
-  // (16384 x 4096: 34.4 us against 40.6, 8192 x 8192: 35.2 against 43.8).
+  // Many rows and one reduction: two chunks a thread, half the wavefronts that meet
+  // (us, without and with smoothing scales: 16384 x 4096 34.6, 41.3 against 45.6,
+  // 47.6; 8192 x 8192 33.8, 41.7 against 43.1, 48.6; 2100 x 4096 7.0, 8.5 against
+  // 8.0, 8.6).
   if (T > 2048 && K > 2048 && K <= 4096) return run(RowShape<256, 2>{});
   if (T > 2048 && K > 4096 && K <= 8192) return run(RowShape<512, 2>{});
   return by_width(K, run);

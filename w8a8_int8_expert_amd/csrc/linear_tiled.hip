@@ -512,8 +512,13 @@ hipError_t join(const TiledLinear &a, int mul, hipStream_t st) {
 //    1000,  8192      51 / 48  44 / 43  39 / 38  51 / 45  45 / 40  48 / 45
 //    1400,  6144      49 / 43  43 / 41  65 / 62  51 / 45  58 / 53  57 / 52
 //    3000,  4096      55 / 52  83 / 81  67 / 64  75 / 67  63 / 58  72 / 65
-// (64x128 fits twice on a unit.) FP8 products of one round of 64x128 take eight
-// wavefronts and five stages: 14.5 against 15.9, INT8 16.8 against 16.3.
+// (64x128 fits twice on a unit.) Products of one round of 64x128 on the FP8
+// instructions take eight wavefronts and five stages (us, against four and three;
+// tokens, K, outputs): 256, 512, 6144 6.1, 6.7; 200, 1024, 8192 7.8, 8.3; 1000, 1024,
+// 1500 7.2, 8.2; 300, 2048, 5000 9.4, 10.6; 100, 2048, 16384 10.3, 11.1; 256, 4096,
+// 6144 14.1, 15.0; 512, 8192, 4096 24.0, 24.7. INT8: 16.8, 16.3 (256, 4096, 6144).
+// FP8 codes multiplied as bf16 follow the same estimate: of 33 shapes of 40 to 16384
+// tokens the tile it names is at most 5 % behind the fastest.
 //
 // A launch that leaves compute units idle splits K where that saves more than
 // the second launch (1.5 us) and the partial sums (2.6 us a million) cost: 100,
