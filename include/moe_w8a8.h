@@ -463,7 +463,8 @@ int moe_w8a8_act_quant(int32_t K, int32_t format, const uint16_t *x, int64_t ld_
                        const float *inv_smooth, int8_t *q, float *s, void *stream);
 
 /* y[t][n] = s[t] * scale[n] * sum_k q[t][k] * w[n][k] + bias[n], then the
- * result's gate and add. INT8: the sum is exact (INT32). FP8: exact products
+ * result's gate and add: the sum times s[t] first, in fp32, so a sum that leaves
+ * the range there is infinite. INT8: the sum is exact (INT32). FP8: exact products
  * accumulated in fp32, except for bf16 results of more than 32 tokens. Those may
  * come from the FP8 matrix instructions, which keep the products of each eight
  * consecutive k (from a multiple of eight) to 13 bits below the largest of them

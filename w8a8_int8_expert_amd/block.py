@@ -53,17 +53,15 @@ def _call(name, device, *args, captured=None):
     `captured` is called after it where the call was captured into a graph."""
     if device.type != "cuda":
         _fail("the operands must be on a GPU")
-    f = getattr(_m._lib or _m.load_library(), name)
     i = device.index
-    if torch.cuda.current_device() == i:
-        rc = f(*args, _raw_stream(i))
-        if captured is not None and _capturing():
-            captured()
-    else:
+    if torch.cuda.current_device() != i:
         with torch.cuda.device(i):
             return _call(name, device, *args, captured=captured)
+    rc = getattr(_m._lib or _m.load_library(), name)(*args, _raw_stream(i))
     if rc != 0:
         _m._check(rc, name)
+    if captured is not None and _capturing():
+        captured()
 
 
 def _rows(t, name, dtypes, T, width, device):
