@@ -471,7 +471,8 @@ int moe_w8a8_act_quant(int32_t K, int32_t format, const uint16_t *x, int64_t ld_
  * (truncated) before they add them in fp32: a sum is then off by at most
  * 7 * 2^-13 times the sum of the groups' largest |q| * largest |w| (1.5e-5 of the
  * sums' rms on normal data) beside the fp32 roundings. The sum's order depends on
- * the shape (T, N, K) only. `workspace` holds at least
+ * the shape (T, N, K) and, for FP8, on out_type only: not on whether tokens or
+ * their codes are given. `workspace` holds at least
  * moe_w8a8_linear_workspace_size(N, K, T) bytes (NULL where that is 0).
  * Errors: MOE_W8A8_ERR_INVALID (NULL or misaligned pointer, T outside
  * [0, 2^22), bad pitch, format or types, overlap, gated weights),

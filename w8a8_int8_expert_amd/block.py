@@ -28,11 +28,13 @@ _FORMATS = {"int8": 0, "fp8": 1}
 _NORMS = {None: 0, "none": 0, "rms": 1, "layer": 2}
 _MAX_PITCH = 1 << 26  # elements, the library's limit
 # A call of one token is a few microseconds of GPU work: what the binding does
-# per call is kept as small. The stream's handle comes from the same function
-# that torch.cuda.current_stream wraps in an object.
+# per call is kept as small. The stream's handle, the current device and whether a
+# graph is being captured come from the functions that torch.cuda wraps (a call with
+# GPU operands finds torch.cuda initialised).
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
     torch._C, "_cuda_getCurrentRawStream") else \
     (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing",
                      torch.cuda.is_current_stream_capturing)
 
@@ -54,7 +56,7 @@ def _call(name, device, *args, captured=None):
     if device.type != "cuda":
         _fail("the operands must be on a GPU")
     i = device.index
-    if torch.cuda.current_device() != i:
+    if _current_device() != i:
         with torch.cuda.device(i):
             return _call(name, device, *args, captured=captured)
     rc = getattr(_m._lib or _m.load_library(), name)(*args, _raw_stream(i))
