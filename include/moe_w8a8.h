@@ -550,6 +550,155 @@ typedef struct {
 } moe_w8a8_add_norm_args;
 int moe_w8a8_add_norm(const moe_w8a8_add_norm_args *args, int64_t T, void *stream);
 
+/* ------------------------------------------- attention between the projections
+ * What lies between a block's QKV projection and its output projection, over a
+ * paged cache in the same quantisation, and what the LM head's logits answer:
+ *   moe_w8a8_qk_norm_rope      norms of queries and keys for each head and the
+ *                              position rotation in one pass; keys and values go
+ *                              into the cache;
+ *   moe_w8a8_paged_attention   attention of the batch's new tokens (one for each
+ *                              sequence, or chunks) over the cache;
+ *   moe_w8a8_token_logprobs    log probabilities of given tokens, entropy, top
+ *                              alternatives.
+ *
+ * A cache of keys and values in pages (device memory; the struct is host memory).
+ *   k, v         [num_pages][kv_heads][page_size][head_dim] in `format`: bf16, int8
+ *                or e4m3 bytes; 16-byte aligned. Each page is contiguous; page p
+ *                begins page_stride elements after page p - 1 (at least a page, a
+ *                multiple of 16), so that one buffer can hold many caches.
+ *   k_scale,     fp32 [num_pages][kv_heads][page_size], 16-byte aligned, pages
+ *   v_scale      scale_stride values apart (a multiple of 4): an element stands for
+ *                code * scale. NULL for a bf16 cache.
+ * Supported: head_dim 64, 128, 256; page_size 16, 32, 64, 128, 256; kv_heads up to
+ * 1024; num_pages from 1; strides up to 2^40. */
+#define MOE_W8A8_CACHE_BF16 2
+typedef struct {
+  int32_t num_pages, page_size, kv_heads, head_dim;
+  int32_t format; /* MOE_W8A8_CACHE_BF16, MOE_W8A8_FORMAT_INT8 or _FP8 */
+  void *k, *v;
+  int64_t page_stride;
+  float *k_scale, *v_scale;
+  int64_t scale_stride;
+} moe_w8a8_kv_cache;
+
+/* The sequences of a step (device memory, read when the kernels run: a captured
+ * call follows what is written there later).
+ *   cu_tokens   int32 [num_seqs + 1]: the new tokens of sequence b are token rows
+ *               cu_tokens[b] .. cu_tokens[b + 1] - 1. Values are taken into
+ *               [0, T], a sequence that ends before it begins has none. Rows behind
+ *               the last sequence are neither read nor written.
+ *   lengths     int32 [num_seqs]: keys of the sequence in the cache, its new tokens
+ *               (the last ones) included: new token i of n is at place
+ *               length - n + i. A token of negative place has no place in the
+ *               cache. Lengths are taken into [0, table_width * page_size].
+ *   page_table  int32 [num_seqs][table_width], pitch ld_table: place p of sequence b
+ *               lies in page page_table[b][p / page_size]. A page outside [0,
+ *               num_pages) holds nothing: its keys are not seen, and what is
+ *               written there is dropped.
+ *   max_tokens  the most new tokens of a sequence: a bound (tokens past it are not
+ *               computed).
+ *   max_length  about the longest length: it sizes the launch, a longer one is still
+ *               computed right. */
+typedef struct {
+  int32_t num_seqs, max_tokens, max_length, table_width;
+  const int32_t *cu_tokens, *lengths, *page_table;
+  int64_t ld_table;
+} moe_w8a8_batch;
+
+/* Queries and keys normed for each head and rotated by their position; keys and
+ * values written into the cache at their tokens' places. With D = head_dim, for each
+ * head row x[D] of the queries and of the keys, in fp32:
+ *   norm != 0:   x = x / sqrt(mean(x^2) + eps) * weight (q_weight or k_weight, fp32
+ *                [D], or NULL: 1)
+ *   rotary > 0:  for i < rotary / 2, with t = position * inv_freq[i] (in fp64):
+ *                (a, b) = (a cos t - b sin t, b cos t + a sin t), where (a, b) is
+ *                (x[i], x[i + rotary/2]), or, interleaved, (x[2i], x[2i + 1])
+ * and one rounding: queries and a bf16 cache to bf16, an INT8 or FP8 cache to codes of
+ * the D values with a scale of their own by the rule of the per-token codes above (a
+ * head row that holds a NaN or an infinity gets codes 0 and a NaN scale). Values are
+ * written as they are (or coded). No two tokens may have the same place.
+ *   qkv        bf16 [T][(heads + 2 kv_heads) D], pitch ld_qkv: query heads, key heads,
+ *              value heads
+ *   q          bf16 [T][heads D], pitch ld_q; may be `qkv` itself with the same pitch
+ *   inv_freq   fp64 [rotary / 2], not NULL where rotary > 0
+ *   positions  int64 [T], or NULL: each token's place
+ * q_weight and k_weight are NULL where norm is 0. `q` overlaps no other input and not
+ * the cache, nor does the cache overlap an input. Supported: heads up to 65536 / D,
+ * rotary a multiple of 16 up to D. One launch, no workspace. T below 2^22. Errors:
+ * MOE_W8A8_ERR_INVALID, MOE_W8A8_ERR_UNSUPPORTED, MOE_W8A8_ERR_HIP. T == 0 is a no-op. */
+typedef struct {
+  int32_t heads, norm, rotary, interleaved;
+  float eps;
+  const uint16_t *qkv;
+  int64_t ld_qkv;
+  uint16_t *q;
+  int64_t ld_q;
+  const float *q_weight, *k_weight;
+  const double *inv_freq;
+  const int64_t *positions;
+} moe_w8a8_qk_norm_rope_args;
+int moe_w8a8_qk_norm_rope(const moe_w8a8_qk_norm_rope_args *args, const moe_w8a8_kv_cache *cache,
+                          const moe_w8a8_batch *batch, int64_t T, void *stream);
+
+/* Attention of the new tokens over the cache. Query head j of `heads` reads kv head
+ * j / (heads / kv_heads). A token at place p sees the keys at places c < length with
+ * c <= p (causal) and c > p - window (window > 0), in pages that exist:
+ *   out = sum_c softmax_c(scale * q . k_c) v_c
+ * A token that sees no key gets zeros; keys and values that it does not see have no
+ * part in its result, whatever they hold. Products are exact and summed in fp32, the
+ * softmax is fp32, and each probability (times its value's scale) is rounded to bf16
+ * before it multiplies the values; the result is rounded once.
+ *   q    bf16 [T][heads D], pitch ld_q;  out  bf16 [T][heads D], pitch ld_out, which
+ *        overlaps neither q nor the cache nor the batch's arrays.
+ * Supported: heads a multiple of kv_heads up to 65536 / D; window >= 0 (0: none); scale
+ * finite. `workspace` holds at least moe_w8a8_paged_attention_workspace_size bytes
+ * (256-byte aligned; 0 for arguments that are refused). T below 2^22. Errors:
+ * MOE_W8A8_ERR_INVALID, MOE_W8A8_ERR_UNSUPPORTED, MOE_W8A8_ERR_WORKSPACE,
+ * MOE_W8A8_ERR_HIP. T == 0 is a no-op. */
+typedef struct {
+  int32_t heads, causal, window;
+  float scale;
+  const uint16_t *q;
+  int64_t ld_q;
+  uint16_t *out;
+  int64_t ld_out;
+} moe_w8a8_attention_args;
+size_t moe_w8a8_paged_attention_workspace_size(const moe_w8a8_kv_cache *cache,
+                                               const moe_w8a8_batch *batch, int32_t heads,
+                                               int64_t T);
+int moe_w8a8_paged_attention(const moe_w8a8_attention_args *args, const moe_w8a8_kv_cache *cache,
+                             const moe_w8a8_batch *batch, int64_t T, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* For each row x[V] of logits (bf16 or fp32, `type`), with z = log sum_j exp(x_j):
+ *   logprobs[t]      x[tokens[t]] - z (NaN for a token outside [0, V))
+ *   entropy[t]       z - sum_j exp(x_j - z) x_j
+ *   top_tokens[t][]  the `top` tokens of largest logit, in falling order, of equal
+ *                    ones the lower first; top_logprobs[t][]  their x - z
+ * in fp32, relative to the row's largest logit. Logits of -inf have probability 0. A row
+ * that holds a NaN or +inf, or nothing but -inf, has NaN results; its top tokens are
+ * still ordered (a NaN counts as larger than every number).
+ *   logits  [T][V], pitch ld;  tokens int64 [T], or NULL (then logprobs is NULL)
+ *   logprobs, entropy  fp32 [T], or NULL;  top_tokens int64, top_logprobs fp32
+ *           [T][top], both or neither (top 0)
+ * Supported: V in [1, 2^20], top in [0, min(V, 64)]. Outputs overlap neither an input
+ * nor each other. Workspace: moe_w8a8_token_logprobs_workspace_size bytes, 256-byte
+ * aligned (NULL where that is 0). T below 2^22. Errors: MOE_W8A8_ERR_INVALID,
+ * MOE_W8A8_ERR_UNSUPPORTED, MOE_W8A8_ERR_WORKSPACE, MOE_W8A8_ERR_HIP. T == 0 is a
+ * no-op. */
+typedef struct {
+  int32_t vocab, type, top; /* type: MOE_W8A8_BF16 or MOE_W8A8_F32 */
+  const void *logits;
+  int64_t ld;
+  const int64_t *tokens;
+  float *logprobs, *entropy;
+  int64_t *top_tokens;
+  float *top_logprobs;
+} moe_w8a8_logprobs_args;
+size_t moe_w8a8_token_logprobs_workspace_size(int32_t vocab, int32_t top, int64_t T);
+int moe_w8a8_token_logprobs(const moe_w8a8_logprobs_args *args, int64_t T, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
 /* Static description of a return code (never NULL). */
 const char *moe_w8a8_strerror(int code);
 

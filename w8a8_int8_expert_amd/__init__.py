@@ -26,6 +26,7 @@ MOE_W8A8_ERR_SCRATCH = -5
 MOE_W8A8_SCRATCH_BYTES = 64 << 20
 MOE_W8A8_FORMAT_INT8 = 0
 MOE_W8A8_FORMAT_FP8 = 1
+MOE_W8A8_CACHE_BF16 = 2
 
 _P = ctypes.c_void_p
 
@@ -75,6 +76,39 @@ class moe_w8a8_add_norm_args(ctypes.Structure):
                 ("ld_normed", ctypes.c_int64), ("inv_smooth", _P), ("q", _P), ("s", _P)]
 
 
+class moe_w8a8_kv_cache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("format", ctypes.c_int32), ("k", _P), ("v", _P), ("page_stride", ctypes.c_int64),
+                ("k_scale", _P), ("v_scale", _P), ("scale_stride", ctypes.c_int64)]
+
+
+class moe_w8a8_batch(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
+                ("max_length", ctypes.c_int32), ("table_width", ctypes.c_int32),
+                ("cu_tokens", _P), ("lengths", _P), ("page_table", _P),
+                ("ld_table", ctypes.c_int64)]
+
+
+class moe_w8a8_qk_norm_rope_args(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("norm", ctypes.c_int32), ("rotary", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float), ("qkv", _P),
+                ("ld_qkv", ctypes.c_int64), ("q", _P), ("ld_q", ctypes.c_int64),
+                ("q_weight", _P), ("k_weight", _P), ("inv_freq", _P), ("positions", _P)]
+
+
+class moe_w8a8_attention_args(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q", _P), ("ld_q", ctypes.c_int64), ("out", _P),
+                ("ld_out", ctypes.c_int64)]
+
+
+class moe_w8a8_logprobs_args(ctypes.Structure):
+    _fields_ = [("vocab", ctypes.c_int32), ("type", ctypes.c_int32), ("top", ctypes.c_int32),
+                ("logits", _P), ("ld", ctypes.c_int64), ("tokens", _P), ("logprobs", _P),
+                ("entropy", _P), ("top_tokens", _P), ("top_logprobs", _P)]
+
+
 STAGES = ("route", "scan", "scatter", "act_quant", "gemm1", "requant", "gemm2", "combine",
           "router")
 
@@ -85,7 +119,9 @@ EXPORTS = ("moe_w8a8_workspace_size", "moe_w8a8_calibrate", "moe_w8a8_calibrate_
            "moe_w8a8_linear_codes_bytes", "moe_w8a8_linear_scales", "moe_w8a8_linear_quantise",
            "moe_w8a8_linear_pack", "moe_w8a8_act_quant", "moe_w8a8_linear_workspace_size",
            "moe_w8a8_linear", "moe_w8a8_ffn_workspace_size", "moe_w8a8_ffn",
-           "moe_w8a8_add_norm")
+           "moe_w8a8_add_norm", "moe_w8a8_qk_norm_rope",
+           "moe_w8a8_paged_attention_workspace_size", "moe_w8a8_paged_attention",
+           "moe_w8a8_token_logprobs_workspace_size", "moe_w8a8_token_logprobs")
 
 _lib = None
 
@@ -128,6 +164,7 @@ def load_library(path: str = LIB_PATH):
     lib.moe_w8a8_pack.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P]
     LW, AC, RS = (ctypes.POINTER(c) for c in (moe_w8a8_linear_weights, moe_w8a8_act,
                                               moe_w8a8_result))
+    KC, BA = ctypes.POINTER(moe_w8a8_kv_cache), ctypes.POINTER(moe_w8a8_batch)
     i32, i64, size_t = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     for name, ret, args in (
             ("row_pitch", i64, [i32]), ("linear_codes_bytes", size_t, [i32, i32, i32]),
@@ -139,7 +176,15 @@ def load_library(path: str = LIB_PATH):
             ("linear", ctypes.c_int, [LW, AC, i64, RS, _P, size_t, _P]),
             ("ffn_workspace_size", size_t, [i32, i32, i32, i64]),
             ("ffn", ctypes.c_int, [LW, LW, AC, i64, RS, _P, size_t, _P]),
-            ("add_norm", ctypes.c_int, [ctypes.POINTER(moe_w8a8_add_norm_args), i64, _P])):
+            ("add_norm", ctypes.c_int, [ctypes.POINTER(moe_w8a8_add_norm_args), i64, _P]),
+            ("qk_norm_rope", ctypes.c_int,
+             [ctypes.POINTER(moe_w8a8_qk_norm_rope_args), KC, BA, i64, _P]),
+            ("paged_attention_workspace_size", size_t, [KC, BA, i32, i64]),
+            ("paged_attention", ctypes.c_int,
+             [ctypes.POINTER(moe_w8a8_attention_args), KC, BA, i64, _P, size_t, _P]),
+            ("token_logprobs_workspace_size", size_t, [i32, i32, i64]),
+            ("token_logprobs", ctypes.c_int,
+             [ctypes.POINTER(moe_w8a8_logprobs_args), i64, _P, size_t, _P])):
         f = getattr(lib, "moe_w8a8_" + name)
         f.restype, f.argtypes = ret, args
     lib.moe_w8a8_strerror.restype = ctypes.c_char_p
@@ -278,6 +323,36 @@ def moe_w8a8_ffn(gate_up: moe_w8a8_linear_weights, down: moe_w8a8_linear_weights
 
 def moe_w8a8_add_norm(args: moe_w8a8_add_norm_args, T, stream=None) -> int:
     return int(load_library().moe_w8a8_add_norm(ctypes.byref(args), T, _stream(stream)))
+
+
+def moe_w8a8_qk_norm_rope(args: moe_w8a8_qk_norm_rope_args, cache: moe_w8a8_kv_cache,
+                          batch: moe_w8a8_batch, T, stream=None) -> int:
+    return int(load_library().moe_w8a8_qk_norm_rope(
+        ctypes.byref(args), ctypes.byref(cache), ctypes.byref(batch), T, _stream(stream)))
+
+
+def moe_w8a8_paged_attention_workspace_size(cache: moe_w8a8_kv_cache, batch: moe_w8a8_batch,
+                                            heads: int, T: int) -> int:
+    return int(load_library().moe_w8a8_paged_attention_workspace_size(
+        ctypes.byref(cache), ctypes.byref(batch), heads, T))
+
+
+def moe_w8a8_paged_attention(args: moe_w8a8_attention_args, cache: moe_w8a8_kv_cache,
+                             batch: moe_w8a8_batch, T, workspace, workspace_bytes,
+                             stream=None) -> int:
+    return int(load_library().moe_w8a8_paged_attention(
+        ctypes.byref(args), ctypes.byref(cache), ctypes.byref(batch), T, _ptr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
+def moe_w8a8_token_logprobs_workspace_size(vocab: int, top: int, T: int) -> int:
+    return int(load_library().moe_w8a8_token_logprobs_workspace_size(vocab, top, T))
+
+
+def moe_w8a8_token_logprobs(args: moe_w8a8_logprobs_args, T, workspace, workspace_bytes,
+                            stream=None) -> int:
+    return int(load_library().moe_w8a8_token_logprobs(
+        ctypes.byref(args), T, _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 class MoEW8A8Error(RuntimeError):
@@ -480,13 +555,21 @@ class MoEW8A8:
 
 
 _BLOCK = ("AddNorm", "W8A8FFN", "W8A8Linear", "act_quant", "add_norm")
+_ATTENTION = ("KVCache", "SequenceBatch", "TokenLogprobs", "paged_attention", "qk_norm_rope",
+              "token_logprobs")
 
 
 def __getattr__(name):
-    """The block operators come from .block, which imports torch, on first use."""
+    """The block operators come from .block, those between its projections and behind
+    the LM head from .attention, which import torch, on first use."""
     if name in _BLOCK:
         from . import block
         for n in _BLOCK:
             globals()[n] = getattr(block, n)
+        return globals()[name]
+    if name in _ATTENTION:
+        from . import attention
+        for n in _ATTENTION:
+            globals()[n] = getattr(attention, n)
         return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -1,0 +1,249 @@
+// attention_abi.hip -- host side of moe_w8a8_qk_norm_rope, _paged_attention and
+// _token_logprobs: argument validation before anything touches HIP, workspace sizes
+// and the launches on the caller's stream.
+#include <math.h>
+
+#include "attention_internal.h"
+#include "host_checks.h"
+
+using namespace moe;
+
+namespace {
+
+constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int kMaxSeqs = 1 << 20;
+constexpr int kMaxTop = 64;
+constexpr int kMaxVocab = 1 << 20;
+
+int elem(const moe_w8a8_kv_cache &c) { return c.format == kBf16Cache ? 2 : 1; }
+int64_t page_elems(const moe_w8a8_kv_cache &c) {
+  return (int64_t)c.page_size * c.kv_heads * c.head_dim;
+}
+int log2_of(int v) {
+  int l = 0;
+  while (v >> (l + 1)) ++l;
+  return l;
+}
+
+// Shape and format (what the workspace depends on), without the pointers.
+int cache_shape(const moe_w8a8_kv_cache *c) {
+  if (!c || c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->head_dim < 1 ||
+      (c->format != kBf16Cache && !format_ok(c->format)))
+    return MOE_W8A8_ERR_INVALID;
+  if ((c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) || c->page_size < 16 ||
+      c->page_size > 256 || (c->page_size & (c->page_size - 1)) || c->kv_heads > 1024)
+    return MOE_W8A8_ERR_UNSUPPORTED;
+  return MOE_W8A8_OK;
+}
+int cache_check(const moe_w8a8_kv_cache *c) {
+  MOE_TRY(cache_shape(c));
+  if (!c->k || !c->v || !al(c->k, 16) || !al(c->v, 16) || c->page_stride < page_elems(*c) ||
+      c->page_stride > kMaxStride || c->page_stride % 16)
+    return MOE_W8A8_ERR_INVALID;
+  if (c->format == kBf16Cache)
+    return c->k_scale || c->v_scale ? MOE_W8A8_ERR_INVALID : MOE_W8A8_OK;
+  if (!c->k_scale || !c->v_scale || !al(c->k_scale, 16) || !al(c->v_scale, 16) ||
+      c->scale_stride < (int64_t)c->page_size * c->kv_heads || c->scale_stride > kMaxStride ||
+      c->scale_stride % 4)
+    return MOE_W8A8_ERR_INVALID;
+  return MOE_W8A8_OK;
+}
+int batch_shape(const moe_w8a8_batch *b) {
+  if (!b || b->num_seqs < 0 || b->max_tokens < 0 || b->max_length < 0 || b->table_width < 0)
+    return MOE_W8A8_ERR_INVALID;
+  return b->num_seqs > kMaxSeqs ? MOE_W8A8_ERR_UNSUPPORTED : MOE_W8A8_OK;
+}
+int batch_check(const moe_w8a8_batch *b) {
+  MOE_TRY(batch_shape(b));
+  if (b->num_seqs == 0) return MOE_W8A8_OK;
+  if (!b->cu_tokens || !b->lengths || !al(b->cu_tokens, 4) || !al(b->lengths, 4) ||
+      !al(b->page_table, 4) || (b->table_width > 0 && !b->page_table) ||
+      b->ld_table < b->table_width || b->ld_table > kMaxPitch)
+    return MOE_W8A8_ERR_INVALID;
+  return MOE_W8A8_OK;
+}
+
+// The cache's buffers, as their pages span them, and the batch's arrays.
+struct Buffers {
+  Mat m[7];
+};
+Buffers buffers(const moe_w8a8_kv_cache &c, const moe_w8a8_batch &b) {
+  Buffers r{};
+  auto pages = [&](const void *p, int64_t stride, int64_t each, size_t size) {
+    return mat(p, c.num_pages, stride, each, size);
+  };
+  r.m[0] = pages(c.k, c.page_stride, page_elems(c), elem(c));
+  r.m[1] = pages(c.v, c.page_stride, page_elems(c), elem(c));
+  if (c.k_scale) {
+    r.m[2] = pages(c.k_scale, c.scale_stride, (int64_t)c.page_size * c.kv_heads, 4);
+    r.m[3] = pages(c.v_scale, c.scale_stride, (int64_t)c.page_size * c.kv_heads, 4);
+  }
+  r.m[4] = flat(b.cu_tokens, ((size_t)b.num_seqs + 1) * 4);
+  r.m[5] = flat(b.lengths, (size_t)b.num_seqs * 4);
+  r.m[6] = mat(b.table_width ? b.page_table : nullptr, b.num_seqs, b.ld_table, b.table_width, 4);
+  return r;
+}
+
+CacheView view(const moe_w8a8_kv_cache &c) {
+  CacheView v{};
+  v.k = (char *)c.k; v.v = (char *)c.v; v.k_scale = c.k_scale; v.v_scale = c.v_scale;
+  v.page_bytes = c.page_stride * elem(c); v.scale_stride = c.scale_stride;
+  v.num_pages = c.num_pages; v.log2_page = log2_of(c.page_size); v.kv_heads = c.kv_heads;
+  return v;
+}
+BatchView view(const moe_w8a8_batch &b, int page_size, int64_t T) {
+  BatchView v{};
+  v.cu = b.cu_tokens; v.lengths = b.lengths; v.table = b.page_table; v.ld_table = b.ld_table;
+  v.num_seqs = b.num_seqs; v.T = (int)T;
+  // (no sequence has more new tokens than there are rows)
+  v.max_tokens = b.max_tokens < T ? b.max_tokens : (int)T;
+  const int64_t most = (int64_t)b.table_width * page_size, top = 0x7fffffff - 256;
+  v.most = (int)(most < top ? most : top);
+  return v;
+}
+bool heads_ok(int32_t heads, int D) { return heads <= kMaxWidth / D; }
+
+}  // namespace
+
+extern "C" int moe_w8a8_qk_norm_rope(const moe_w8a8_qk_norm_rope_args *a,
+                                     const moe_w8a8_kv_cache *c, const moe_w8a8_batch *b, int64_t T,
+                                     void *stream) {
+  if (!a || T < 0 || T > kMaxRows || a->heads < 1 || a->rotary < 0 || !isfinite(a->eps) ||
+      a->eps < 0.0f || (!a->norm && (a->q_weight || a->k_weight)))
+    return MOE_W8A8_ERR_INVALID;
+  MOE_TRY(cache_check(c));
+  MOE_TRY(batch_check(b));
+  const int D = c->head_dim;
+  if (!heads_ok(a->heads, D) || a->rotary > D || a->rotary % 16) return MOE_W8A8_ERR_UNSUPPORTED;
+  if (T == 0 || b->num_seqs == 0) return MOE_W8A8_OK;
+  const int64_t in = (int64_t)(a->heads + 2 * c->kv_heads) * D, out = (int64_t)a->heads * D;
+  if (!a->qkv || !a->q || !al(a->qkv, 2) || !al(a->q, 2) || !pitch_ok(a->ld_qkv, in) ||
+      !pitch_ok(a->ld_q, out) || !al(a->q_weight, 4) || !al(a->k_weight, 4) ||
+      (a->rotary > 0 && !a->inv_freq) || !al(a->inv_freq, 8) || !al(a->positions, 8))
+    return MOE_W8A8_ERR_INVALID;
+  const Mat q = mat(a->q, T, a->ld_q, out, 2), qkv = mat(a->qkv, T, a->ld_qkv, in, 2);
+  const Mat ins[4] = {flat(a->q_weight, (size_t)D * 4), flat(a->k_weight, (size_t)D * 4),
+                      flat(a->inv_freq, (size_t)a->rotary * 4),
+                      flat(a->positions, (size_t)T * 8)};
+  const bool in_place = a->q == a->qkv && a->ld_q == a->ld_qkv;
+  if (!in_place && overlap(q, qkv)) return MOE_W8A8_ERR_INVALID;
+  const Buffers bf = buffers(*c, *b);
+  for (const Mat &m : ins)
+    if (overlap(q, m)) return MOE_W8A8_ERR_INVALID;
+  for (int i = 0; i < 7; ++i) {
+    if (overlap(q, bf.m[i])) return MOE_W8A8_ERR_INVALID;
+    if (i >= 4) continue;
+    if (overlap(bf.m[i], qkv)) return MOE_W8A8_ERR_INVALID;
+    for (const Mat &m : ins)
+      if (overlap(bf.m[i], m)) return MOE_W8A8_ERR_INVALID;
+    for (int j = i + 1; j < 7; ++j)
+      if (overlap(bf.m[i], bf.m[j])) return MOE_W8A8_ERR_INVALID;
+  }
+  RopeArgs r{};
+  r.qkv = a->qkv; r.ld_qkv = a->ld_qkv; r.q = a->q; r.ld_q = a->ld_q;
+  r.q_weight = a->q_weight; r.k_weight = a->k_weight; r.inv_freq = a->inv_freq;
+  r.positions = a->positions; r.heads = a->heads; r.rotary = a->rotary;
+  r.norm = a->norm != 0; r.interleaved = a->interleaved != 0; r.eps = a->eps;
+  MOE_CHECK(launch_qk_norm_rope(r, view(*c), D, c->format, view(*b, c->page_size, T),
+                                (hipStream_t)stream));
+  return MOE_W8A8_OK;
+}
+
+namespace {
+// Checks of the shapes that the workspace depends on.
+int attention_shape(const moe_w8a8_kv_cache *c, const moe_w8a8_batch *b, int32_t heads,
+                    int64_t T) {
+  if (T < 0 || T > kMaxRows || heads < 1) return MOE_W8A8_ERR_INVALID;
+  MOE_TRY(cache_shape(c));
+  MOE_TRY(batch_shape(b));
+  if (!heads_ok(heads, c->head_dim) || heads % c->kv_heads) return MOE_W8A8_ERR_UNSUPPORTED;
+  return MOE_W8A8_OK;
+}
+AttnPlan plan_of(const moe_w8a8_kv_cache &c, const moe_w8a8_batch &b, int32_t heads, int64_t T) {
+  return attention_plan(view(c), c.head_dim, c.format, view(b, c.page_size, T), heads,
+                        b.max_length);
+}
+}  // namespace
+
+extern "C" size_t moe_w8a8_paged_attention_workspace_size(const moe_w8a8_kv_cache *c,
+                                                          const moe_w8a8_batch *b, int32_t heads,
+                                                          int64_t T) {
+  if (attention_shape(c, b, heads, T) != MOE_W8A8_OK) return 0;
+  if (T == 0 || b->num_seqs == 0 || b->max_tokens == 0) return 0;
+  return up256(plan_of(*c, *b, heads, T).partial);
+}
+
+extern "C" int moe_w8a8_paged_attention(const moe_w8a8_attention_args *a,
+                                        const moe_w8a8_kv_cache *c, const moe_w8a8_batch *b,
+                                        int64_t T, void *workspace, size_t workspace_bytes,
+                                        void *stream) {
+  if (!a || a->window < 0 || !isfinite(a->scale)) return MOE_W8A8_ERR_INVALID;
+  MOE_TRY(attention_shape(c, b, a->heads, T));
+  MOE_TRY(cache_check(c));
+  MOE_TRY(batch_check(b));
+  if (T == 0 || b->num_seqs == 0 || b->max_tokens == 0) return MOE_W8A8_OK;
+  const int D = c->head_dim;
+  const int64_t width = (int64_t)a->heads * D;
+  if (!a->q || !a->out || !al(a->q, 2) || !al(a->out, 2) || !pitch_ok(a->ld_q, width) ||
+      !pitch_ok(a->ld_out, width))
+    return MOE_W8A8_ERR_INVALID;
+  const Mat out = mat(a->out, T, a->ld_out, width, 2);
+  const AttnPlan p = plan_of(*c, *b, a->heads, T);
+  const Mat ws = flat(workspace, p.partial), q = mat(a->q, T, a->ld_q, width, 2);
+  if (!al(workspace, 256) || overlap(out, q) || overlap(ws, q) || overlap(ws, out))
+    return MOE_W8A8_ERR_INVALID;
+  const Buffers bf = buffers(*c, *b);
+  for (const Mat &m : bf.m)
+    if (overlap(out, m) || overlap(ws, m)) return MOE_W8A8_ERR_INVALID;
+  if (p.partial > 0 && (!workspace || workspace_bytes < p.partial)) return MOE_W8A8_ERR_WORKSPACE;
+  AttnArgs r{};
+  r.q = a->q; r.ld_q = a->ld_q; r.out = a->out; r.ld_out = a->ld_out;
+  r.heads = a->heads; r.group = a->heads / c->kv_heads; r.causal = a->causal != 0;
+  r.window = a->window; r.scale2 = a->scale * 1.44269504088896340736f;
+  MOE_CHECK(launch_attention(r, view(*c), D, c->format, view(*b, c->page_size, T), p,
+                             (float *)workspace, (hipStream_t)stream));
+  return MOE_W8A8_OK;
+}
+
+extern "C" size_t moe_w8a8_token_logprobs_workspace_size(int32_t V, int32_t top, int64_t T) {
+  (void)V;
+  (void)top;
+  (void)T;
+  return 0;
+}
+
+extern "C" int moe_w8a8_token_logprobs(const moe_w8a8_logprobs_args *a, int64_t T,
+                                       void *workspace, size_t workspace_bytes, void *stream) {
+  if (!a || T < 0 || T > kMaxRows || a->vocab < 1 || a->top < 0 || a->top > a->vocab ||
+      !type_ok(a->type))
+    return MOE_W8A8_ERR_INVALID;
+  if (a->vocab > kMaxVocab || a->top > kMaxTop) return MOE_W8A8_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_W8A8_OK;
+  const int64_t V = a->vocab;
+  const size_t size = a->type == MOE_W8A8_F32 ? 4 : 2;
+  if (!a->logits || !al(a->logits, size) || !pitch_ok(a->ld, V) ||
+      (a->tokens == nullptr) != (a->logprobs == nullptr) ||
+      (a->top > 0) != (a->top_tokens != nullptr) || (a->top > 0) != (a->top_logprobs != nullptr) ||
+      (!a->logprobs && !a->entropy && a->top == 0))
+    return MOE_W8A8_ERR_INVALID;
+  if (!al(a->tokens, 8) || !al(a->logprobs, 4) || !al(a->entropy, 4) || !al(a->top_tokens, 8) ||
+      !al(a->top_logprobs, 4))
+    return MOE_W8A8_ERR_INVALID;
+  const Mat ins[2] = {mat(a->logits, T, a->ld, V, size), flat(a->tokens, (size_t)T * 8)};
+  const Mat outs[4] = {flat(a->logprobs, (size_t)T * 4), flat(a->entropy, (size_t)T * 4),
+                       flat(a->top_tokens, (size_t)T * a->top * 8),
+                       flat(a->top_logprobs, (size_t)T * a->top * 4)};
+  for (int i = 0; i < 4; ++i) {
+    if (overlap(outs[i], ins[0]) || overlap(outs[i], ins[1])) return MOE_W8A8_ERR_INVALID;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return MOE_W8A8_ERR_INVALID;
+  }
+  (void)workspace;
+  (void)workspace_bytes;
+  LogprobArgs r{};
+  r.x = a->logits; r.ld = a->ld; r.tokens = a->tokens; r.logprobs = a->logprobs;
+  r.entropy = a->entropy; r.top_tokens = a->top_tokens; r.top_logprobs = a->top_logprobs;
+  r.V = a->vocab; r.top = a->top;
+  MOE_CHECK(launch_token_logprobs(r, a->type == MOE_W8A8_F32, T, (hipStream_t)stream));
+  return MOE_W8A8_OK;
+}

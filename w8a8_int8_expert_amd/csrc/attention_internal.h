@@ -1,0 +1,105 @@
+// attention_internal.h -- internal declarations of the operators over the paged
+// cache (moe_w8a8_qk_norm_rope, _paged_attention) and of _token_logprobs. Not part
+// of the public ABI (include/moe_w8a8.h).
+#pragma once
+
+#include "block_internal.h"
+
+namespace moe {
+
+constexpr int kBf16Cache = MOE_W8A8_CACHE_BF16;
+
+// A cache and a step's sequences as the kernels take them. Sizes in bytes are of
+// keys and values alike.
+struct CacheView {
+  char *k, *v;
+  float *k_scale, *v_scale;
+  int64_t page_bytes, scale_stride;  // from one page to the next
+  int num_pages, log2_page, kv_heads;
+};
+struct BatchView {
+  const int32_t *cu, *lengths, *table;
+  int64_t ld_table;
+  int num_seqs, max_tokens, T;
+  int most;  // places that the page table has room for
+};
+
+// Rows and keys of one sequence: first token row, new tokens, keys. Whatever the
+// arrays hold, rows lie in [0, T) and keys in what the table covers.
+struct Seq {
+  int start, n, len;
+};
+
+#if defined(__HIP_DEVICE_COMPILE__) || defined(__HIPCC__)
+__device__ __forceinline__ int clamp_int(int v, int lo, int hi) {
+  return v < lo ? lo : v > hi ? hi : v;
+}
+__device__ __forceinline__ Seq seq_of(const BatchView &bt, int b) {
+  Seq s;
+  s.start = clamp_int(bt.cu[b], 0, bt.T);
+  const int end = clamp_int(bt.cu[b + 1], s.start, bt.T);
+  s.n = end - s.start;
+  s.len = clamp_int(bt.lengths[b], 0, bt.most);
+  return s;
+}
+// Keys [lo, hi) that the token at `place` of a sequence of `len` keys sees.
+__device__ __forceinline__ int seen_hi(int place, int len, bool causal) {
+  return causal ? (place + 1 < len ? place + 1 : len) : len;
+}
+__device__ __forceinline__ int seen_lo(int place, int window) {
+  const int lo = place - window + 1;
+  return window > 0 && lo > 0 ? lo : 0;
+}
+#endif
+
+struct RopeArgs {
+  const uint16_t *qkv;
+  int64_t ld_qkv;
+  uint16_t *q;
+  int64_t ld_q;
+  const float *q_weight, *k_weight;
+  const double *inv_freq;
+  const int64_t *positions;
+  int heads, rotary;
+  bool norm, interleaved;
+  float eps;
+};
+hipError_t launch_qk_norm_rope(const RopeArgs &a, const CacheView &c, int D, int format,
+                               const BatchView &b, hipStream_t st);
+
+struct AttnArgs {
+  const uint16_t *q;
+  int64_t ld_q;
+  uint16_t *out;
+  int64_t ld_out;
+  int heads, group;  // query heads, and of them to one kv head
+  bool causal;
+  int window;
+  float scale2;  // scale * log2(e): the softmax is taken to base 2
+};
+
+// Workspace and launch sizes, of shapes alone.
+struct AttnPlan {
+  int units;       // most work units for each kv head, counted for the workspace
+  int target;      // units for each kv head that the keys are split into, about
+  int grid;        // units launched for each kv head (a block strides over the rest)
+  size_t partial;  // bytes of the partial results
+};
+AttnPlan attention_plan(const CacheView &c, int D, int format, const BatchView &b, int heads,
+                        int max_length);
+hipError_t launch_attention(const AttnArgs &a, const CacheView &c, int D, int format,
+                            const BatchView &b, const AttnPlan &p, float *partial,
+                            hipStream_t st);
+
+struct LogprobArgs {
+  const void *x;
+  int64_t ld;
+  const int64_t *tokens;
+  float *logprobs, *entropy;
+  int64_t *top_tokens;
+  float *top_logprobs;
+  int V, top;
+};
+hipError_t launch_token_logprobs(const LogprobArgs &a, bool f32, int64_t T, hipStream_t st);
+
+}  // namespace moe

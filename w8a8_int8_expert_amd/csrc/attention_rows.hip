@@ -1,0 +1,530 @@
+// attention_rows.hip -- attention of few query rows of each kv head over the paged
+// cache (decode steps). A row is one query head of one token; the rows of the heads
+// that share a kv head are taken together, 16 to a matrix instruction.
+//
+// With keys as the instruction's rows and queries as its columns, lane l holds the
+// scores of query l % 16 and of the keys 4 (l / 16) + 0..3: the softmax runs inside
+// lanes but for one exchange over the four lane groups, and the probabilities are
+// where the second product (values transposed by the LDS reads) takes them from.
+// Bound by the cache's bytes. Every wavefront brings its own tiles of 32 keys into
+// LDS by direct loads, the next in flight while one is worked on, and no two of them
+// meet until the end.
+#include "attention_device.h"
+
+namespace moe {
+namespace {
+
+constexpr int kKeys = 32;
+constexpr int kMostBlocks = 1 << 20;  // a launch counts threads in 32 bits
+
+template <int D, int kFormat, int NQ>
+struct Rows {
+  typedef Tile<D, kFormat, kKeys> TL;
+  static constexpr int kScaleBytes = TL::k8 ? 256 : 0;
+  static constexpr int kStage = 2 * TL::kBytes + kScaleBytes;
+  static constexpr int kWaves = 4 * 2 * kStage <= 150 * 1024 ? 4 : 2;
+  static constexpr int kRows = 16 * NQ;
+  static constexpr int kLoads = 2 * TL::kLoads + (TL::k8 ? 1 : 0);
+  // joining the wavefronts: their results of 16 rows each, and (m, l) of all rows
+  static constexpr int kPad = D + 4;
+  static constexpr int kJoin = kWaves * 16 * kPad * 4;
+  static constexpr int kStages = kWaves * 2 * kStage;
+  static constexpr int kLds = kStages > kJoin ? kStages : kJoin;
+};
+
+struct Part {  // where partial results lie: of each kv head `units` slots of kRows rows
+  float *o, *ml;
+  int units;
+};
+
+// What one kv head's rows of the batch come to: of each sequence a number of units
+// (pieces of its keys if its rows fit one, else pieces of its rows).
+struct Split {
+  int64_t tiles;  // of the sequences split by keys
+  int chunk;      // tiles of a unit
+};
+struct SeqWork {
+  Seq s;
+  int rows;    // query rows of one kv head
+  int t0, t1;  // key tiles
+};
+__device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, const BatchView &bt, int b) {
+  SeqWork w{};
+  if (b >= bt.num_seqs) return w;
+  w.s = seq_of(bt, b);
+  const int n = w.s.n < bt.max_tokens ? w.s.n : bt.max_tokens;
+  w.rows = n * a.group;
+  if (n > 0) {
+    const int first = w.s.len - w.s.n;
+    const int lo = seen_lo(first, a.window), hi = seen_hi(first + n - 1, w.s.len, a.causal);
+    w.t0 = lo / kKeys;
+    w.t1 = hi > lo ? (hi + kKeys - 1) / kKeys : w.t0;
+  }
+  return w;
+}
+__device__ __forceinline__ int units_of(const SeqWork &w, int chunk, int most_rows) {
+  if (w.rows == 0) return 0;
+  if (w.rows > most_rows) return (w.rows + most_rows - 1) / most_rows;
+  const int n = (w.t1 - w.t0 + chunk - 1) / chunk;
+  return n > 1 ? n : 1;
+}
+// Tiles of a unit such that the keys make about `target` units.
+__device__ __forceinline__ int chunk_of(const AttnArgs &a, const BatchView &bt, int target,
+                                        int most_rows, int waves, int lane) {
+  uint64_t sum = 0;
+  for (int b0 = 0; b0 < bt.num_seqs; b0 += 64) {
+    const SeqWork w = seq_work(a, bt, b0 + lane);
+    if (w.rows <= most_rows) sum += (uint64_t)(w.t1 - w.t0);
+  }
+  sum = wave_incl_scan_u64(sum);
+  const uint64_t total =
+      (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(sum >> 32), 63) << 32 |
+      (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)sum, 63);
+  uint64_t c = (total + target - 1) / target;
+  if (c > 1u << 30) c = 1u << 30;  // (past any sequence's tiles)
+  const int chunk = (int)((c + waves - 1) / waves) * waves;
+  return chunk > waves ? chunk : waves;
+}
+// The sequence that unit u falls into, and the unit's number in it; b = -1 past the end.
+// slot: where its partial result goes (only sequences split by keys have them, so
+// that there are at most target + num_seqs).
+struct Unit {
+  int b, piece, pieces, slot;
+  SeqWork w;
+};
+__device__ __forceinline__ Unit find_unit(const AttnArgs &a, const BatchView &bt, int u, int chunk,
+                                          int most_rows, int lane) {
+  int before = 0, slots = 0;
+  for (int b0 = 0; b0 < bt.num_seqs; b0 += 64) {
+    const SeqWork w = seq_work(a, bt, b0 + lane);
+    const int n = units_of(w, chunk, most_rows), end = before + wave_incl_scan(n);
+    const int ns = w.rows <= most_rows ? n : 0, send = slots + wave_incl_scan(ns);
+    const uint64_t hit = __ballot(end > u);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      auto rd = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+      Unit r;
+      r.b = b0 + l;
+      r.pieces = rd(n);
+      r.piece = u - (rd(end) - r.pieces);
+      r.slot = rd(send) - rd(ns) + r.piece;
+      r.w.s = Seq{rd(w.s.start), rd(w.s.n), rd(w.s.len)};
+      r.w.rows = rd(w.rows);
+      r.w.t0 = rd(w.t0);
+      r.w.t1 = rd(w.t1);
+      return r;
+    }
+    before = __builtin_amdgcn_readlane(end, 63);
+    slots = __builtin_amdgcn_readlane(send, 63);
+  }
+  Unit r{};
+  r.b = -1;
+  return r;
+}
+
+template <int D, int kFormat, int NQ>
+__global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kernel(
+    AttnArgs a, CacheView c, BatchView bt, int target, Part part) {
+  typedef Rows<D, kFormat, NQ> C;
+  typedef typename C::TL TL;
+  constexpr int W = C::kWaves, kSteps = D / 32, kOut = D / 16;
+  __shared__ __attribute__((aligned(1024))) char lds[C::kLds];
+  __shared__ float ml[W][C::kRows][2];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, col = lane & 15;
+  const int h = blockIdx.x % c.kv_heads;
+  const int chunk = chunk_of(a, bt, target, C::kRows, W, lane);
+  const int page_size = 1 << c.log2_page;
+  char *const mine = lds + wave * 2 * C::kStage;
+  const uint32_t mine_at = __builtin_amdgcn_readfirstlane(lds_addr(mine));
+
+  for (int u = blockIdx.x / c.kv_heads;; u += gridDim.x / c.kv_heads) {
+    const Unit un = find_unit(a, bt, u, chunk, C::kRows, lane);
+    if (un.b < 0) break;
+    const bool by_rows = un.w.rows > C::kRows;
+    const int r0 = by_rows ? un.piece * C::kRows : 0;
+    const int r1 = by_rows && un.w.rows > r0 + C::kRows ? r0 + C::kRows : un.w.rows;
+    const int len = un.w.s.len, first = len - un.w.s.n;
+    // keys that some row, and that every row sees
+    const int p0 = first + r0 / a.group, p1 = first + (r1 - 1) / a.group;
+    const int any_lo = seen_lo(p0, a.window), any_hi = seen_hi(p1, len, a.causal);
+    const int all_lo = seen_lo(p1, a.window), all_hi = seen_hi(p0, len, a.causal);
+    int t0 = un.w.t0, t1 = un.w.t1;
+    if (by_rows) {
+      t0 = any_lo / kKeys;
+      t1 = any_hi > any_lo ? (any_hi + kKeys - 1) / kKeys : t0;
+    } else {
+      t0 += un.piece * chunk;
+      t1 = t0 + chunk < t1 ? t0 + chunk : t1;
+    }
+
+    // queries, and what each sees
+    v8bf q[NQ][kSteps];
+    int lo[NQ], hi[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int r = r0 + n * 16 + col, i = r / a.group;
+      const bool there = r < r1;
+      lo[n] = seen_lo(first + i, a.window);
+      hi[n] = there ? seen_hi(first + i, len, a.causal) : 0;
+      const uint16_t *src =
+          a.q + (int64_t)(un.w.s.start + i) * a.ld_q + (h * a.group + r % a.group) * D;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+        q[n][s] = there ? __builtin_bit_cast(v8bf, (v4i)*reinterpret_cast<const v4i_a2 *>(
+                                                       src + TL::query_at(s, lane)))
+                        : v8bf{};
+    }
+
+    // direct loads of tile t into a stage; a page that does not exist is read as page 0
+    // and masked
+    auto page_of = [&](int key) {
+      const int i = key >> c.log2_page;
+      return key < any_hi ? scalar_word(bt.table, (int64_t)un.b * bt.ld_table + i) : -1;
+    };
+    auto issue = [&](int stage, int t, int pg0, int pg1) {
+      const int64_t in0 = ((int64_t)h * page_size + (t * kKeys & (page_size - 1)));
+      const int64_t in1 = ((int64_t)h * page_size + ((t * kKeys + 16) & (page_size - 1)));
+      const int64_t s0 = (uint32_t)pg0 < (uint32_t)c.num_pages ? pg0 : 0;
+      const int64_t s1 = (uint32_t)pg1 < (uint32_t)c.num_pages ? pg1 : 0;
+      const int64_t b0 = s0 * c.page_bytes + in0 * TL::kRow, b1 = s1 * c.page_bytes + in1 * TL::kRow;
+      const uint32_t at = mine_at + stage * C::kStage;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < TL::kLoads; ++i) {
+          const int byte = i * 1024 + lane * 16, r = byte / TL::kRow, p = byte % TL::kRow / 16;
+          const int ch = x ? TL::value_chunk(r, p) : TL::key_chunk(r, p);
+          const int64_t from = (i * 1024 / TL::kRow < 16 ? b0 : b1) + (r & 15) * TL::kRow + ch * 16;
+          dma16((x ? c.v : c.k) + from, at + x * TL::kBytes + i * 1024);
+        }
+      if constexpr (TL::k8) {
+        const float *sc = lane < 32 ? c.k_scale : c.v_scale;
+        const int r = lane & 31;
+        dma4(sc + (r < 16 ? s0 * c.scale_stride + in0 : s1 * c.scale_stride + in1) + (r & 15),
+             at + 2 * TL::kBytes);
+      }
+    };
+
+    v4f o[NQ][kOut];
+    float m[NQ], l[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      m[n] = kNoMax;
+      l[n] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) o[n][d] = v4f{0, 0, 0, 0};
+    }
+
+    int t = t0 + wave, stage = 0;
+    int pg0 = -1, pg1 = -1, ng0 = -1, ng1 = -1;
+    if (t < t1) {
+      pg0 = page_of(t * kKeys);
+      pg1 = page_of(t * kKeys + 16);
+      issue(0, t, pg0, pg1);
+      ng0 = page_of((t + W) * kKeys);
+      ng1 = page_of((t + W) * kKeys + 16);
+    }
+    for (; t < t1; t += W, stage ^= 1) {
+      // the stage of the tile before this one has been read to its end
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (t + W < t1) {
+        issue(stage ^ 1, t + W, ng0, ng1);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::kLoads) : "memory");
+      } else {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      }
+      char *const kt = mine + stage * C::kStage, *const vt = kt + TL::kBytes;
+      const float *const sc = reinterpret_cast<const float *>(vt + TL::kBytes);
+      const int key0 = t * kKeys;
+      const bool ok0 = (uint32_t)pg0 < (uint32_t)c.num_pages,
+                 ok1 = (uint32_t)pg1 < (uint32_t)c.num_pages;
+      const bool masked = !(key0 >= all_lo && key0 + kKeys <= all_hi && ok0 && ok1);
+      pg0 = ng0;
+      pg1 = ng1;
+      ng0 = page_of((t + 2 * W) * kKeys);
+      ng1 = page_of((t + 2 * W) * kKeys + 16);
+      if (masked) {
+        // values that no row sees count as zeros, whatever lies there
+        for (int i = lane; i < TL::kBytes / 16; i += 64) {
+          const int r = i / TL::kChunks, key = key0 + r;
+          if (key < any_lo || key >= any_hi || !(r < 16 ? ok0 : ok1))
+            reinterpret_cast<v4i *>(vt)[i] = v4i{0, 0, 0, 0};
+        }
+      }
+
+      // scores: keys 16 x + 4 g + i of column col
+      v4f s[NQ][2];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = v4f{0, 0, 0, 0};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if constexpr (TL::k8) {
+#pragma unroll
+          for (int s2 = 0; s2 < kSteps / 2; ++s2) {
+            v8bf f[2];
+            TL::key2(kt, 16 * x, s2, lane, f);
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+              s[n][x] = mfma16bf(f[0], q[n][2 * s2], s[n][x]);
+              s[n][x] = mfma16bf(f[1], q[n][2 * s2 + 1], s[n][x]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            const v8bf f = TL::key(kt, 16 * x, i, lane);
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) s[n][x] = mfma16bf(f, q[n][i], s[n][x]);
+          }
+        }
+      }
+      v4f ks[2], vs[2];
+      if constexpr (TL::k8) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          ks[x] = *reinterpret_cast<const v4f *>(sc + 16 * x + 4 * g);
+          vs[x] = *reinterpret_cast<const v4f *>(sc + 32 + 16 * x + 4 * g);
+        }
+      }
+      v8bf p[NQ];
+      uint32_t seen[NQ];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        float mx = kNoMax;
+        seen[n] = 0xffu;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = s[n][x][i] * a.scale2;
+            if constexpr (TL::k8) v *= ks[x][i];
+            if (masked) {
+              const int key = key0 + 16 * x + 4 * g + i;
+              const bool there = key >= lo[n] && key < hi[n] && (x ? ok1 : ok0);
+              v = there ? v : -INFINITY;
+              if (!there) seen[n] &= ~(1u << (4 * x + i));
+            }
+            s[n][x][i] = v;
+            mx = fmaxf(mx, v);
+          }
+        mx = fmaxf(m[n], groups_max(mx));
+        const float f = __builtin_amdgcn_exp2f(m[n] - mx);
+        m[n] = mx;
+        float e[8], sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          e[j] = __builtin_amdgcn_exp2f(s[n][j / 4][j % 4] - mx);
+          sum += e[j];
+          if constexpr (TL::k8) {
+            e[j] *= vs[j / 4][j % 4];
+            if (masked && !(seen[n] >> j & 1)) e[j] = 0.0f;
+          }
+        }
+        l[n] = l[n] * f + sum;
+        // rounded to bf16 for the second product: half a step of 2^-8 each, which the
+        // result, itself rounded so, averages over its keys
+        p[n] = __builtin_bit_cast(v8bf, v4i{(int)bf16x2(e[0], e[1]), (int)bf16x2(e[2], e[3]),
+                                            (int)bf16x2(e[4], e[5]), (int)bf16x2(e[6], e[7])});
+#pragma unroll
+        for (int d = 0; d < kOut; ++d) o[n][d] *= f;
+      }
+      // values that are not finite, in a tile of which some rows do not see all: an
+      // unseen one must not reach a row through 0 times infinity. They are taken out,
+      // and put back as indicators times the keys that a row sees.
+      bool odd = false;
+      if (masked) {
+#pragma unroll
+        for (int d = 0; d < kOut; ++d) odd |= any_odd(TL::value(vt, 0, d, lane));
+        odd = __any(odd);
+      }
+      if (!odd) {
+#pragma unroll
+        for (int d = 0; d < kOut; ++d) {
+          const v8bf f = TL::value(vt, 0, d, lane);
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) o[n][d] = mfma16bf(f, p[n], o[n][d]);
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          v4i one = {0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (seen[n] >> j & 1) one[j / 2] |= 0x3f80 << 16 * (j & 1);
+          const v8bf sees = __builtin_bit_cast(v8bf, one);
+#pragma unroll
+          for (int d = 0; d < kOut; ++d) {
+            const v8bf f = TL::value(vt, 0, d, lane);
+            const v4f marks = mfma16bf(odd_part<true>(f), sees, v4f{0, 0, 0, 0});
+            o[n][d] = mfma16bf(odd_part<false>(f), p[n], o[n][d]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n][d][i] = add_odd(o[n][d][i], marks[i]);
+            __builtin_amdgcn_sched_barrier(0);  // (this path need not be fast: few registers)
+          }
+        }
+      }
+    }
+
+    // join the wavefronts: o / l with the weights exp2(m - largest m)
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      l[n] = groups_sum(l[n]);
+      if (g == 0) {
+        ml[wave][n * 16 + col][0] = m[n];
+        ml[wave][n * 16 + col][1] = l[n];
+      }
+    }
+    __syncthreads();
+    const bool whole = by_rows || un.pieces == 1;
+    float *const jo = reinterpret_cast<float *>(lds);
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      float big = ml[0][n * 16 + col][0];
+#pragma unroll
+      for (int w = 1; w < W; ++w) big = fmaxf(big, ml[w][n * 16 + col][0]);
+      const float f = __builtin_amdgcn_exp2f(m[n] - big);
+#pragma unroll
+      for (int d = 0; d < kOut; ++d)
+        *reinterpret_cast<v4f *>(jo + (wave * 16 + col) * C::kPad + d * 16 + 4 * g) = o[n][d] * f;
+      __syncthreads();
+      for (int i = tid; i < 16 * D / 4; i += 64 * W) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4, row = n * 16 + r;
+        if (r0 + row >= r1) continue;
+        float mm = ml[0][row][0], ll = 0.0f;
+        for (int w = 1; w < W; ++w) mm = fmaxf(mm, ml[w][row][0]);
+        v4f v = {0, 0, 0, 0};
+        for (int w = 0; w < W; ++w) {
+          ll += ml[w][row][1] * __builtin_amdgcn_exp2f(ml[w][row][0] - mm);
+          v += *reinterpret_cast<const v4f *>(jo + (w * 16 + r) * C::kPad + d);
+        }
+        if (whole) {
+          const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
+          v *= inv;
+          const int rr = r0 + row;
+          uint16_t *dst = a.out + (int64_t)(un.w.s.start + rr / a.group) * a.ld_out +
+                          (h * a.group + rr % a.group) * D + d;
+          *reinterpret_cast<v2i_e2 *>(dst) = v2i{(int)bf16x2(v[0], v[1]), (int)bf16x2(v[2], v[3])};
+        } else {
+          const int64_t at = ((int64_t)h * part.units + un.slot) * C::kRows + row;
+          *reinterpret_cast<v4f *>(part.o + at * D + d) = v;
+          if (d == 0) {
+            part.ml[2 * at] = mm;
+            part.ml[2 * at + 1] = ll;
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Joins the pieces of each sequence whose keys were split.
+template <int D, int kRows>
+__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int kv_heads, BatchView bt,
+                                                   int target, int waves, Part part) {
+  const int lane = threadIdx.x & 63;
+  const int chunk = chunk_of(a, bt, target, kRows, waves, lane);
+  for (int64_t x = blockIdx.x; x < (int64_t)bt.num_seqs * kv_heads; x += gridDim.x) {
+    const int h = (int)(x % kv_heads), b = (int)(x / kv_heads);
+    int before = 0, pieces = 0;
+    SeqWork w{};
+    for (int b0 = 0; b0 <= b; b0 += 64) {
+      const SeqWork y = seq_work(a, bt, b0 + lane);
+      const int n = y.rows <= kRows ? units_of(y, chunk, kRows) : 0;
+      const int end = before + wave_incl_scan(n);
+      if (b < b0 + 64) {
+        auto rd = [&](int v) { return __builtin_amdgcn_readlane(v, b - b0); };
+        w.s = Seq{rd(y.s.start), rd(y.s.n), rd(y.s.len)};
+        w.rows = rd(y.rows);
+        pieces = rd(n);
+        before = rd(end) - pieces;
+      } else {
+        before = __builtin_amdgcn_readlane(end, 63);
+      }
+    }
+    if (pieces < 2) continue;
+    const int64_t at0 = ((int64_t)h * part.units + before) * kRows;
+    for (int i = threadIdx.x; i < w.rows * (D / 4); i += 256) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4;
+      float m = kNoMax, l = 0.0f;
+      for (int p = 0; p < pieces; ++p) m = fmaxf(m, part.ml[2 * (at0 + p * kRows + r)]);
+      v4f v = {0, 0, 0, 0};
+      for (int p = 0; p < pieces; ++p) {
+        const int64_t at = at0 + p * kRows + r;
+        const float f = __builtin_amdgcn_exp2f(part.ml[2 * at] - m);
+        l += part.ml[2 * at + 1] * f;
+        v += *reinterpret_cast<const v4f *>(part.o + at * D + d) * f;
+      }
+      v *= l != 0.0f ? 1.0f / l : 0.0f;
+      uint16_t *dst = a.out + (int64_t)(w.s.start + r / a.group) * a.ld_out +
+                      (h * a.group + r % a.group) * D + d;
+      *reinterpret_cast<v2i_e2 *>(dst) = v2i{(int)bf16x2(v[0], v[1]), (int)bf16x2(v[2], v[3])};
+    }
+  }
+}
+
+int row_tiles(int rows, int D) {
+  const int most = D == 256 ? 2 : 4;
+  const int n = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  return n < most ? n : most;
+}
+
+template <int D, int kFormat, int NQ>
+hipError_t launch(const AttnArgs &a, const CacheView &c, const BatchView &b, const AttnPlan &p,
+                  float *partial, hipStream_t st) {
+  typedef Rows<D, kFormat, NQ> C;
+  const Part part{partial, partial + (size_t)p.units * c.kv_heads * C::kRows * D, p.units};
+  hipError_t e = launch_kernel(rows_kernel<D, kFormat, NQ>, dim3(p.grid * c.kv_heads),
+                               dim3(64 * C::kWaves), st, {}, a, c, b, p.target, part);
+  if (e != hipSuccess) return e;
+  const int64_t joins = (int64_t)b.num_seqs * c.kv_heads;
+  return launch_kernel(join_kernel<D, C::kRows>, dim3(joins < kMostBlocks ? joins : kMostBlocks),
+                       dim3(256), st, {}, a, c.kv_heads, b, p.target, (int)C::kWaves, part);
+}
+template <int D, int kFormat>
+hipError_t launch(const AttnArgs &a, const CacheView &c, const BatchView &b, const AttnPlan &p,
+                  float *partial, hipStream_t st) {
+  const int n = row_tiles(b.max_tokens * a.group, D);
+  if (n == 1) return launch<D, kFormat, 1>(a, c, b, p, partial, st);
+  if (n == 2) return launch<D, kFormat, 2>(a, c, b, p, partial, st);
+  if constexpr (D < 256) return launch<D, kFormat, 4>(a, c, b, p, partial, st);
+  return hipErrorInvalidValue;
+}
+template <int D>
+hipError_t launch(const AttnArgs &a, const CacheView &c, int format, const BatchView &b,
+                  const AttnPlan &p, float *partial, hipStream_t st) {
+  if (format == kBf16Cache) return launch<D, kBf16Cache>(a, c, b, p, partial, st);
+  if (format == MOE_W8A8_FORMAT_FP8)
+    return launch<D, MOE_W8A8_FORMAT_FP8>(a, c, b, p, partial, st);
+  return launch<D, MOE_W8A8_FORMAT_INT8>(a, c, b, p, partial, st);
+}
+
+}  // namespace
+
+AttnPlan attention_plan(const CacheView &c, int D, int format, const BatchView &b, int heads,
+                        int max_length) {
+  AttnPlan p{};
+  const int group = heads / c.kv_heads;
+  const int64_t rows = (int64_t)b.max_tokens * group;
+  const int kRows = 16 * row_tiles(rows > 64 ? 64 : (int)rows, D);
+  p.target = (1024 + c.kv_heads - 1) / c.kv_heads;
+  p.units = p.target + b.num_seqs;
+  const int64_t blocks = (int64_t)b.num_seqs * ((max_length + 127) / 128 + rows / kRows + 1);
+  const int64_t most = kMostBlocks / c.kv_heads;
+  p.grid = (int)(blocks < most ? blocks : most);
+  p.partial = (size_t)p.units * c.kv_heads * kRows * (D + 2) * sizeof(float);
+  (void)format;
+  return p;
+}
+
+hipError_t launch_attention(const AttnArgs &a, const CacheView &c, int D, int format,
+                            const BatchView &b, const AttnPlan &p, float *partial,
+                            hipStream_t st) {
+  if (D == 64) return launch<64>(a, c, format, b, p, partial, st);
+  if (D == 128) return launch<128>(a, c, format, b, p, partial, st);
+  return launch<256>(a, c, format, b, p, partial, st);
+}
+
+}  // namespace moe
