@@ -206,10 +206,9 @@ extern "C" int moe_w8a8_paged_attention(const moe_w8a8_attention_args *a,
 }
 
 extern "C" size_t moe_w8a8_token_logprobs_workspace_size(int32_t V, int32_t top, int64_t T) {
-  (void)V;
-  (void)top;
-  (void)T;
-  return 0;
+  if (V < 1 || V > kMaxVocab || top < 0 || top > kMaxTop || top > V || T < 1 || T > kMaxRows)
+    return 0;
+  return up256(token_logprobs_workspace(V, top, T));
 }
 
 extern "C" int moe_w8a8_token_logprobs(const moe_w8a8_logprobs_args *a, int64_t T,
@@ -238,12 +237,17 @@ extern "C" int moe_w8a8_token_logprobs(const moe_w8a8_logprobs_args *a, int64_t 
     for (int j = 0; j < i; ++j)
       if (overlap(outs[i], outs[j])) return MOE_W8A8_ERR_INVALID;
   }
-  (void)workspace;
-  (void)workspace_bytes;
+  const size_t need = moe_w8a8_token_logprobs_workspace_size(a->vocab, a->top, T);
+  const Mat ws = flat(workspace, need);
+  if (!al(workspace, 256) || overlap(ws, ins[0]) || overlap(ws, ins[1])) return MOE_W8A8_ERR_INVALID;
+  for (const Mat &o : outs)
+    if (overlap(ws, o)) return MOE_W8A8_ERR_INVALID;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_W8A8_ERR_WORKSPACE;
   LogprobArgs r{};
   r.x = a->logits; r.ld = a->ld; r.tokens = a->tokens; r.logprobs = a->logprobs;
   r.entropy = a->entropy; r.top_tokens = a->top_tokens; r.top_logprobs = a->top_logprobs;
   r.V = a->vocab; r.top = a->top;
-  MOE_CHECK(launch_token_logprobs(r, a->type == MOE_W8A8_F32, T, (hipStream_t)stream));
+  MOE_CHECK(launch_token_logprobs(r, a->type == MOE_W8A8_F32, T, workspace,
+                                  (hipStream_t)stream));
   return MOE_W8A8_OK;
 }

@@ -100,6 +100,8 @@ struct LogprobArgs {
   float *top_logprobs;
   int V, top;
 };
-hipError_t launch_token_logprobs(const LogprobArgs &a, bool f32, int64_t T, hipStream_t st);
+size_t token_logprobs_workspace(int V, int top, int64_t T);
+hipError_t launch_token_logprobs(const LogprobArgs &a, bool f32, int64_t T, void *ws,
+                                 hipStream_t st);
 
 }  // namespace moe

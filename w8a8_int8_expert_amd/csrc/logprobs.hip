@@ -1,14 +1,30 @@
 // logprobs.hip -- log probabilities of given tokens, entropy and top alternatives of
-// rows of logits. With m the row's largest logit, s = sum exp(x - m) and
-// e = sum (x - m) exp(x - m):  z - m = log s,  entropy = log s - e / s,  so that
-// every sum is of numbers near the row's largest, whatever the logits' offset.
+// rows of logits, in one pass over them. With m the row's largest logit,
+// s = sum exp(x - m) and e = sum (x - m) exp(x - m):  z - m = log s and
+// entropy = log s - e / s, so that every sum is of numbers near the row's largest,
+// whatever the logits' offset. Each thread keeps its own (m, s, e) and takes the sums
+// along when its m grows.
+//
+// The alternatives are found in the same pass. The n-th largest of the first chunk's
+// thread maxima is a bound that at least n elements reach; only elements past it go
+// into a list in LDS (about n log(V / 2048) of a row in random order), which is cut
+// back to its n best, and the bound raised, when it fills up: an order in which every
+// element is a candidate costs time, not room.
+//
+// Bound by memory for many rows. Few rows are cut into parts of at least 4096
+// elements, one to a block, and joined by a second launch.
 #include "attention_internal.h"
 #include "row_device.h"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kChunk = 8 * kThreads;
+constexpr int kKeep = 256;              // candidates that may wait between two chunks
+constexpr int kRoom = kKeep + kChunk;   // and what one chunk may add
+constexpr int kMostParts = 64;          // one lane each where they are joined
+constexpr float kFar = -200.0f;         // exp of it is 0 in fp32
 
 __device__ __forceinline__ float logit(const float *x, int i) { return x[i]; }
 __device__ __forceinline__ float logit(const uint16_t *x, int i) { return bf16_to_f32(x[i]); }
@@ -25,96 +41,279 @@ __device__ __forceinline__ float rank_value(uint64_t r) {
   u = u & 0x80000000u ? u & 0x7fffffffu : ~u;
   return __uint_as_float(u);
 }
+__device__ __forceinline__ int rank_token(uint64_t r) { return (int)~(uint32_t)r; }
 
-// Running largest value, and the two sums relative to it.
+// Largest value so far and the two sums relative to it. A row with a NaN has s = NaN
+// in the end; +inf is seen in m, nothing but -inf in s = 0.
 struct Sums {
   float m, s, e;
 };
-__device__ __forceinline__ void join(Sums &a, const Sums &b) {
+constexpr float kLowest = -3.402823466e38f;
+__device__ __forceinline__ void rescale(Sums &a, float m) {
+  const float d = fmaxf(a.m - m, kFar), f = expf(d);
+  a.e = (a.e + a.s * d) * f;
+  a.s *= f;
+  a.m = m;
+}
+__device__ __forceinline__ void join(Sums &a, Sums b) {
   const float m = fmaxf(a.m, b.m);
-  auto part = [&](const Sums &p, float &s, float &e) {
-    if (p.m == -INFINITY) {  // nothing, or nothing but -inf (or NaN: kept in s)
-      s = p.s;
-      e = p.e;
-      return;
-    }
-    const float d = p.m - m, f = expf(d);
-    s = p.s * f;
-    e = f > 0.0f ? (p.e + p.s * d) * f : 0.0f;  // (d may be past the fp32 range)
-  };
-  float s0, e0, s1, e1;
-  part(a, s0, e0);
-  part(b, s1, e1);
-  a = Sums{m, s0 + s1, e0 + e1};
+  rescale(a, m);
+  rescale(b, m);
+  a.s += b.s;
+  a.e += b.e;
 }
 
+// What a part hands to the join: its sums, and its best candidates in order.
+struct Parts {
+  Sums *sums;      // [T][parts]
+  uint64_t *best;  // [T][parts][top], 0 past the part's end
+  int parts;
+};
+struct Result {
+  float z, h;  // z - m and the entropy, NaN where the row has none
+};
+__device__ __forceinline__ Result result_of(const Sums &a) {
+  const bool none = a.s == 0.0f || a.m == INFINITY;
+  const float z = none ? NAN : logf(a.s);
+  return Result{z, z - a.e / a.s};
+}
 template <typename T>
-__global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
-  __shared__ float red[3][kThreads / 64];
-  __shared__ uint64_t best[kThreads / 64];
-  const int64_t t = blockIdx.x;
+__device__ __forceinline__ void write_sums(const LogprobArgs &a, int64_t t, const T *x,
+                                           const Sums &s, const Result &r) {
+  if (a.logprobs) {
+    const int64_t k = a.tokens[t];
+    a.logprobs[t] = k >= 0 && k < a.V ? logit(x, (int)k) - s.m - r.z : NAN;
+  }
+  if (a.entropy) a.entropy[t] = r.h;
+}
+__device__ __forceinline__ void write_top(const LogprobArgs &a, int64_t t, int n, uint64_t k,
+                                          const Sums &s, const Result &r) {
+  a.top_tokens[t * a.top + n] = rank_token(k);
+  a.top_logprobs[t * a.top + n] = rank_value(k) - s.m - r.z;
+}
+
+template <typename T, bool kTop>
+__global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, Parts parts, int per) {
+  __shared__ uint64_t list[kTop ? kRoom : 1], best[64];
+  __shared__ uint64_t wave_best[kWaves];
+  __shared__ Sums red[kWaves];
+  __shared__ int count;
+  __shared__ uint64_t bound;
+  const int64_t t = blockIdx.x / parts.parts;
+  const int part = blockIdx.x % parts.parts;
   const T *x = reinterpret_cast<const T *>(a.x) + t * a.ld;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  float m = -INFINITY;
+  const int c0 = part * per, c1 = c0 + per < a.V ? c0 + per : a.V;
+  const int top = a.top;
+  Sums p{kLowest, 0.0f, 0.0f};
   bool nan = false;
-  for (int i = tid; i < a.V; i += kThreads) {
-    const float v = logit(x, i);
-    nan |= v != v;
-    m = fmaxf(m, v);
+  float bar = 0.0f;       // of elements behind the first chunk: candidates lie above
+  uint64_t bar_rank = 0;  // of those in it: candidates reach it
+  if (kTop && tid == 0) count = 0;
+
+  // The `n` best of the list, in order, in `best`; the list is spent (every thread).
+  auto take_best = [&](int n, int have) {
+    uint64_t mine[(kRoom + kThreads - 1) / kThreads];
+#pragma unroll
+    for (int i = 0; i < (kRoom + kThreads - 1) / kThreads; ++i)
+      mine[i] = i * kThreads + tid < have ? list[i * kThreads + tid] : 0;
+    for (int k = 0; k < n; ++k) {
+      uint64_t r = 0;
+#pragma unroll
+      for (int i = 0; i < (kRoom + kThreads - 1) / kThreads; ++i) r = mine[i] > r ? mine[i] : r;
+      r = wave_max_u64(r);
+      if (lane == 0) wave_best[wave] = r;
+      __syncthreads();
+      r = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) r = wave_best[w] > r ? wave_best[w] : r;
+      __syncthreads();
+      if (tid == 0) best[k] = r;
+#pragma unroll
+      for (int i = 0; i < (kRoom + kThreads - 1) / kThreads; ++i) mine[i] = mine[i] == r ? 0 : mine[i];
+    }
+    __syncthreads();
+  };
+
+  auto raw = fetch8(x, c0 + 8 * tid, a.V);
+  for (int c = c0; c < c1; c += kChunk) {
+    float v[8];
+    const int at = c + 8 * tid;
+    unpack8(raw, at, a.V, v);
+    if (c + kChunk < c1) raw = fetch8(x, at + kChunk, a.V);
+    if (at + 8 > c1) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = at + j < c1 ? v[j] : -INFINITY;
+    }
+    float big = v[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) big = fmaxf(big, v[j]);
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) nan |= __builtin_isunordered(v[j], v[j + 1]);
+    if (big > p.m) rescale(p, big);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float d = fmaxf(v[j] - p.m, kFar), f = __expf(d);
+      p.s += f;
+      p.e = __builtin_fmaf(d, f, p.e);
+    }
+    if constexpr (kTop) {
+      const bool first = c == c0;
+      if (first) {
+        // the bound: the top-th largest of the threads' maxima (0 if fewer have any)
+        int j = 0;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) j = v[i] == big ? i : j;
+        const uint64_t mine = at < c1 ? rank_of(big, at + j) : 0;
+        list[tid] = mine;
+        if (tid == 0) bound = 0;
+        __syncthreads();
+        int above = 0;
+        for (int i = 0; i < kThreads; i += 2) {
+          typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+          const u64x2 o = *reinterpret_cast<const u64x2 *>(&list[i]);
+          above += (o[0] > mine) + (o[1] > mine);
+        }
+        if (mine != 0 && above == top - 1) bound = mine;
+        __syncthreads();
+        bar_rank = bound;
+      }
+      bool added = false;
+      if (first ? at < c1 : big > bar) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint64_t r = rank_of(v[j], at + j);
+          if (at + j < c1 && (first ? r >= bar_rank : v[j] > bar)) {
+            list[atomicAdd(&count, 1)] = r;
+            added = true;
+          }
+        }
+      }
+      if (first) bar = bar_rank ? rank_value(bar_rank) : -INFINITY;
+      if (__syncthreads_or(added)) {
+        const int have = count;
+        __syncthreads();
+        if (have > kKeep) {
+          take_best(top, have);
+          if (tid < top) list[tid] = best[tid];
+          if (tid == 0) count = top;
+          bar = rank_value(best[top - 1]);
+          __syncthreads();
+        }
+      }
+    }
   }
-  Sums p{m, 0.0f, 0.0f};
-  for (int i = tid; i < a.V; i += kThreads) {
-    const float v = logit(x, i);
-    if (v == -INFINITY) continue;
-    const float d = v - m, f = expf(d);
-    p.s += f;
-    p.e += f > 0.0f ? d * f : 0.0f;
-  }
-  if (nan) p.s = NAN;
+
+  if (__syncthreads_or(nan)) p.s = NAN;
+#pragma unroll
   for (int o = 32; o > 0; o >>= 1)
     join(p, Sums{__shfl_xor(p.m, o), __shfl_xor(p.s, o), __shfl_xor(p.e, o)});
-  if (lane == 0) {
-    red[0][wave] = p.m;
-    red[1][wave] = p.s;
-    red[2][wave] = p.e;
-  }
+  if (lane == 0) red[wave] = p;
   __syncthreads();
-  p = Sums{red[0][0], red[1][0], red[2][0]};
-  for (int w = 1; w < kThreads / 64; ++w) join(p, Sums{red[0][w], red[1][w], red[2][w]});
-  const float z = p.m == -INFINITY ? NAN : logf(p.s);
+  p = red[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) join(p, red[w]);
+  const bool whole = parts.parts == 1;
+  const Result r = result_of(p);
   if (tid == 0) {
-    if (a.logprobs) {
-      const int64_t k = a.tokens[t];
-      a.logprobs[t] = k >= 0 && k < a.V ? logit(x, (int)k) - p.m - z : NAN;
-    }
-    if (a.entropy) a.entropy[t] = z - p.e / p.s;
+    if (whole) write_sums(a, t, x, p, r);
+    else parts.sums[blockIdx.x] = p;
   }
-  uint64_t last = ~0ull;
-  for (int n = 0; n < a.top; ++n) {
-    uint64_t r = 0;
-    for (int i = tid; i < a.V; i += kThreads) {
-      const uint64_t k = rank_of(logit(x, i), i);
-      if (k < last && k > r) r = k;
+  if constexpr (kTop) {
+    auto put = [&](int n, uint64_t k) {
+      if (whole) write_top(a, t, n, k, p, r);
+      else parts.best[(int64_t)blockIdx.x * top + n] = k;
+    };
+    if (p.s != p.s) {
+      // a NaN compares with nothing: such a row takes one round over it for each place
+      uint64_t last = ~0ull;
+      for (int n = 0; n < top; ++n) {
+        uint64_t k = 0;
+        for (int i = c0 + tid; i < c1; i += kThreads) {
+          const uint64_t o = rank_of(logit(x, i), i);
+          if (o < last && o > k) k = o;
+        }
+        k = wave_max_u64(k);
+        if (lane == 0) wave_best[wave] = k;
+        __syncthreads();
+        k = 0;
+        for (int w = 0; w < kWaves; ++w) k = wave_best[w] > k ? wave_best[w] : k;
+        __syncthreads();
+        if (tid == 0) put(n, k);
+        last = k;
+      }
+      return;
     }
-    r = wave_max_u64(r);
-    if (lane == 0) best[wave] = r;
-    __syncthreads();
-    last = 0;
-    for (int w = 0; w < kThreads / 64; ++w) last = best[w] > last ? best[w] : last;
-    __syncthreads();
-    if (tid == 0) {
-      a.top_tokens[t * a.top + n] = (int)~(uint32_t)last;
-      a.top_logprobs[t * a.top + n] = rank_value(last) - p.m - z;
+    // every candidate counts those above it: its place
+    const int have = count;
+    for (int i = tid; i < have; i += kThreads) {
+      const uint64_t mine = list[i];
+      int above = 0;
+      for (int j = 0; j < have; ++j) above += list[j] > mine;
+      if (above < top) put(above, mine);
     }
+    for (int n = have + tid; n < top; n += kThreads) put(n, 0);  // (a short last part)
   }
+}
+
+// Joins a row's parts: one wavefront, a part to a lane. The lists are in order, so the
+// next place goes to the largest of their heads.
+template <typename T>
+__global__ __launch_bounds__(64) void logprobs_join_kernel(LogprobArgs a, Parts parts) {
+  __shared__ uint64_t lists[64 * 64];
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x, n = parts.parts, top = a.top;
+  Sums p{kLowest, 0.0f, 0.0f};
+  if (lane < n) p = parts.sums[t * n + lane];
+  for (int i = lane; i < n * top; i += 64) lists[i] = parts.best[t * n * top + i];
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1)
+    join(p, Sums{__shfl_xor(p.m, o), __shfl_xor(p.s, o), __shfl_xor(p.e, o)});
+  const Result r = result_of(p);
+  if (lane == 0) write_sums(a, t, reinterpret_cast<const T *>(a.x) + t * a.ld, p, r);
+  __syncthreads();
+  int head = 0;
+  uint64_t mine = lane < n && top > 0 ? lists[lane * top] : 0, got = 0;
+  for (int k = 0; k < top; ++k) {
+    const uint64_t big = wave_max_u64(mine);
+    if (lane == k) got = big;
+    if (mine == big && lane < n) mine = ++head < top ? lists[lane * top + head] : 0;
+  }
+  if (lane < top) write_top(a, t, lane, got, p, r);
+}
+
+// Parts of a row: about 1024 blocks in all.
+int parts_of(int V, int64_t T) {
+  const int64_t want = (1024 + T - 1) / T;
+  const int most = (V + 2 * kChunk - 1) / (2 * kChunk);
+  const int n = (int)(want < most ? want : most);
+  return n < kMostParts ? n : kMostParts;
+}
+size_t sums_bytes(int parts, int64_t T) { return ((size_t)T * parts * sizeof(Sums) + 255) / 256 * 256; }
+
+template <typename T>
+hipError_t launch(const LogprobArgs &a, int64_t T_, void *ws, hipStream_t st) {
+  const int want = parts_of(a.V, T_);
+  const int per = ((a.V + want - 1) / want + kChunk - 1) / kChunk * kChunk;
+  const int n = (a.V + per - 1) / per;
+  Parts p{(Sums *)ws, nullptr, n};
+  p.best = reinterpret_cast<uint64_t *>((char *)ws + sums_bytes(n, T_));
+  const dim3 grid((unsigned)(T_ * n)), block(kThreads);
+  const hipError_t e = a.top ? launch_kernel(logprobs_kernel<T, true>, grid, block, st, {}, a, p, per)
+                             : launch_kernel(logprobs_kernel<T, false>, grid, block, st, {}, a, p, per);
+  if (e != hipSuccess || n == 1) return e;
+  return launch_kernel(logprobs_join_kernel<T>, dim3((unsigned)T_), dim3(64), st, {}, a, p);
 }
 
 }  // namespace
 
-hipError_t launch_token_logprobs(const LogprobArgs &a, bool f32, int64_t T, hipStream_t st) {
-  const dim3 grid((unsigned)T), block(kThreads);
-  if (f32) return launch_kernel(logprobs_kernel<float>, grid, block, st, {}, a);
-  return launch_kernel(logprobs_kernel<uint16_t>, grid, block, st, {}, a);
+size_t token_logprobs_workspace(int V, int top, int64_t T) {
+  const int n = parts_of(V, T);
+  return n > 1 ? sums_bytes(n, T) + (size_t)T * n * top * sizeof(uint64_t) : 0;
+}
+hipError_t launch_token_logprobs(const LogprobArgs &a, bool f32, int64_t T, void *ws,
+                                 hipStream_t st) {
+  return f32 ? launch<float>(a, T, ws, st) : launch<uint16_t>(a, T, ws, st);
 }
 
 }  // namespace moe
