@@ -149,6 +149,44 @@ extern "C" int moe_w8a8_qk_norm_rope(const moe_w8a8_qk_norm_rope_args *a,
   return MOE_W8A8_OK;
 }
 
+AttnPlan moe::attention_plan(const CacheView &c, int D, const BatchView &b, int heads,
+                             int max_length) {
+  AttnPlan p{};
+  const int group = heads / c.kv_heads;
+  const int64_t rows = (int64_t)b.max_tokens * group;  // most of a sequence and kv head
+  const int most_few = D == 256 ? 16 : 32;
+  const int grid_cap = kMostBlocks / c.kv_heads;
+  auto at_most = [](int64_t v, int64_t most) { return (int)(v < most ? v : most); };
+  // All sequences have few rows; or some may, beside longer ones (where one sequence
+  // is all there is, or every row is needed for the longest, none does).
+  const bool all_few = rows <= most_few;
+  const bool some_few =
+      group <= most_few && b.num_seqs > 1 && (int64_t)b.num_seqs * b.max_tokens > b.T;
+  size_t total = 0;
+  if (all_few || some_few) {
+    p.few_rows = most_few;
+    p.row_tiles = at_most(rows, most_few) <= 16 ? 1 : 2;
+    p.row_target = (1024 + c.kv_heads - 1) / c.kv_heads;
+    p.row_slots = 2 * p.row_target;
+    // (keys of 128 at least make a unit)
+    const int64_t units = (int64_t)b.num_seqs * ((max_length + 127) / 128 + 1);
+    p.row_grid = at_most(at_most(units, (int64_t)p.row_target + b.num_seqs), grid_cap);
+    total += up256((size_t)p.row_slots * c.kv_heads * 16 * p.row_tiles * (D + 2) * sizeof(float));
+  }
+  p.tile_at = total;
+  if (!all_few) {
+    p.tiles = true;
+    // blocks of rows that the batch can make
+    const int64_t blocks = (int64_t)b.T * group / kTileRows + at_most(b.num_seqs, b.T);
+    p.tile_target = (1024 + c.kv_heads - 1) / c.kv_heads;
+    p.tile_slots = 2 * p.tile_target;
+    p.tile_grid = at_most(blocks + p.tile_target, grid_cap);
+    total += up256((size_t)p.tile_slots * c.kv_heads * kTileRows * (D + 2) * sizeof(float));
+  }
+  p.total = total;
+  return p;
+}
+
 namespace {
 // Checks of the shapes that the workspace depends on.
 int attention_shape(const moe_w8a8_kv_cache *c, const moe_w8a8_batch *b, int32_t heads,
@@ -160,8 +198,7 @@ int attention_shape(const moe_w8a8_kv_cache *c, const moe_w8a8_batch *b, int32_t
   return MOE_W8A8_OK;
 }
 AttnPlan plan_of(const moe_w8a8_kv_cache &c, const moe_w8a8_batch &b, int32_t heads, int64_t T) {
-  return attention_plan(view(c), c.head_dim, c.format, view(b, c.page_size, T), heads,
-                        b.max_length);
+  return attention_plan(view(c), c.head_dim, view(b, c.page_size, T), heads, b.max_length);
 }
 }  // namespace
 
@@ -170,7 +207,7 @@ extern "C" size_t moe_w8a8_paged_attention_workspace_size(const moe_w8a8_kv_cach
                                                           int64_t T) {
   if (attention_shape(c, b, heads, T) != MOE_W8A8_OK) return 0;
   if (T == 0 || b->num_seqs == 0 || b->max_tokens == 0) return 0;
-  return up256(plan_of(*c, *b, heads, T).partial);
+  return plan_of(*c, *b, heads, T).total;
 }
 
 extern "C" int moe_w8a8_paged_attention(const moe_w8a8_attention_args *a,
@@ -189,19 +226,26 @@ extern "C" int moe_w8a8_paged_attention(const moe_w8a8_attention_args *a,
     return MOE_W8A8_ERR_INVALID;
   const Mat out = mat(a->out, T, a->ld_out, width, 2);
   const AttnPlan p = plan_of(*c, *b, a->heads, T);
-  const Mat ws = flat(workspace, p.partial), q = mat(a->q, T, a->ld_q, width, 2);
+  const Mat ws = flat(workspace, p.total), q = mat(a->q, T, a->ld_q, width, 2);
   if (!al(workspace, 256) || overlap(out, q) || overlap(ws, q) || overlap(ws, out))
     return MOE_W8A8_ERR_INVALID;
   const Buffers bf = buffers(*c, *b);
   for (const Mat &m : bf.m)
     if (overlap(out, m) || overlap(ws, m)) return MOE_W8A8_ERR_INVALID;
-  if (p.partial > 0 && (!workspace || workspace_bytes < p.partial)) return MOE_W8A8_ERR_WORKSPACE;
+  if (p.total > 0 && (!workspace || workspace_bytes < p.total)) return MOE_W8A8_ERR_WORKSPACE;
   AttnArgs r{};
   r.q = a->q; r.ld_q = a->ld_q; r.out = a->out; r.ld_out = a->ld_out;
   r.heads = a->heads; r.group = a->heads / c->kv_heads; r.causal = a->causal != 0;
   r.window = a->window; r.scale2 = a->scale * 1.44269504088896340736f;
-  MOE_CHECK(launch_attention(r, view(*c), D, c->format, view(*b, c->page_size, T), p,
-                             (float *)workspace, (hipStream_t)stream));
+  r.few_rows = p.few_rows;
+  const CacheView cv = view(*c);
+  const BatchView bv = view(*b, c->page_size, T);
+  if (p.tiles)
+    MOE_CHECK(launch_attention_tiles(r, cv, D, c->format, bv, p, (float *)workspace,
+                                     (hipStream_t)stream));
+  if (p.few_rows > 0)
+    MOE_CHECK(launch_attention_rows(r, cv, D, c->format, bv, p, (float *)workspace,
+                                    (hipStream_t)stream));
   return MOE_W8A8_OK;
 }
 

@@ -75,21 +75,32 @@ struct AttnArgs {
   int heads, group;  // query heads, and of them to one kv head
   bool causal;
   int window;
-  float scale2;  // scale * log2(e): the softmax is taken to base 2
+  float scale2;   // scale * log2(e): the softmax is taken to base 2
+  int few_rows;   // sequences of at most so many query rows of a kv head go to the kernel
+                  // of few rows, the others to that of tiles
 };
 
-// Workspace and launch sizes, of shapes alone.
+constexpr int kMostBlocks = 1 << 20;  // a launch counts threads in 32 bits
+
+// Which kernels run, their launch sizes and the workspace, from shapes alone. Of each
+// kv head: a number of units that the keys are split into, about; the slots for partial
+// results that these can need; and the units launched (a block strides over the rest).
 struct AttnPlan {
-  int units;       // most work units for each kv head, counted for the workspace
-  int target;      // units for each kv head that the keys are split into, about
-  int grid;        // units launched for each kv head (a block strides over the rest)
-  size_t partial;  // bytes of the partial results
+  int few_rows;   // as in AttnArgs; 0: the kernel of few rows does not run
+  int row_tiles;  // 16-row tiles of the kernel of few rows
+  int row_target, row_slots, row_grid;
+  bool tiles;     // whether the kernel of tiles runs
+  int tile_target, tile_slots, tile_grid;
+  size_t tile_at, total;  // bytes before the partial results of tiles, and of all
 };
-AttnPlan attention_plan(const CacheView &c, int D, int format, const BatchView &b, int heads,
-                        int max_length);
-hipError_t launch_attention(const AttnArgs &a, const CacheView &c, int D, int format,
-                            const BatchView &b, const AttnPlan &p, float *partial,
-                            hipStream_t st);
+AttnPlan attention_plan(const CacheView &c, int D, const BatchView &b, int heads, int max_length);
+hipError_t launch_attention_rows(const AttnArgs &a, const CacheView &c, int D, int format,
+                                 const BatchView &b, const AttnPlan &p, float *partial,
+                                 hipStream_t st);
+constexpr int kTileRows = 128;  // query rows of a block of the kernel of tiles
+hipError_t launch_attention_tiles(const AttnArgs &a, const CacheView &c, int D, int format,
+                                  const BatchView &b, const AttnPlan &p, float *partial,
+                                  hipStream_t st);
 
 struct LogprobArgs {
   const void *x;

@@ -15,7 +15,6 @@ namespace moe {
 namespace {
 
 constexpr int kKeys = 32;
-constexpr int kMostBlocks = 1 << 20;  // a launch counts threads in 32 bits
 
 template <int D, int kFormat, int NQ>
 struct Rows {
@@ -32,20 +31,16 @@ struct Rows {
   static constexpr int kLds = kStages > kJoin ? kStages : kJoin;
 };
 
-struct Part {  // where partial results lie: of each kv head `units` slots of kRows rows
+struct Part {  // where partial results lie: of each kv head `slots` of kRows rows
   float *o, *ml;
-  int units;
+  int slots;
 };
 
-// What one kv head's rows of the batch come to: of each sequence a number of units
-// (pieces of its keys if its rows fit one, else pieces of its rows).
-struct Split {
-  int64_t tiles;  // of the sequences split by keys
-  int chunk;      // tiles of a unit
-};
+// Pieces of the keys of each sequence of few rows (units): as many as make about
+// `target` of all sequences together.
 struct SeqWork {
   Seq s;
-  int rows;    // query rows of one kv head
+  int rows;    // query rows of one kv head; 0: none, or more than these kernels take
   int t0, t1;  // key tiles
 };
 __device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, const BatchView &bt, int b) {
@@ -53,8 +48,8 @@ __device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, const BatchView &
   if (b >= bt.num_seqs) return w;
   w.s = seq_of(bt, b);
   const int n = w.s.n < bt.max_tokens ? w.s.n : bt.max_tokens;
-  w.rows = n * a.group;
-  if (n > 0) {
+  if (n > 0 && n <= a.few_rows / a.group) {
+    w.rows = n * a.group;
     const int first = w.s.len - w.s.n;
     const int lo = seen_lo(first, a.window), hi = seen_hi(first + n - 1, w.s.len, a.causal);
     w.t0 = lo / kKeys;
@@ -62,43 +57,38 @@ __device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, const BatchView &
   }
   return w;
 }
-__device__ __forceinline__ int units_of(const SeqWork &w, int chunk, int most_rows) {
+__device__ __forceinline__ int pieces_of(const SeqWork &w, int chunk) {
   if (w.rows == 0) return 0;
-  if (w.rows > most_rows) return (w.rows + most_rows - 1) / most_rows;
   const int n = (w.t1 - w.t0 + chunk - 1) / chunk;
   return n > 1 ? n : 1;
 }
-// Tiles of a unit such that the keys make about `target` units.
 __device__ __forceinline__ int chunk_of(const AttnArgs &a, const BatchView &bt, int target,
-                                        int most_rows, int waves, int lane) {
+                                        int waves, int lane) {
   uint64_t sum = 0;
   for (int b0 = 0; b0 < bt.num_seqs; b0 += 64) {
     const SeqWork w = seq_work(a, bt, b0 + lane);
-    if (w.rows <= most_rows) sum += (uint64_t)(w.t1 - w.t0);
+    sum += (uint64_t)(w.t1 - w.t0);
   }
-  sum = wave_incl_scan_u64(sum);
-  const uint64_t total =
-      (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(sum >> 32), 63) << 32 |
-      (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)sum, 63);
-  uint64_t c = (total + target - 1) / target;
+  sum = wave_sum_u64(sum);
+  uint64_t c = (sum + target - 1) / target;
   if (c > 1u << 30) c = 1u << 30;  // (past any sequence's tiles)
   const int chunk = (int)((c + waves - 1) / waves) * waves;
   return chunk > waves ? chunk : waves;
 }
 // The sequence that unit u falls into, and the unit's number in it; b = -1 past the end.
-// slot: where its partial result goes (only sequences split by keys have them, so
-// that there are at most target + num_seqs).
+// slot: where its partial result goes. Only sequences of two pieces or more have slots:
+// these have more tiles than a chunk, so that their pieces are at most 2 `target`.
 struct Unit {
   int b, piece, pieces, slot;
   SeqWork w;
 };
 __device__ __forceinline__ Unit find_unit(const AttnArgs &a, const BatchView &bt, int u, int chunk,
-                                          int most_rows, int lane) {
+                                          int lane) {
   int before = 0, slots = 0;
   for (int b0 = 0; b0 < bt.num_seqs; b0 += 64) {
     const SeqWork w = seq_work(a, bt, b0 + lane);
-    const int n = units_of(w, chunk, most_rows), end = before + wave_incl_scan(n);
-    const int ns = w.rows <= most_rows ? n : 0, send = slots + wave_incl_scan(ns);
+    const int n = pieces_of(w, chunk), end = before + wave_incl_scan(n);
+    const int ns = n > 1 ? n : 0, send = slots + wave_incl_scan(ns);
     const uint64_t hit = __ballot(end > u);
     if (hit) {
       const int l = __builtin_ctzll(hit);
@@ -134,38 +124,29 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, col = lane & 15;
   const int h = blockIdx.x % c.kv_heads;
-  const int chunk = chunk_of(a, bt, target, C::kRows, W, lane);
+  const int chunk = chunk_of(a, bt, target, W, lane);
   const int page_size = 1 << c.log2_page;
   char *const mine = lds + wave * 2 * C::kStage;
   const uint32_t mine_at = __builtin_amdgcn_readfirstlane(lds_addr(mine));
 
   for (int u = blockIdx.x / c.kv_heads;; u += gridDim.x / c.kv_heads) {
-    const Unit un = find_unit(a, bt, u, chunk, C::kRows, lane);
+    const Unit un = find_unit(a, bt, u, chunk, lane);
     if (un.b < 0) break;
-    const bool by_rows = un.w.rows > C::kRows;
-    const int r0 = by_rows ? un.piece * C::kRows : 0;
-    const int r1 = by_rows && un.w.rows > r0 + C::kRows ? r0 + C::kRows : un.w.rows;
     const int len = un.w.s.len, first = len - un.w.s.n;
     // keys that some row, and that every row sees
-    const int p0 = first + r0 / a.group, p1 = first + (r1 - 1) / a.group;
+    const int rows = un.w.rows, p0 = first, p1 = first + (rows - 1) / a.group;
     const int any_lo = seen_lo(p0, a.window), any_hi = seen_hi(p1, len, a.causal);
     const int all_lo = seen_lo(p1, a.window), all_hi = seen_hi(p0, len, a.causal);
-    int t0 = un.w.t0, t1 = un.w.t1;
-    if (by_rows) {
-      t0 = any_lo / kKeys;
-      t1 = any_hi > any_lo ? (any_hi + kKeys - 1) / kKeys : t0;
-    } else {
-      t0 += un.piece * chunk;
-      t1 = t0 + chunk < t1 ? t0 + chunk : t1;
-    }
+    const int t0 = un.w.t0 + un.piece * chunk;
+    const int t1 = t0 + chunk < un.w.t1 ? t0 + chunk : un.w.t1;
 
     // queries, and what each sees
     v8bf q[NQ][kSteps];
     int lo[NQ], hi[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      const int r = r0 + n * 16 + col, i = r / a.group;
-      const bool there = r < r1;
+      const int r = n * 16 + col, i = r / a.group;
+      const bool there = r < rows;
       lo[n] = seen_lo(first + i, a.window);
       hi[n] = there ? seen_hi(first + i, len, a.causal) : 0;
       const uint16_t *src =
@@ -377,7 +358,7 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
       }
     }
     __syncthreads();
-    const bool whole = by_rows || un.pieces == 1;
+    const bool whole = un.pieces == 1;
     float *const jo = reinterpret_cast<float *>(lds);
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -391,7 +372,7 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
       __syncthreads();
       for (int i = tid; i < 16 * D / 4; i += 64 * W) {
         const int r = i / (D / 4), d = i % (D / 4) * 4, row = n * 16 + r;
-        if (r0 + row >= r1) continue;
+        if (row >= rows) continue;
         float mm = ml[0][row][0], ll = 0.0f;
         for (int w = 1; w < W; ++w) mm = fmaxf(mm, ml[w][row][0]);
         v4f v = {0, 0, 0, 0};
@@ -402,12 +383,11 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
         if (whole) {
           const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
           v *= inv;
-          const int rr = r0 + row;
-          uint16_t *dst = a.out + (int64_t)(un.w.s.start + rr / a.group) * a.ld_out +
-                          (h * a.group + rr % a.group) * D + d;
+          uint16_t *dst = a.out + (int64_t)(un.w.s.start + row / a.group) * a.ld_out +
+                          (h * a.group + row % a.group) * D + d;
           *reinterpret_cast<v2i_e2 *>(dst) = v2i{(int)bf16x2(v[0], v[1]), (int)bf16x2(v[2], v[3])};
         } else {
-          const int64_t at = ((int64_t)h * part.units + un.slot) * C::kRows + row;
+          const int64_t at = ((int64_t)h * part.slots + un.slot) * C::kRows + row;
           *reinterpret_cast<v4f *>(part.o + at * D + d) = v;
           if (d == 0) {
             part.ml[2 * at] = mm;
@@ -425,27 +405,27 @@ template <int D, int kRows>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int kv_heads, BatchView bt,
                                                    int target, int waves, Part part) {
   const int lane = threadIdx.x & 63;
-  const int chunk = chunk_of(a, bt, target, kRows, waves, lane);
+  const int chunk = chunk_of(a, bt, target, waves, lane);
   for (int64_t x = blockIdx.x; x < (int64_t)bt.num_seqs * kv_heads; x += gridDim.x) {
     const int h = (int)(x % kv_heads), b = (int)(x / kv_heads);
     int before = 0, pieces = 0;
     SeqWork w{};
     for (int b0 = 0; b0 <= b; b0 += 64) {
       const SeqWork y = seq_work(a, bt, b0 + lane);
-      const int n = y.rows <= kRows ? units_of(y, chunk, kRows) : 0;
-      const int end = before + wave_incl_scan(n);
+      const int n = pieces_of(y, chunk), ns = n > 1 ? n : 0;
+      const int end = before + wave_incl_scan(ns);
       if (b < b0 + 64) {
         auto rd = [&](int v) { return __builtin_amdgcn_readlane(v, b - b0); };
         w.s = Seq{rd(y.s.start), rd(y.s.n), rd(y.s.len)};
         w.rows = rd(y.rows);
-        pieces = rd(n);
+        pieces = rd(ns);
         before = rd(end) - pieces;
       } else {
         before = __builtin_amdgcn_readlane(end, 63);
       }
     }
     if (pieces < 2) continue;
-    const int64_t at0 = ((int64_t)h * part.units + before) * kRows;
+    const int64_t at0 = ((int64_t)h * part.slots + before) * kRows;
     for (int i = threadIdx.x; i < w.rows * (D / 4); i += 256) {
       const int r = i / (D / 4), d = i % (D / 4) * 4;
       float m = kNoMax, l = 0.0f;
@@ -465,32 +445,24 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int kv_heads, Bat
   }
 }
 
-int row_tiles(int rows, int D) {
-  const int most = D == 256 ? 2 : 4;
-  const int n = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  return n < most ? n : most;
-}
-
 template <int D, int kFormat, int NQ>
 hipError_t launch(const AttnArgs &a, const CacheView &c, const BatchView &b, const AttnPlan &p,
                   float *partial, hipStream_t st) {
   typedef Rows<D, kFormat, NQ> C;
-  const Part part{partial, partial + (size_t)p.units * c.kv_heads * C::kRows * D, p.units};
-  hipError_t e = launch_kernel(rows_kernel<D, kFormat, NQ>, dim3(p.grid * c.kv_heads),
-                               dim3(64 * C::kWaves), st, {}, a, c, b, p.target, part);
+  const Part part{partial, partial + (size_t)p.row_slots * c.kv_heads * C::kRows * D, p.row_slots};
+  hipError_t e = launch_kernel(rows_kernel<D, kFormat, NQ>, dim3(p.row_grid * c.kv_heads),
+                               dim3(64 * C::kWaves), st, {}, a, c, b, p.row_target, part);
   if (e != hipSuccess) return e;
   const int64_t joins = (int64_t)b.num_seqs * c.kv_heads;
   return launch_kernel(join_kernel<D, C::kRows>, dim3(joins < kMostBlocks ? joins : kMostBlocks),
-                       dim3(256), st, {}, a, c.kv_heads, b, p.target, (int)C::kWaves, part);
+                       dim3(256), st, {}, a, c.kv_heads, b, p.row_target, (int)C::kWaves, part);
 }
 template <int D, int kFormat>
 hipError_t launch(const AttnArgs &a, const CacheView &c, const BatchView &b, const AttnPlan &p,
                   float *partial, hipStream_t st) {
-  const int n = row_tiles(b.max_tokens * a.group, D);
-  if (n == 1) return launch<D, kFormat, 1>(a, c, b, p, partial, st);
-  if (n == 2) return launch<D, kFormat, 2>(a, c, b, p, partial, st);
-  if constexpr (D < 256) return launch<D, kFormat, 4>(a, c, b, p, partial, st);
-  return hipErrorInvalidValue;
+  if constexpr (D < 256)
+    if (p.row_tiles == 2) return launch<D, kFormat, 2>(a, c, b, p, partial, st);
+  return launch<D, kFormat, 1>(a, c, b, p, partial, st);
 }
 template <int D>
 hipError_t launch(const AttnArgs &a, const CacheView &c, int format, const BatchView &b,
@@ -503,25 +475,9 @@ hipError_t launch(const AttnArgs &a, const CacheView &c, int format, const Batch
 
 }  // namespace
 
-AttnPlan attention_plan(const CacheView &c, int D, int format, const BatchView &b, int heads,
-                        int max_length) {
-  AttnPlan p{};
-  const int group = heads / c.kv_heads;
-  const int64_t rows = (int64_t)b.max_tokens * group;
-  const int kRows = 16 * row_tiles(rows > 64 ? 64 : (int)rows, D);
-  p.target = (1024 + c.kv_heads - 1) / c.kv_heads;
-  p.units = p.target + b.num_seqs;
-  const int64_t blocks = (int64_t)b.num_seqs * ((max_length + 127) / 128 + rows / kRows + 1);
-  const int64_t most = kMostBlocks / c.kv_heads;
-  p.grid = (int)(blocks < most ? blocks : most);
-  p.partial = (size_t)p.units * c.kv_heads * kRows * (D + 2) * sizeof(float);
-  (void)format;
-  return p;
-}
-
-hipError_t launch_attention(const AttnArgs &a, const CacheView &c, int D, int format,
-                            const BatchView &b, const AttnPlan &p, float *partial,
-                            hipStream_t st) {
+hipError_t launch_attention_rows(const AttnArgs &a, const CacheView &c, int D, int format,
+                                 const BatchView &b, const AttnPlan &p, float *partial,
+                                 hipStream_t st) {
   if (D == 64) return launch<64>(a, c, format, b, p, partial, st);
   if (D == 128) return launch<128>(a, c, format, b, p, partial, st);
   return launch<256>(a, c, format, b, p, partial, st);

@@ -1,0 +1,555 @@
+// attention_tiles.hip -- attention of many query rows of each kv head over the paged
+// cache (chunks of a prefill). A row is one query head of one token; the rows of the
+// heads that share a kv head follow each other token by token, 128 to a block.
+//
+// Each wavefront has 32 rows, the block's four share tiles of keys and values in LDS.
+// Scores are taken with keys as the matrix instruction's rows and queries as its
+// columns: lane l holds query l % 32 and half of the keys, so that a row's maximum and
+// sum stay in the lane but for one exchange with lane l ^ 32, and the probabilities
+// are where the second product takes them from, with the values transposed by the LDS
+// reads. The running maximum is raised only when a row's grows by more than 2^8, so
+// that most tiles leave the results alone: a probability may be as large as that, which
+// neither its bf16 rounding nor the fp32 sums mind.
+//
+// Bound by the matrix instructions together with the exponentials: of 64 keys, 32
+// matrix instructions of 32 cycles against about 1000 cycles of vector instructions.
+// Two blocks share a compute unit, one's softmax under the other's products.
+#include "attention_device.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256, kWaves = 4;
+constexpr float kGrow = 8.0f;  // log2 of what a row's maximum may grow unseen
+
+template <int D, int kFormat>
+struct Cfg {
+  static constexpr bool k8 = kFormat != kBf16Cache;
+  static constexpr int kKeys = D == 256 ? 32 : 64;  // of a tile
+  static constexpr int kSub = kKeys / 16;           // runs of 16 keys: each in one page
+  static constexpr int kRow = 2 * D;                // bytes of a row in LDS (bf16)
+  static constexpr int kTile = kKeys * kRow;
+  static constexpr int kScales = k8 ? 2 * kKeys * 4 : 0;
+  static constexpr int kStage = 2 * kTile + kScales;
+  static constexpr int kLds = 2 * kStage;
+  static constexpr int kBlocks = kKeys / 32;  // of 32 keys
+  static constexpr int kSteps = D / 16;       // matrix instructions of a score block
+  static constexpr int kOut = D / 32;
+  static constexpr int kPerUnit = D == 256 ? 1 : 2;  // blocks on a compute unit (registers)
+};
+
+__device__ __forceinline__ v16f mfma32bf(v8bf a, v8bf b, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+// The other half of the wavefront's value, joined to this one's.
+__device__ __forceinline__ float halves_max(float v) { return fmaxf(v, __shfl_xor(v, 32)); }
+__device__ __forceinline__ float halves_sum(float v) { return v + __shfl_xor(v, 32); }
+
+// Work of one sequence: row tiles, and pieces that the keys of each are split into.
+struct TileWork {
+  Seq s;
+  int rows, tiles;  // query rows of a kv head, and blocks of them; 0: none here
+  int keys;         // key tiles of the last row tile
+};
+template <int kKeys>
+__device__ __forceinline__ TileWork tile_work(const AttnArgs &a, const BatchView &bt, int b) {
+  TileWork w{};
+  if (b >= bt.num_seqs) return w;
+  w.s = seq_of(bt, b);
+  const int n = w.s.n < bt.max_tokens ? w.s.n : bt.max_tokens;
+  if (n > 0 && n > a.few_rows / a.group) {
+    w.rows = n * a.group;
+    w.tiles = (w.rows + kTileRows - 1) / kTileRows;
+    const int first = w.s.len - w.s.n, i0 = (w.tiles - 1) * kTileRows / a.group;
+    const int lo = seen_lo(first + i0, a.window);
+    const int hi = seen_hi(first + n - 1, w.s.len, a.causal);
+    w.keys = hi > lo ? (hi + kKeys - 1) / kKeys - lo / kKeys : 0;
+  }
+  return w;
+}
+__device__ __forceinline__ int pieces_of(const TileWork &w, int chunk) {
+  const int n = (w.keys + chunk - 1) / chunk;
+  return n > 1 ? n : 1;
+}
+// Key tiles of a piece, at least 512 keys, such that all row tiles make about `target`.
+template <int kKeys>
+__device__ __forceinline__ int chunk_of(const AttnArgs &a, const BatchView &bt, int target,
+                                        int lane) {
+  uint64_t sum = 0;
+  for (int b0 = 0; b0 < bt.num_seqs; b0 += 64) {
+    const TileWork w = tile_work<kKeys>(a, bt, b0 + lane);
+    sum += (uint64_t)w.tiles * (uint64_t)w.keys;
+  }
+  sum = wave_sum_u64(sum);
+  uint64_t c = (sum + target - 1) / target;
+  if (c > 1u << 30) c = 1u << 30;
+  constexpr int least = 512 / kKeys;
+  return (int)c > least ? (int)c : least;
+}
+struct TileUnit {
+  int b, tile, piece, pieces, slot;
+  TileWork w;
+};
+// Unit u of a kv head: of each sequence its row tiles from the last, each piece by
+// piece (the last tile sees the most keys: the long ones come first).
+template <int kKeys>
+__device__ __forceinline__ TileUnit find_unit(const AttnArgs &a, const BatchView &bt, int64_t u,
+                                              int chunk, int lane) {
+  int64_t before = 0;
+  int slots = 0;
+  for (int b0 = 0; b0 < bt.num_seqs; b0 += 64) {
+    const TileWork w = tile_work<kKeys>(a, bt, b0 + lane);
+    const int p = pieces_of(w, chunk), n = w.tiles * p;
+    const int64_t end = before + wave_incl_scan(n);
+    const int ns = p > 1 ? n : 0, send = slots + wave_incl_scan(ns);
+    const uint64_t hit = __ballot(end > u);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      auto rd = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+      TileUnit r;
+      r.b = b0 + l;
+      r.pieces = rd(p);
+      const int all = rd(n), at = (int)(u - (int64_t)lane_read64((uint64_t)end, l) + all);
+      r.tile = all / r.pieces - 1 - at / r.pieces;
+      r.piece = at % r.pieces;
+      r.slot = rd(send) - rd(ns) + at;
+      r.w.s = Seq{rd(w.s.start), rd(w.s.n), rd(w.s.len)};
+      r.w.rows = rd(w.rows);
+      r.w.tiles = rd(w.tiles);
+      r.w.keys = rd(w.keys);
+      return r;
+    }
+    before = (int64_t)lane_read64((uint64_t)end, 63);
+    slots = __builtin_amdgcn_readlane(send, 63);
+  }
+  TileUnit r{};
+  r.b = -1;
+  return r;
+}
+
+struct TilePart {  // of each kv head `slots` of kTileRows rows
+  float *o, *ml;
+  int slots;
+};
+
+// Rows of a tile of bf16 elements in LDS, chunks of 16 bytes exchanged as Tile has them.
+template <int D>
+__device__ __forceinline__ int key_at(int r, int c) {
+  return r * 2 * D + Tile<D, kBf16Cache>::key_chunk(r, c) * 16;
+}
+template <int D>
+__device__ __forceinline__ int value_at(int r, int c) {
+  return r * 2 * D + Tile<D, kBf16Cache>::value_chunk(r, c) * 16;
+}
+// A operand of 32 elements x 16 keys (keys r0 + 8 e + 4 (l / 32) + 0..3, e = 0, 1):
+// lane l has element 32 dt + l % 32.
+template <int D>
+__device__ __forceinline__ v8bf value_frag(const char *tile, int r0, int dt, int lane) {
+  typedef __attribute__((address_space(3))) v4s L;
+  const int i = lane & 15, r = r0 + 4 * (lane >> 5) + (i >> 2);
+  const int c = 4 * dt + 2 * ((lane >> 4) & 1) + ((i >> 1) & 1), o = (i & 1) * 8;
+  const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L *)(tile + value_at<D>(r, c) + o));
+  const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L *)(tile + value_at<D>(r + 8, c) + o));
+  return __builtin_bit_cast(v8bf, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+template <int D, int kFormat>
+__global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_kernel(
+    AttnArgs a, CacheView c, BatchView bt, int target, TilePart part) {
+  typedef Cfg<D, kFormat> C;
+  constexpr int K = C::kKeys, NB = C::kBlocks;
+  __shared__ __attribute__((aligned(1024))) char lds[C::kLds];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = lane >> 5, col = lane & 31;
+  const int h = blockIdx.x % c.kv_heads;
+  const int chunk = chunk_of<K>(a, bt, target, lane);
+  const int page_size = 1 << c.log2_page;
+  const uint32_t lds_at = __builtin_amdgcn_readfirstlane(lds_addr(lds));
+  const float scale2 = fabsf(a.scale2);
+  const uint32_t flip = a.scale2 < 0.0f ? 0x80008000u : 0u;  // (queries take the sign)
+
+  for (int64_t u = blockIdx.x / c.kv_heads;; u += gridDim.x / c.kv_heads) {
+    const TileUnit un = find_unit<K>(a, bt, u, chunk, lane);
+    if (un.b < 0) break;
+    const int r0 = un.tile * kTileRows;
+    const int r1 = un.w.rows < r0 + kTileRows ? un.w.rows : r0 + kTileRows;
+    const int len = un.w.s.len, first = len - un.w.s.n;
+    const int p0 = first + r0 / a.group, p1 = first + (r1 - 1) / a.group;
+    const int any_lo = seen_lo(p0, a.window), any_hi = seen_hi(p1, len, a.causal);
+    const int all_lo = seen_lo(p1, a.window), all_hi = seen_hi(p0, len, a.causal);
+    const int end = any_hi > any_lo ? (any_hi + K - 1) / K : any_lo / K;
+    const int t0 = any_lo / K + un.piece * chunk;
+    const int t1 = un.piece + 1 < un.pieces && t0 + chunk < end ? t0 + chunk : end;
+
+    const int row = r0 + 32 * wave + col, tok = row / a.group;
+    const bool there = row < r1;
+    const int lo = seen_lo(first + tok, a.window);
+    const int hi = there ? seen_hi(first + tok, len, a.causal) : 0;
+    v8bf q[C::kSteps];
+    {
+      const uint16_t *src = a.q + (int64_t)(un.w.s.start + tok) * a.ld_q +
+                            (h * a.group + row % a.group) * D + 8 * half;
+#pragma unroll
+      for (int s = 0; s < C::kSteps; ++s) {
+        v4i w = {0, 0, 0, 0};
+        if (there) w = *reinterpret_cast<const v4i_a2 *>(src + 16 * s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] ^= (int)flip;
+        q[s] = __builtin_bit_cast(v8bf, w);
+      }
+    }
+
+    // page of run x of 16 keys of tile t (-1: no key of it is seen)
+    auto page_of = [&](int t, int x) {
+      const int key = t * K + 16 * x;
+      return key < any_hi && t < t1
+                 ? scalar_word(bt.table, (int64_t)un.b * bt.ld_table + (key >> c.log2_page))
+                 : -1;
+    };
+    auto exists = [&](int p) { return (uint32_t)p < (uint32_t)c.num_pages; };
+    // places of run x of tile t in its page (a page that does not exist: page 0, masked)
+    auto place = [&](int t, int x) {
+      return ((int64_t)h << c.log2_page) + ((t * K + 16 * x) & (page_size - 1));
+    };
+
+    typedef int Pages __attribute__((ext_vector_type(C::kSub)));
+    Pages pg, ng;
+    // a tile on its way: direct loads (bf16), or codes in registers, converted when
+    // they are put into LDS
+    constexpr int kPer = C::k8 ? K * D / 16 / kThreads : 1;
+    v4i codes[2][kPer];
+    float scl = 0.0f;
+    auto fetch = [&](int buf, int t, Pages pages) {
+      if constexpr (!C::k8) {
+        constexpr int kEach = C::kTile / 1024 / kWaves;  // loads of 1 KB by a wavefront
+        const int x = wave * (K / kWaves) / 16;
+        int p = pages[0];
+#pragma unroll
+        for (int i = 1; i < C::kSub; ++i) p = x == i ? pages[i] : p;
+        const int64_t from = (exists(p) ? p : 0) * c.page_bytes + place(t, x) * C::kRow;
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) {
+            const int byte = (wave * kEach + i) * 1024 + lane * 16, r = byte / C::kRow;
+            const int ch = byte % C::kRow / 16;
+            const int src = v ? Tile<D, kBf16Cache>::value_chunk(r, ch)
+                              : Tile<D, kBf16Cache>::key_chunk(r, ch);
+            dma16((v ? c.v : c.k) + from + (r & 15) * C::kRow + src * 16,
+                  lds_at + buf * C::kStage + v * C::kTile + (wave * kEach + i) * 1024);
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          // (a wavefront's rows lie in one run of 16)
+          const int piece = i * kThreads + tid, r = piece / (D / 16);
+          const int x = __builtin_amdgcn_readfirstlane(r >> 4);
+          int p = pages[0];
+#pragma unroll
+          for (int j = 1; j < C::kSub; ++j) p = x == j ? pages[j] : p;
+          const int64_t from = (exists(p) ? p : 0) * c.page_bytes +
+                               (place(t, x) + (r & 15)) * D + piece % (D / 16) * 16;
+          codes[0][i] = *reinterpret_cast<const v4i *>(c.k + from);
+          codes[1][i] = *reinterpret_cast<const v4i *>(c.v + from);
+        }
+        if (tid < 2 * K) {
+          const int r = tid % K, x = r >> 4;
+          int p = pages[0];
+#pragma unroll
+          for (int j = 1; j < C::kSub; ++j) p = x == j ? pages[j] : p;
+          scl = (tid < K ? c.k_scale : c.v_scale)[(exists(p) ? p : 0) * c.scale_stride +
+                                                  place(t, x) + (r & 15)];
+        }
+      }
+    };
+    auto put = [&](int buf) {
+      if constexpr (C::k8) {
+        char *const st = lds + buf * C::kStage;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int piece = i * kThreads + tid, r = piece / (D / 16), ch = piece % (D / 16) * 2;
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const v8bf x = code8_bf16<kFormat>(codes[v][i][2 * e], codes[v][i][2 * e + 1]);
+              *reinterpret_cast<v8bf *>(st + v * C::kTile + (v ? value_at<D>(r, ch + e)
+                                                               : key_at<D>(r, ch + e))) = x;
+            }
+        }
+        if (tid < 2 * K) reinterpret_cast<float *>(st + 2 * C::kTile)[tid] = scl;
+      }
+    };
+
+    v16f o[C::kOut];
+#pragma unroll
+    for (int d = 0; d < C::kOut; ++d) o[d] = v16f{};
+    float m = kNoMax, l = 0.0f;
+
+    if (t0 < t1) {
+#pragma unroll
+      for (int x = 0; x < C::kSub; ++x) pg[x] = page_of(t0, x);
+      fetch(0, t0, pg);
+#pragma unroll
+      for (int x = 0; x < C::kSub; ++x) ng[x] = page_of(t0 + 1, x);
+      put(0);
+    }
+    for (int t = t0, buf = 0; t < t1; ++t, buf ^= 1) {
+      // tile t is in LDS, and every wavefront is done with the one before
+      if constexpr (C::k8) __syncthreads();
+      else wait_barrier<0>();
+      if (t + 1 < t1) fetch(buf ^ 1, t + 1, ng);
+      char *const kt = lds + buf * C::kStage, *const vt = kt + C::kTile;
+      const float *const sc = reinterpret_cast<const float *>(vt + C::kTile);
+      const int key0 = t * K;
+      bool whole = key0 >= all_lo && key0 + K <= all_hi;
+      bool ok[C::kSub];
+#pragma unroll
+      for (int x = 0; x < C::kSub; ++x) {
+        ok[x] = exists(pg[x]);
+        whole = whole && ok[x];
+        pg[x] = ng[x];
+        ng[x] = page_of(t + 2, x);
+      }
+      const bool masked = !whole;
+      if (masked) {
+        // values that no row of the block sees count as zeros, whatever lies there
+        for (int i = tid; i < C::kTile / 16; i += kThreads) {
+          const int r = i / (C::kRow / 16), key = key0 + r;
+          bool gone = key < any_lo || key >= any_hi;
+#pragma unroll
+          for (int x = 0; x < C::kSub; ++x) gone = gone || ((r >> 4) == x && !ok[x]);
+          if (gone) reinterpret_cast<v4i *>(vt)[i] = v4i{0, 0, 0, 0};
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      }
+
+      // scores: block n, register i: key 32 n + 8 (i / 4) + 4 half + i % 4
+      v16f s[NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        s[n] = v16f{};
+#pragma unroll
+        for (int i = 0; i < C::kSteps; ++i) {
+          const v8bf f = *reinterpret_cast<const v8bf *>(
+              kt + key_at<D>(32 * n + col, 2 * i + half));
+          s[n] = mfma32bf(f, q[i], s[n]);
+        }
+      }
+      if constexpr (C::k8) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const v4f ks = *reinterpret_cast<const v4f *>(sc + 32 * n + 8 * i + 4 * half);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[n][4 * i + j] *= ks[j];
+          }
+      }
+      uint32_t seen = 0xffffffffu;
+      if (masked) {
+        seen = 0;
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int at = 32 * n + 8 * (i / 4) + 4 * half + i % 4, key = key0 + at;
+            const bool see = key >= lo && key < hi && ok[2 * n + i / 8];
+            s[n][i] = see ? s[n][i] : -INFINITY;
+            if (see) seen |= 1u << (16 * n + i);
+          }
+      }
+      float big = s[0][0];
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) big = fmaxf(big, s[n][i]);
+      big = halves_max(big) * scale2;
+      if (__any(big > m + kGrow)) {
+        const float mm = fmaxf(m, big), f = __builtin_amdgcn_exp2f(m - mm);
+        m = mm;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < C::kOut; ++d) o[d] *= f;
+      }
+      v8bf p[2 * NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        float e[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], scale2, -m));
+        if (masked) {  // (-inf times a scale of 0)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) e[i] = seen >> (16 * n + i) & 1 ? e[i] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) l += e[i];
+        if constexpr (C::k8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const v4f vs = *reinterpret_cast<const v4f *>(sc + K + 32 * n + 8 * i + 4 * half);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const bool see = !masked || (seen >> (16 * n + 4 * i + j) & 1);
+              e[4 * i + j] = see ? e[4 * i + j] * vs[j] : 0.0f;
+            }
+          }
+        }
+        // rounded to bf16 for the second product: half a step of 2^-8 each, which the
+        // result, itself rounded so, averages over its keys
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          p[2 * n + x] = __builtin_bit_cast(
+              v8bf, v4i{(int)bf16x2(e[8 * x], e[8 * x + 1]), (int)bf16x2(e[8 * x + 2], e[8 * x + 3]),
+                        (int)bf16x2(e[8 * x + 4], e[8 * x + 5]),
+                        (int)bf16x2(e[8 * x + 6], e[8 * x + 7])});
+      }
+      // Values that are not finite, in a tile of which some rows do not see all: an unseen
+      // one must not reach a row through 0 times infinity. They are taken out here, and
+      // put back after the product as marks (in the keys' place) times what a row sees.
+      // (Every wavefront looks at the whole tile, so that all come to the same.)
+      bool odd = false;
+      if (masked) {
+        for (int i = lane; i < C::kTile / 16; i += 64)
+          odd |= any_odd(reinterpret_cast<const v8bf *>(vt)[i]);
+        odd = __any(odd);
+        if (odd) {
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          for (int i = tid; i < C::kTile / 16; i += kThreads) {
+            const v8bf v = reinterpret_cast<const v8bf *>(vt)[i];
+            reinterpret_cast<v8bf *>(kt)[i] = odd_part<true>(v);
+            reinterpret_cast<v8bf *>(vt)[i] = odd_part<false>(v);
+          }
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2 * NB; ++x)
+#pragma unroll
+        for (int d = 0; d < C::kOut; ++d)
+          o[d] = mfma32bf(value_frag<D>(vt, 16 * x, d, lane), p[x], o[d]);
+      if (odd) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {  // 32 keys: what a sum of marks can count
+          v8bf sees[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            v4i one = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              one[j / 2] |= (seen >> (16 * n + 8 * x + j) & 1) * 0x3f80 << 16 * (j & 1);
+            sees[x] = __builtin_bit_cast(v8bf, one);
+          }
+#pragma unroll
+          for (int d = 0; d < C::kOut; ++d) {
+            v16f marks = v16f{};
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              marks = mfma32bf(value_frag<D>(kt, 32 * n + 16 * x, d, lane), sees[x], marks);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] = add_odd(o[d][i], marks[i]);
+            __builtin_amdgcn_sched_barrier(0);  // (this path need not be fast: few registers)
+          }
+        }
+      }
+      if (t + 1 < t1) put(buf ^ 1);
+    }
+
+    l = halves_sum(l);
+    if (there) {
+      if (un.pieces == 1) {
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        uint16_t *dst = a.out + (int64_t)(un.w.s.start + tok) * a.ld_out +
+                        (h * a.group + row % a.group) * D + 4 * half;
+#pragma unroll
+        for (int d = 0; d < C::kOut; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<v2i_e2 *>(dst + 32 * d + 8 * i) =
+                v2i{(int)bf16x2(o[d][4 * i] * inv, o[d][4 * i + 1] * inv),
+                    (int)bf16x2(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
+      } else {
+        const int64_t at = ((int64_t)h * part.slots + un.slot) * kTileRows + (row - r0);
+#pragma unroll
+        for (int d = 0; d < C::kOut; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<v4f *>(part.o + at * D + 32 * d + 8 * i + 4 * half) =
+                v4f{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+        if (half == 0) {
+          part.ml[2 * at] = m;
+          part.ml[2 * at + 1] = l;
+        }
+      }
+    }
+    __syncthreads();  // LDS is the next unit's
+  }
+}
+
+// Joins the pieces of each row tile whose keys were split.
+template <int D, int kKeys>
+__global__ __launch_bounds__(kThreads) void tiles_join_kernel(AttnArgs a, int kv_heads, BatchView bt,
+                                                              int target, TilePart part) {
+  const int h = blockIdx.x % kv_heads, lane = threadIdx.x & 63;
+  const int chunk = chunk_of<kKeys>(a, bt, target, lane);
+  // (a block takes the row tile whose first piece its unit is, and passes over others)
+  for (int64_t u = blockIdx.x / kv_heads;; u += gridDim.x / kv_heads) {
+    const TileUnit un = find_unit<kKeys>(a, bt, u, chunk, lane);
+    if (un.b < 0) break;
+    if (un.pieces < 2 || un.piece > 0) continue;
+    const int r0 = un.tile * kTileRows;
+    const int rows = un.w.rows - r0 < kTileRows ? un.w.rows - r0 : kTileRows;
+    const int64_t at0 = ((int64_t)h * part.slots + un.slot) * kTileRows;
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4, row = r0 + r;
+      float m = kNoMax, l = 0.0f;
+      for (int p = 0; p < un.pieces; ++p) m = fmaxf(m, part.ml[2 * (at0 + p * kTileRows + r)]);
+      v4f v = {0, 0, 0, 0};
+      for (int p = 0; p < un.pieces; ++p) {
+        const int64_t at = at0 + p * kTileRows + r;
+        const float f = __builtin_amdgcn_exp2f(part.ml[2 * at] - m);
+        l += part.ml[2 * at + 1] * f;
+        v += *reinterpret_cast<const v4f *>(part.o + at * D + d) * f;
+      }
+      v *= l != 0.0f ? 1.0f / l : 0.0f;
+      uint16_t *dst = a.out + (int64_t)(un.w.s.start + row / a.group) * a.ld_out +
+                      (h * a.group + row % a.group) * D + d;
+      *reinterpret_cast<v2i_e2 *>(dst) = v2i{(int)bf16x2(v[0], v[1]), (int)bf16x2(v[2], v[3])};
+    }
+  }
+}
+
+template <int D, int kFormat>
+hipError_t launch(const AttnArgs &a, const CacheView &c, const BatchView &b, const AttnPlan &p,
+                  float *partial, hipStream_t st) {
+  float *const at = reinterpret_cast<float *>((char *)partial + p.tile_at);
+  const TilePart part{at, at + (size_t)p.tile_slots * c.kv_heads * kTileRows * D, p.tile_slots};
+  const dim3 grid(p.tile_grid * c.kv_heads), block(kThreads);
+  const hipError_t e = launch_kernel(tiles_kernel<D, kFormat>, grid, block, st, {}, a, c, b,
+                                     p.tile_target, part);
+  if (e != hipSuccess || p.tile_slots == 0) return e;
+  return launch_kernel(tiles_join_kernel<D, Cfg<D, kFormat>::kKeys>, grid, block, st, {}, a,
+                       c.kv_heads, b, p.tile_target, part);
+}
+template <int D>
+hipError_t launch(const AttnArgs &a, const CacheView &c, int format, const BatchView &b,
+                  const AttnPlan &p, float *partial, hipStream_t st) {
+  if (format == kBf16Cache) return launch<D, kBf16Cache>(a, c, b, p, partial, st);
+  if (format == MOE_W8A8_FORMAT_FP8)
+    return launch<D, MOE_W8A8_FORMAT_FP8>(a, c, b, p, partial, st);
+  return launch<D, MOE_W8A8_FORMAT_INT8>(a, c, b, p, partial, st);
+}
+
+}  // namespace
+
+hipError_t launch_attention_tiles(const AttnArgs &a, const CacheView &c, int D, int format,
+                                  const BatchView &b, const AttnPlan &p, float *partial,
+                                  hipStream_t st) {
+  if (D == 64) return launch<64>(a, c, format, b, p, partial, st);
+  if (D == 128) return launch<128>(a, c, format, b, p, partial, st);
+  return launch<256>(a, c, format, b, p, partial, st);
+}
+
+}  // namespace moe

@@ -194,6 +194,15 @@ __device__ __forceinline__ uint64_t wave_incl_scan_u64(uint64_t v) {
   v += dpp_u64<0x143, 0xC>(v);
   return v;
 }
+// A lane's 64-bit value, and the sum over the wavefront, in every lane.
+__device__ __forceinline__ uint64_t lane_read64(uint64_t v, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
+  return ((uint64_t)hi << 32) | lo;
+}
+__device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
+  return lane_read64(wave_incl_scan_u64(v), 63);
+}
 // Maximum of 64-bit unsigned values over the wavefront, in every lane (every
 // lane active; 0 is the identity).
 __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
