@@ -24,14 +24,30 @@ __device__ __forceinline__ int scalar_word(const int32_t *p, int64_t i) {
   return ((const __attribute__((address_space(4))) int32_t *)(uintptr_t)p)[i];
 }
 
+// This lane's value and that of lane l ^ 32, in the order of the halves.
+struct Two {
+  float lo, hi;
+};
+__device__ __forceinline__ Two halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return Two{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+__device__ __forceinline__ float halves_max(float v) {
+  const Two t = halves(v);
+  return fmaxf(t.lo, t.hi);
+}
+__device__ __forceinline__ float halves_sum(float v) {
+  const Two t = halves(v);
+  return t.lo + t.hi;
+}
 // Largest of the four 16-lane groups' values, and their sum, in every lane.
 __device__ __forceinline__ float groups_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return halves_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
 }
 __device__ __forceinline__ float groups_sum(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return halves_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
 // Eight codes as bf16, exactly.

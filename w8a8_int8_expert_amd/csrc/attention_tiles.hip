@@ -14,6 +14,12 @@
 // Bound by the matrix instructions together with the exponentials: of 64 keys, 32
 // matrix instructions of 32 cycles against about 1000 cycles of vector instructions.
 // Two blocks share a compute unit, one's softmax under the other's products.
+//
+// Nothing between a tile's barriers diverges (loops run by shared counts, conditions of
+// single lanes select): the compiler has been seen to put a copy of a live register,
+// where registers are short, before the restore of the lanes that such a branch left.
+#include <type_traits>
+
 #include "attention_device.h"
 
 namespace moe {
@@ -35,16 +41,12 @@ struct Cfg {
   static constexpr int kBlocks = kKeys / 32;  // of 32 keys
   static constexpr int kSteps = D / 16;       // matrix instructions of a score block
   static constexpr int kOut = D / 32;
-  static constexpr int kPerUnit = D == 256 ? 1 : 2;  // blocks on a compute unit (registers)
+  static constexpr int kPerUnit = D == 256 || (k8 && D == 128) ? 1 : 2;  // blocks on a compute unit (registers)
 };
 
 __device__ __forceinline__ v16f mfma32bf(v8bf a, v8bf b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
-// The other half of the wavefront's value, joined to this one's.
-__device__ __forceinline__ float halves_max(float v) { return fmaxf(v, __shfl_xor(v, 32)); }
-__device__ __forceinline__ float halves_sum(float v) { return v + __shfl_xor(v, 32); }
-
 // Work of one sequence: row tiles, and pieces that the keys of each are split into.
 struct TileWork {
   Seq s;
@@ -169,6 +171,19 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
   const float scale2 = fabsf(a.scale2);
   const uint32_t flip = a.scale2 < 0.0f ? 0x80008000u : 0u;  // (queries take the sign)
 
+  // Direct loads: a wavefront's kEach loads of 1 KB take consecutive rows; which chunk
+  // a lane reads depends on its row and the exchange, the same for loads 8 rows apart.
+  constexpr int kEach = C::kTile / 1024 / kWaves, kLoadRows = 1024 / C::kRow;
+  constexpr int kKinds = kLoadRows >= 8 ? 1 : 8 / kLoadRows < kEach ? 8 / kLoadRows : kEach;
+  uint32_t lane_at[2][kKinds];
+#pragma unroll
+  for (int i = 0; i < kKinds; ++i) {
+    const int r = wave * kEach * kLoadRows + i * kLoadRows + lane * 16 / C::kRow;
+    const int ch = lane * 16 % C::kRow / 16, in = lane * 16 / C::kRow * C::kRow;
+    lane_at[0][i] = in + Tile<D, kBf16Cache>::key_chunk(r, ch) * 16;
+    lane_at[1][i] = in + Tile<D, kBf16Cache>::value_chunk(r, ch) * 16;
+  }
+
   for (int64_t u = blockIdx.x / c.kv_heads;; u += gridDim.x / c.kv_heads) {
     const TileUnit un = find_unit<K>(a, bt, u, chunk, lane);
     if (un.b < 0) break;
@@ -182,8 +197,10 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
     const int t0 = any_lo / K + un.piece * chunk;
     const int t1 = un.piece + 1 < un.pieces && t0 + chunk < end ? t0 + chunk : end;
 
-    const int row = r0 + 32 * wave + col, tok = row / a.group;
-    const bool there = row < r1;
+    // (a lane past the last row computes that one again and sees nothing)
+    const int row_ = r0 + 32 * wave + col;
+    const bool there = row_ < r1;
+    const int row = there ? row_ : r1 - 1, tok = row / a.group;
     const int lo = seen_lo(first + tok, a.window);
     const int hi = there ? seen_hi(first + tok, len, a.causal) : 0;
     v8bf q[C::kSteps];
@@ -192,8 +209,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
                             (h * a.group + row % a.group) * D + 8 * half;
 #pragma unroll
       for (int s = 0; s < C::kSteps; ++s) {
-        v4i w = {0, 0, 0, 0};
-        if (there) w = *reinterpret_cast<const v4i_a2 *>(src + 16 * s);
+        v4i w = *reinterpret_cast<const v4i_a2 *>(src + 16 * s);
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] ^= (int)flip;
         q[s] = __builtin_bit_cast(v8bf, w);
@@ -220,25 +236,21 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
     constexpr int kPer = C::k8 ? K * D / 16 / kThreads : 1;
     v4i codes[2][kPer];
     float scl = 0.0f;
-    auto fetch = [&](int buf, int t, Pages pages) {
+    auto fetch = [&](int buf, int t, Pages pages) __attribute__((always_inline)) {
       if constexpr (!C::k8) {
-        constexpr int kEach = C::kTile / 1024 / kWaves;  // loads of 1 KB by a wavefront
         const int x = wave * (K / kWaves) / 16;
         int p = pages[0];
 #pragma unroll
         for (int i = 1; i < C::kSub; ++i) p = x == i ? pages[i] : p;
-        const int64_t from = (exists(p) ? p : 0) * c.page_bytes + place(t, x) * C::kRow;
+        const int64_t from = (exists(p) ? p : 0) * c.page_bytes +
+                             (place(t, x) + wave * (K / kWaves) % 16) * C::kRow;
 #pragma unroll
         for (int v = 0; v < 2; ++v)
 #pragma unroll
-          for (int i = 0; i < kEach; ++i) {
-            const int byte = (wave * kEach + i) * 1024 + lane * 16, r = byte / C::kRow;
-            const int ch = byte % C::kRow / 16;
-            const int src = v ? Tile<D, kBf16Cache>::value_chunk(r, ch)
-                              : Tile<D, kBf16Cache>::key_chunk(r, ch);
-            dma16((v ? c.v : c.k) + from + (r & 15) * C::kRow + src * 16,
+          for (int i = 0; i < kEach; ++i)
+            // a load's rows: of the four kinds of exchange that its number decides
+            dma16((v ? c.v : c.k) + from + i * 1024, lane_at[v][i % kKinds],
                   lds_at + buf * C::kStage + v * C::kTile + (wave * kEach + i) * 1024);
-          }
       } else {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -253,14 +265,13 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
           codes[0][i] = *reinterpret_cast<const v4i *>(c.k + from);
           codes[1][i] = *reinterpret_cast<const v4i *>(c.v + from);
         }
-        if (tid < 2 * K) {
-          const int r = tid % K, x = r >> 4;
-          int p = pages[0];
+        // (the scales of 2 K places, by all threads: the same one more than once)
+        const int r = tid % K, x = r >> 4;
+        int p = pages[0];
 #pragma unroll
-          for (int j = 1; j < C::kSub; ++j) p = x == j ? pages[j] : p;
-          scl = (tid < K ? c.k_scale : c.v_scale)[(exists(p) ? p : 0) * c.scale_stride +
-                                                  place(t, x) + (r & 15)];
-        }
+        for (int j = 1; j < C::kSub; ++j) p = x == j ? pages[j] : p;
+        scl = (tid & K ? c.v_scale : c.k_scale)[(exists(p) ? p : 0) * c.scale_stride + place(t, x) +
+                                                (r & 15)];
       }
     };
     auto put = [&](int buf) {
@@ -278,7 +289,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
                                                                : key_at<D>(r, ch + e))) = x;
             }
         }
-        if (tid < 2 * K) reinterpret_cast<float *>(st + 2 * C::kTile)[tid] = scl;
+        reinterpret_cast<float *>(st + 2 * C::kTile)[tid % (2 * K)] = scl;
       }
     };
 
@@ -286,44 +297,29 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
 #pragma unroll
     for (int d = 0; d < C::kOut; ++d) o[d] = v16f{};
     float m = kNoMax, l = 0.0f;
+    bool some_odd = false;
 
-    if (t0 < t1) {
+    // values of a tile in LDS that no row of the block sees count as zeros, whatever lies
+    // there
+    auto clear_unseen = [&](char *vt, int key0, const bool *ok) {
+      for (int y = 0; y < C::kTile / 16 / kThreads; ++y) {
+        const int i = y * kThreads + tid, r = i / (C::kRow / 16), key = key0 + r;
+        int gone = (key < any_lo) | (key >= any_hi);
 #pragma unroll
-      for (int x = 0; x < C::kSub; ++x) pg[x] = page_of(t0, x);
-      fetch(0, t0, pg);
+        for (int x = 0; x < C::kSub; ++x) gone |= (r >> 4 == x) & !ok[x];
+        v4i v = reinterpret_cast<const v4i *>(vt)[i];
 #pragma unroll
-      for (int x = 0; x < C::kSub; ++x) ng[x] = page_of(t0 + 1, x);
-      put(0);
-    }
-    for (int t = t0, buf = 0; t < t1; ++t, buf ^= 1) {
-      // tile t is in LDS, and every wavefront is done with the one before
-      if constexpr (C::k8) __syncthreads();
-      else wait_barrier<0>();
-      if (t + 1 < t1) fetch(buf ^ 1, t + 1, ng);
+        for (int j = 0; j < 4; ++j) v[j] = gone ? 0 : v[j];
+        reinterpret_cast<v4i *>(vt)[i] = v;
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
+    // scores, softmax and product of the tile in stage buf
+    auto step = [&](auto kind, int buf, int key0, const bool *ok) __attribute__((always_inline)) {
+      constexpr bool kMasked = decltype(kind)::value;
       char *const kt = lds + buf * C::kStage, *const vt = kt + C::kTile;
       const float *const sc = reinterpret_cast<const float *>(vt + C::kTile);
-      const int key0 = t * K;
-      bool whole = key0 >= all_lo && key0 + K <= all_hi;
-      bool ok[C::kSub];
-#pragma unroll
-      for (int x = 0; x < C::kSub; ++x) {
-        ok[x] = exists(pg[x]);
-        whole = whole && ok[x];
-        pg[x] = ng[x];
-        ng[x] = page_of(t + 2, x);
-      }
-      const bool masked = !whole;
-      if (masked) {
-        // values that no row of the block sees count as zeros, whatever lies there
-        for (int i = tid; i < C::kTile / 16; i += kThreads) {
-          const int r = i / (C::kRow / 16), key = key0 + r;
-          bool gone = key < any_lo || key >= any_hi;
-#pragma unroll
-          for (int x = 0; x < C::kSub; ++x) gone = gone || ((r >> 4) == x && !ok[x]);
-          if (gone) reinterpret_cast<v4i *>(vt)[i] = v4i{0, 0, 0, 0};
-        }
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      }
+      if constexpr (kMasked) clear_unseen(vt, key0, ok);
 
       // scores: block n, register i: key 32 n + 8 (i / 4) + 4 half + i % 4
       v16f s[NB];
@@ -348,7 +344,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
           }
       }
       uint32_t seen = 0xffffffffu;
-      if (masked) {
+      if constexpr (kMasked) {
         seen = 0;
 #pragma unroll
         for (int n = 0; n < NB; ++n)
@@ -373,88 +369,127 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
 #pragma unroll
         for (int d = 0; d < C::kOut; ++d) o[d] *= f;
       }
-      v8bf p[2 * NB];
-#pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        float e[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], scale2, -m));
-        if (masked) {  // (-inf times a scale of 0)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) e[i] = seen >> (16 * n + i) & 1 ? e[i] : 0.0f;
+      // Values that are not finite, in a tile of which some rows do not see all: an unseen
+      // one must not reach a row through 0 times infinity. They are taken out here, and
+      // put back behind the loop. (Every wavefront looks at the whole tile, so that all
+      // come to the same.)
+      if constexpr (kMasked) {
+        bool odd = false;
+        for (int y = 0; y < C::kTile / 16 / 64; ++y)
+          odd |= any_odd(reinterpret_cast<const v8bf *>(vt)[y * 64 + lane]);
+        if (__any(odd)) {
+          some_odd = true;
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          for (int y = 0; y < C::kTile / 16 / kThreads; ++y) {
+            v8bf *const v = reinterpret_cast<v8bf *>(vt) + y * kThreads + tid;
+            *v = odd_part<false>(*v);
+          }
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         }
+      }
+      // the probabilities of 16 keys after the other, each set on its way through the
+      // second product while the next is taken
 #pragma unroll
-        for (int i = 0; i < 16; ++i) l += e[i];
+      for (int x = 0; x < 2 * NB; ++x) {
+        float e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x / 2][8 * (x % 2) + j], scale2, -m));
+          if constexpr (kMasked) e[j] = seen >> (8 * x + j) & 1 ? e[j] : 0.0f;  // (-inf times 0)
+          l += e[j];
+        }
         if constexpr (C::k8) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const v4f vs = *reinterpret_cast<const v4f *>(sc + K + 32 * n + 8 * i + 4 * half);
+          for (int i = 0; i < 2; ++i) {
+            const v4f vs = *reinterpret_cast<const v4f *>(sc + K + 16 * x + 8 * i + 4 * half);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const bool see = !masked || (seen >> (16 * n + 4 * i + j) & 1);
+              const bool see = !kMasked || (seen >> (8 * x + 4 * i + j) & 1);
               e[4 * i + j] = see ? e[4 * i + j] * vs[j] : 0.0f;
             }
           }
         }
         // rounded to bf16 for the second product: half a step of 2^-8 each, which the
         // result, itself rounded so, averages over its keys
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          p[2 * n + x] = __builtin_bit_cast(
-              v8bf, v4i{(int)bf16x2(e[8 * x], e[8 * x + 1]), (int)bf16x2(e[8 * x + 2], e[8 * x + 3]),
-                        (int)bf16x2(e[8 * x + 4], e[8 * x + 5]),
-                        (int)bf16x2(e[8 * x + 6], e[8 * x + 7])});
-      }
-      // Values that are not finite, in a tile of which some rows do not see all: an unseen
-      // one must not reach a row through 0 times infinity. They are taken out here, and
-      // put back after the product as marks (in the keys' place) times what a row sees.
-      // (Every wavefront looks at the whole tile, so that all come to the same.)
-      bool odd = false;
-      if (masked) {
-        for (int i = lane; i < C::kTile / 16; i += 64)
-          odd |= any_odd(reinterpret_cast<const v8bf *>(vt)[i]);
-        odd = __any(odd);
-        if (odd) {
-          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-          for (int i = tid; i < C::kTile / 16; i += kThreads) {
-            const v8bf v = reinterpret_cast<const v8bf *>(vt)[i];
-            reinterpret_cast<v8bf *>(kt)[i] = odd_part<true>(v);
-            reinterpret_cast<v8bf *>(vt)[i] = odd_part<false>(v);
-          }
-          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < 2 * NB; ++x)
+        const v8bf p = __builtin_bit_cast(
+            v8bf, v4i{(int)bf16x2(e[0], e[1]), (int)bf16x2(e[2], e[3]), (int)bf16x2(e[4], e[5]),
+                      (int)bf16x2(e[6], e[7])});
 #pragma unroll
         for (int d = 0; d < C::kOut; ++d)
-          o[d] = mfma32bf(value_frag<D>(vt, 16 * x, d, lane), p[x], o[d]);
-      if (odd) {
+          o[d] = mfma32bf(value_frag<D>(vt, 16 * x, d, lane), p, o[d]);
+      }
+    };
+
+    if (t0 < t1) {
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {  // 32 keys: what a sum of marks can count
-          v8bf sees[2];
+      for (int x = 0; x < C::kSub; ++x) pg[x] = page_of(t0, x);
+      fetch(0, t0, pg);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            v4i one = {0, 0, 0, 0};
+      for (int x = 0; x < C::kSub; ++x) ng[x] = page_of(t0 + 1, x);
+      put(0);
+    }
+    for (int t = t0, buf = 0; t < t1; ++t, buf ^= 1) {
+      // tile t is in LDS, and every wavefront is done with the one before
+      if constexpr (C::k8) __syncthreads();
+      else wait_barrier<0>();
+      if (t + 1 < t1) fetch(buf ^ 1, t + 1, ng);
+      const int key0 = t * K;
+      bool whole = key0 >= all_lo && key0 + K <= all_hi;
+      bool ok[C::kSub];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              one[j / 2] |= (seen >> (16 * n + 8 * x + j) & 1) * 0x3f80 << 16 * (j & 1);
-            sees[x] = __builtin_bit_cast(v8bf, one);
-          }
+      for (int x = 0; x < C::kSub; ++x) {
+        ok[x] = exists(pg[x]);
+        whole = whole && ok[x];
+        pg[x] = ng[x];
+        ng[x] = page_of(t + 2, x);
+      }
+      if (whole) step(std::false_type{}, buf, key0, ok);
+      else step(std::true_type{}, buf, key0, ok);
+      if (t + 1 < t1) put(buf ^ 1);
+    }
+
+    // what was taken out, as marks times the keys that a row sees
+    for (int t = t0; some_odd && t < t1; ++t) {
+      const int key0 = t * K;
+      bool ok[C::kSub], whole = key0 >= all_lo && key0 + K <= all_hi;
 #pragma unroll
-          for (int d = 0; d < C::kOut; ++d) {
-            v16f marks = v16f{};
+      for (int x = 0; x < C::kSub; ++x) {
+        pg[x] = page_of(t, x);
+        ok[x] = exists(pg[x]);
+        whole = whole && ok[x];
+      }
+      if (whole) continue;
+      __syncthreads();
+      fetch(0, t, pg);
+      put(0);
+      if constexpr (C::k8) __syncthreads();
+      else wait_barrier<0>();
+      char *const vt = lds + C::kTile;
+      clear_unseen(vt, key0, ok);
+      for (int y = 0; y < C::kTile / 16 / kThreads; ++y) {
+        v8bf *const v = reinterpret_cast<v8bf *>(vt) + y * kThreads + tid;
+        *v = odd_part<true>(*v);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll 1
+      for (int x = 0; x < 2 * NB; ++x) {  // 16 keys: a sum of marks can count them
+        bool there_x = ok[0];
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-              marks = mfma32bf(value_frag<D>(kt, 32 * n + 16 * x, d, lane), sees[x], marks);
+        for (int j = 1; j < C::kSub; ++j) there_x = x == j ? ok[j] : there_x;
+        v4i one = {0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[d][i] = add_odd(o[d][i], marks[i]);
-            __builtin_amdgcn_sched_barrier(0);  // (this path need not be fast: few registers)
-          }
+        for (int j = 0; j < 8; ++j) {
+          const int key = key0 + 16 * x + 8 * (j / 4) + 4 * half + j % 4;
+          one[j / 2] |= key >= lo && key < hi && there_x ? 0x3f80 << 16 * (j & 1) : 0;
+        }
+#pragma unroll
+        for (int d = 0; d < C::kOut; ++d) {
+          const v16f marks = mfma32bf(value_frag<D>(vt, 16 * x, d, lane),
+                                      __builtin_bit_cast(v8bf, one), v16f{});
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[d][i] = add_odd(o[d][i], marks[i]);
         }
       }
-      if (t + 1 < t1) put(buf ^ 1);
     }
 
     l = halves_sum(l);

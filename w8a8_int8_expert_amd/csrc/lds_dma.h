@@ -24,6 +24,13 @@ __device__ __forceinline__ void dma16(const void *g, uint32_t lds_base) {
                : "v"(g), "s"(lds_base)
                : "memory", "m0");
 }
+// The same from a base that the wavefront shares and a 32-bit offset of each lane.
+__device__ __forceinline__ void dma16(const void *base, uint32_t off, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(lds_base)
+               : "memory", "m0");
+}
 // 4 bytes per lane into LDS at lds_base + 4*lane.
 __device__ __forceinline__ void dma4(const void *g, uint32_t lds_base) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
