@@ -155,7 +155,7 @@ AttnPlan moe::attention_plan(const CacheView &c, int D, const BatchView &b, int 
   const int group = heads / c.kv_heads;
   const int64_t rows = (int64_t)b.max_tokens * group;  // most of a sequence and kv head
   const int most_few = D == 256 ? 16 : 32;
-  const int grid_cap = kMostBlocks / c.kv_heads;
+  const int grid_cap = kMostBlocks / 2 / c.kv_heads;
   auto at_most = [](int64_t v, int64_t most) { return (int)(v < most ? v : most); };
   // All sequences have few rows; or some may, beside longer ones (where one sequence
   // is all there is, or every row is needed for the longest, none does).
@@ -195,6 +195,8 @@ int attention_shape(const moe_w8a8_kv_cache *c, const moe_w8a8_batch *b, int32_t
   MOE_TRY(cache_shape(c));
   MOE_TRY(batch_shape(b));
   if (!heads_ok(heads, c->head_dim) || heads % c->kv_heads) return MOE_W8A8_ERR_UNSUPPORTED;
+  // query rows of a kv head are counted in 32 bits
+  if (T * (heads / c->kv_heads) > 0x7fffffff - kTileRows) return MOE_W8A8_ERR_UNSUPPORTED;
   return MOE_W8A8_OK;
 }
 AttnPlan plan_of(const moe_w8a8_kv_cache &c, const moe_w8a8_batch &b, int32_t heads, int64_t T) {
@@ -246,6 +248,7 @@ extern "C" int moe_w8a8_paged_attention(const moe_w8a8_attention_args *a,
   if (p.few_rows > 0)
     MOE_CHECK(launch_attention_rows(r, cv, D, c->format, bv, p, (float *)workspace,
                                     (hipStream_t)stream));
+  MOE_CHECK(launch_attention_join(r, cv, D, bv, p, (float *)workspace, (hipStream_t)stream));
   return MOE_W8A8_OK;
 }
 

@@ -97,10 +97,25 @@ AttnPlan attention_plan(const CacheView &c, int D, const BatchView &b, int heads
 hipError_t launch_attention_rows(const AttnArgs &a, const CacheView &c, int D, int format,
                                  const BatchView &b, const AttnPlan &p, float *partial,
                                  hipStream_t st);
+// Partial results: of each kv head `slots` of so many rows (16 or 32, and kTileRows) of
+// D values, then as many (maximum, sum).
+struct Partial {
+  float *o, *ml;
+  int slots;
+};
 constexpr int kTileRows = 128;  // query rows of a block of the kernel of tiles
+inline Partial partial_few(const AttnPlan &p, int kv_heads, int D, float *ws) {
+  return Partial{ws, ws + (size_t)p.row_slots * kv_heads * 16 * p.row_tiles * D, p.row_slots};
+}
+inline Partial partial_many(const AttnPlan &p, int kv_heads, int D, float *ws) {
+  float *const at = reinterpret_cast<float *>((char *)ws + p.tile_at);
+  return Partial{at, at + (size_t)p.tile_slots * kv_heads * kTileRows * D, p.tile_slots};
+}
 hipError_t launch_attention_tiles(const AttnArgs &a, const CacheView &c, int D, int format,
                                   const BatchView &b, const AttnPlan &p, float *partial,
                                   hipStream_t st);
+hipError_t launch_attention_join(const AttnArgs &a, const CacheView &c, int D, const BatchView &b,
+                                 const AttnPlan &p, float *partial, hipStream_t st);
 
 struct LogprobArgs {
   const void *x;

@@ -10,11 +10,12 @@
 // LDS by direct loads, the next in flight while one is worked on, and no two of them
 // meet until the end.
 #include "attention_device.h"
+#include "attention_work.h"
 
 namespace moe {
 namespace {
 
-constexpr int kKeys = 32;
+constexpr int kKeys = kFewKeys;
 
 template <int D, int kFormat, int NQ>
 struct Rows {
@@ -31,90 +32,9 @@ struct Rows {
   static constexpr int kLds = kStages > kJoin ? kStages : kJoin;
 };
 
-struct Part {  // where partial results lie: of each kv head `slots` of kRows rows
-  float *o, *ml;
-  int slots;
-};
-
-// Pieces of the keys of each sequence of few rows (units): as many as make about
-// `target` of all sequences together.
-struct SeqWork {
-  Seq s;
-  int rows;    // query rows of one kv head; 0: none, or more than these kernels take
-  int t0, t1;  // key tiles
-};
-__device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, const BatchView &bt, int b) {
-  SeqWork w{};
-  if (b >= bt.num_seqs) return w;
-  w.s = seq_of(bt, b);
-  const int n = w.s.n < bt.max_tokens ? w.s.n : bt.max_tokens;
-  if (n > 0 && n <= a.few_rows / a.group) {
-    w.rows = n * a.group;
-    const int first = w.s.len - w.s.n;
-    const int lo = seen_lo(first, a.window), hi = seen_hi(first + n - 1, w.s.len, a.causal);
-    w.t0 = lo / kKeys;
-    w.t1 = hi > lo ? (hi + kKeys - 1) / kKeys : w.t0;
-  }
-  return w;
-}
-__device__ __forceinline__ int pieces_of(const SeqWork &w, int chunk) {
-  if (w.rows == 0) return 0;
-  const int n = (w.t1 - w.t0 + chunk - 1) / chunk;
-  return n > 1 ? n : 1;
-}
-__device__ __forceinline__ int chunk_of(const AttnArgs &a, const BatchView &bt, int target,
-                                        int waves, int lane) {
-  uint64_t sum = 0;
-  for (int b0 = 0; b0 < bt.num_seqs; b0 += 64) {
-    const SeqWork w = seq_work(a, bt, b0 + lane);
-    sum += (uint64_t)(w.t1 - w.t0);
-  }
-  sum = wave_sum_u64(sum);
-  uint64_t c = (sum + target - 1) / target;
-  if (c > 1u << 30) c = 1u << 30;  // (past any sequence's tiles)
-  const int chunk = (int)((c + waves - 1) / waves) * waves;
-  return chunk > waves ? chunk : waves;
-}
-// The sequence that unit u falls into, and the unit's number in it; b = -1 past the end.
-// slot: where its partial result goes. Only sequences of two pieces or more have slots:
-// these have more tiles than a chunk, so that their pieces are at most 2 `target`.
-struct Unit {
-  int b, piece, pieces, slot;
-  SeqWork w;
-};
-__device__ __forceinline__ Unit find_unit(const AttnArgs &a, const BatchView &bt, int u, int chunk,
-                                          int lane) {
-  int before = 0, slots = 0;
-  for (int b0 = 0; b0 < bt.num_seqs; b0 += 64) {
-    const SeqWork w = seq_work(a, bt, b0 + lane);
-    const int n = pieces_of(w, chunk), end = before + wave_incl_scan(n);
-    const int ns = n > 1 ? n : 0, send = slots + wave_incl_scan(ns);
-    const uint64_t hit = __ballot(end > u);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      auto rd = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
-      Unit r;
-      r.b = b0 + l;
-      r.pieces = rd(n);
-      r.piece = u - (rd(end) - r.pieces);
-      r.slot = rd(send) - rd(ns) + r.piece;
-      r.w.s = Seq{rd(w.s.start), rd(w.s.n), rd(w.s.len)};
-      r.w.rows = rd(w.rows);
-      r.w.t0 = rd(w.t0);
-      r.w.t1 = rd(w.t1);
-      return r;
-    }
-    before = __builtin_amdgcn_readlane(end, 63);
-    slots = __builtin_amdgcn_readlane(send, 63);
-  }
-  Unit r{};
-  r.b = -1;
-  return r;
-}
-
 template <int D, int kFormat, int NQ>
 __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kernel(
-    AttnArgs a, CacheView c, BatchView bt, int target, Part part) {
+    AttnArgs a, CacheView c, BatchView bt, int target, Partial part) {
   typedef Rows<D, kFormat, NQ> C;
   typedef typename C::TL TL;
   constexpr int W = C::kWaves, kSteps = D / 32, kOut = D / 16;
@@ -124,13 +44,14 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, col = lane & 15;
   const int h = blockIdx.x % c.kv_heads;
-  const int chunk = chunk_of(a, bt, target, W, lane);
+  const Schedule<true, kKeys> work(a, bt, target, kLeastFew, kLeastFew);
+  const int chunk = work.chunk;
   const int page_size = 1 << c.log2_page;
   char *const mine = lds + wave * 2 * C::kStage;
   const uint32_t mine_at = __builtin_amdgcn_readfirstlane(lds_addr(mine));
 
   for (int u = blockIdx.x / c.kv_heads;; u += gridDim.x / c.kv_heads) {
-    const Unit un = find_unit(a, bt, u, chunk, lane);
+    const Unit un = work.find(a, bt, u);
     if (un.b < 0) break;
     const int len = un.w.s.len, first = len - un.w.s.n;
     // keys that some row, and that every row sees
@@ -138,24 +59,24 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
     const int any_lo = seen_lo(p0, a.window), any_hi = seen_hi(p1, len, a.causal);
     const int all_lo = seen_lo(p1, a.window), all_hi = seen_hi(p0, len, a.causal);
     const int t0 = un.w.t0 + un.piece * chunk;
-    const int t1 = t0 + chunk < un.w.t1 ? t0 + chunk : un.w.t1;
+    const int end = un.w.t0 + un.w.keys, t1 = t0 + chunk < end ? t0 + chunk : end;
 
     // queries, and what each sees
     v8bf q[NQ][kSteps];
     int lo[NQ], hi[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      const int r = n * 16 + col, i = r / a.group;
-      const bool there = r < rows;
+      // (a lane past the last row takes that one again and sees nothing)
+      const bool there = n * 16 + col < rows;
+      const int r = there ? n * 16 + col : rows - 1, i = r / a.group;
       lo[n] = seen_lo(first + i, a.window);
       hi[n] = there ? seen_hi(first + i, len, a.causal) : 0;
       const uint16_t *src =
           a.q + (int64_t)(un.w.s.start + i) * a.ld_q + (h * a.group + r % a.group) * D;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s)
-        q[n][s] = there ? __builtin_bit_cast(v8bf, (v4i)*reinterpret_cast<const v4i_a2 *>(
-                                                       src + TL::query_at(s, lane)))
-                        : v8bf{};
+        q[n][s] = __builtin_bit_cast(
+            v8bf, (v4i)*reinterpret_cast<const v4i_a2 *>(src + TL::query_at(s, lane)));
     }
 
     // direct loads of tile t into a stage; a page that does not exist is read as page 0
@@ -228,10 +149,13 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
       ng1 = page_of((t + 2 * W) * kKeys + 16);
       if (masked) {
         // values that no row sees count as zeros, whatever lies there
-        for (int i = lane; i < TL::kBytes / 16; i += 64) {
-          const int r = i / TL::kChunks, key = key0 + r;
-          if (key < any_lo || key >= any_hi || !(r < 16 ? ok0 : ok1))
-            reinterpret_cast<v4i *>(vt)[i] = v4i{0, 0, 0, 0};
+        for (int y = 0; y < TL::kBytes / 1024; ++y) {
+          const int i = y * 64 + lane, r = i / TL::kChunks, key = key0 + r;
+          const bool gone = (key < any_lo) | (key >= any_hi) | !(r < 16 ? ok0 : ok1);
+          v4i v = reinterpret_cast<const v4i *>(vt)[i];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = gone ? 0 : v[j];
+          reinterpret_cast<v4i *>(vt)[i] = v;
         }
       }
 
@@ -285,7 +209,7 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
               const int key = key0 + 16 * x + 4 * g + i;
               const bool there = key >= lo[n] && key < hi[n] && (x ? ok1 : ok0);
               v = there ? v : -INFINITY;
-              if (!there) seen[n] &= ~(1u << (4 * x + i));
+              seen[n] &= ~((uint32_t)!there << (4 * x + i));
             }
             s[n][x][i] = v;
             mx = fmaxf(mx, v);
@@ -300,7 +224,7 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
           sum += e[j];
           if constexpr (TL::k8) {
             e[j] *= vs[j / 4][j % 4];
-            if (masked && !(seen[n] >> j & 1)) e[j] = 0.0f;
+            e[j] = masked && !(seen[n] >> j & 1) ? 0.0f : e[j];
           }
         }
         l[n] = l[n] * f + sum;
@@ -400,62 +324,13 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
   }
 }
 
-// Joins the pieces of each sequence whose keys were split.
-template <int D, int kRows>
-__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int kv_heads, BatchView bt,
-                                                   int target, int waves, Part part) {
-  const int lane = threadIdx.x & 63;
-  const int chunk = chunk_of(a, bt, target, waves, lane);
-  for (int64_t x = blockIdx.x; x < (int64_t)bt.num_seqs * kv_heads; x += gridDim.x) {
-    const int h = (int)(x % kv_heads), b = (int)(x / kv_heads);
-    int before = 0, pieces = 0;
-    SeqWork w{};
-    for (int b0 = 0; b0 <= b; b0 += 64) {
-      const SeqWork y = seq_work(a, bt, b0 + lane);
-      const int n = pieces_of(y, chunk), ns = n > 1 ? n : 0;
-      const int end = before + wave_incl_scan(ns);
-      if (b < b0 + 64) {
-        auto rd = [&](int v) { return __builtin_amdgcn_readlane(v, b - b0); };
-        w.s = Seq{rd(y.s.start), rd(y.s.n), rd(y.s.len)};
-        w.rows = rd(y.rows);
-        pieces = rd(ns);
-        before = rd(end) - pieces;
-      } else {
-        before = __builtin_amdgcn_readlane(end, 63);
-      }
-    }
-    if (pieces < 2) continue;
-    const int64_t at0 = ((int64_t)h * part.slots + before) * kRows;
-    for (int i = threadIdx.x; i < w.rows * (D / 4); i += 256) {
-      const int r = i / (D / 4), d = i % (D / 4) * 4;
-      float m = kNoMax, l = 0.0f;
-      for (int p = 0; p < pieces; ++p) m = fmaxf(m, part.ml[2 * (at0 + p * kRows + r)]);
-      v4f v = {0, 0, 0, 0};
-      for (int p = 0; p < pieces; ++p) {
-        const int64_t at = at0 + p * kRows + r;
-        const float f = __builtin_amdgcn_exp2f(part.ml[2 * at] - m);
-        l += part.ml[2 * at + 1] * f;
-        v += *reinterpret_cast<const v4f *>(part.o + at * D + d) * f;
-      }
-      v *= l != 0.0f ? 1.0f / l : 0.0f;
-      uint16_t *dst = a.out + (int64_t)(w.s.start + r / a.group) * a.ld_out +
-                      (h * a.group + r % a.group) * D + d;
-      *reinterpret_cast<v2i_e2 *>(dst) = v2i{(int)bf16x2(v[0], v[1]), (int)bf16x2(v[2], v[3])};
-    }
-  }
-}
-
 template <int D, int kFormat, int NQ>
 hipError_t launch(const AttnArgs &a, const CacheView &c, const BatchView &b, const AttnPlan &p,
                   float *partial, hipStream_t st) {
   typedef Rows<D, kFormat, NQ> C;
-  const Part part{partial, partial + (size_t)p.row_slots * c.kv_heads * C::kRows * D, p.row_slots};
-  hipError_t e = launch_kernel(rows_kernel<D, kFormat, NQ>, dim3(p.row_grid * c.kv_heads),
-                               dim3(64 * C::kWaves), st, {}, a, c, b, p.row_target, part);
-  if (e != hipSuccess) return e;
-  const int64_t joins = (int64_t)b.num_seqs * c.kv_heads;
-  return launch_kernel(join_kernel<D, C::kRows>, dim3(joins < kMostBlocks ? joins : kMostBlocks),
-                       dim3(256), st, {}, a, c.kv_heads, b, p.row_target, (int)C::kWaves, part);
+  return launch_kernel(rows_kernel<D, kFormat, NQ>, dim3(p.row_grid * c.kv_heads),
+                       dim3(64 * C::kWaves), st, {}, a, c, b, p.row_target,
+                       partial_few(p, c.kv_heads, D, partial));
 }
 template <int D, int kFormat>
 hipError_t launch(const AttnArgs &a, const CacheView &c, const BatchView &b, const AttnPlan &p,

@@ -21,6 +21,7 @@
 #include <type_traits>
 
 #include "attention_device.h"
+#include "attention_work.h"
 
 namespace moe {
 namespace {
@@ -31,7 +32,7 @@ constexpr float kGrow = 8.0f;  // log2 of what a row's maximum may grow unseen
 template <int D, int kFormat>
 struct Cfg {
   static constexpr bool k8 = kFormat != kBf16Cache;
-  static constexpr int kKeys = D == 256 ? 32 : 64;  // of a tile
+  static constexpr int kKeys = kManyKeys<D>;  // of a tile
   static constexpr int kSub = kKeys / 16;           // runs of 16 keys: each in one page
   static constexpr int kRow = 2 * D;                // bytes of a row in LDS (bf16)
   static constexpr int kTile = kKeys * kRow;
@@ -47,93 +48,6 @@ struct Cfg {
 __device__ __forceinline__ v16f mfma32bf(v8bf a, v8bf b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
-// Work of one sequence: row tiles, and pieces that the keys of each are split into.
-struct TileWork {
-  Seq s;
-  int rows, tiles;  // query rows of a kv head, and blocks of them; 0: none here
-  int keys;         // key tiles of the last row tile
-};
-template <int kKeys>
-__device__ __forceinline__ TileWork tile_work(const AttnArgs &a, const BatchView &bt, int b) {
-  TileWork w{};
-  if (b >= bt.num_seqs) return w;
-  w.s = seq_of(bt, b);
-  const int n = w.s.n < bt.max_tokens ? w.s.n : bt.max_tokens;
-  if (n > 0 && n > a.few_rows / a.group) {
-    w.rows = n * a.group;
-    w.tiles = (w.rows + kTileRows - 1) / kTileRows;
-    const int first = w.s.len - w.s.n, i0 = (w.tiles - 1) * kTileRows / a.group;
-    const int lo = seen_lo(first + i0, a.window);
-    const int hi = seen_hi(first + n - 1, w.s.len, a.causal);
-    w.keys = hi > lo ? (hi + kKeys - 1) / kKeys - lo / kKeys : 0;
-  }
-  return w;
-}
-__device__ __forceinline__ int pieces_of(const TileWork &w, int chunk) {
-  const int n = (w.keys + chunk - 1) / chunk;
-  return n > 1 ? n : 1;
-}
-// Key tiles of a piece, at least 512 keys, such that all row tiles make about `target`.
-template <int kKeys>
-__device__ __forceinline__ int chunk_of(const AttnArgs &a, const BatchView &bt, int target,
-                                        int lane) {
-  uint64_t sum = 0;
-  for (int b0 = 0; b0 < bt.num_seqs; b0 += 64) {
-    const TileWork w = tile_work<kKeys>(a, bt, b0 + lane);
-    sum += (uint64_t)w.tiles * (uint64_t)w.keys;
-  }
-  sum = wave_sum_u64(sum);
-  uint64_t c = (sum + target - 1) / target;
-  if (c > 1u << 30) c = 1u << 30;
-  constexpr int least = 512 / kKeys;
-  return (int)c > least ? (int)c : least;
-}
-struct TileUnit {
-  int b, tile, piece, pieces, slot;
-  TileWork w;
-};
-// Unit u of a kv head: of each sequence its row tiles from the last, each piece by
-// piece (the last tile sees the most keys: the long ones come first).
-template <int kKeys>
-__device__ __forceinline__ TileUnit find_unit(const AttnArgs &a, const BatchView &bt, int64_t u,
-                                              int chunk, int lane) {
-  int64_t before = 0;
-  int slots = 0;
-  for (int b0 = 0; b0 < bt.num_seqs; b0 += 64) {
-    const TileWork w = tile_work<kKeys>(a, bt, b0 + lane);
-    const int p = pieces_of(w, chunk), n = w.tiles * p;
-    const int64_t end = before + wave_incl_scan(n);
-    const int ns = p > 1 ? n : 0, send = slots + wave_incl_scan(ns);
-    const uint64_t hit = __ballot(end > u);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      auto rd = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
-      TileUnit r;
-      r.b = b0 + l;
-      r.pieces = rd(p);
-      const int all = rd(n), at = (int)(u - (int64_t)lane_read64((uint64_t)end, l) + all);
-      r.tile = all / r.pieces - 1 - at / r.pieces;
-      r.piece = at % r.pieces;
-      r.slot = rd(send) - rd(ns) + at;
-      r.w.s = Seq{rd(w.s.start), rd(w.s.n), rd(w.s.len)};
-      r.w.rows = rd(w.rows);
-      r.w.tiles = rd(w.tiles);
-      r.w.keys = rd(w.keys);
-      return r;
-    }
-    before = (int64_t)lane_read64((uint64_t)end, 63);
-    slots = __builtin_amdgcn_readlane(send, 63);
-  }
-  TileUnit r{};
-  r.b = -1;
-  return r;
-}
-
-struct TilePart {  // of each kv head `slots` of kTileRows rows
-  float *o, *ml;
-  int slots;
-};
-
 // Rows of a tile of bf16 elements in LDS, chunks of 16 bytes exchanged as Tile has them.
 template <int D>
 __device__ __forceinline__ int key_at(int r, int c) {
@@ -157,7 +71,7 @@ __device__ __forceinline__ v8bf value_frag(const char *tile, int r0, int dt, int
 
 template <int D, int kFormat>
 __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_kernel(
-    AttnArgs a, CacheView c, BatchView bt, int target, TilePart part) {
+    AttnArgs a, CacheView c, BatchView bt, int target, Partial part) {
   typedef Cfg<D, kFormat> C;
   constexpr int K = C::kKeys, NB = C::kBlocks;
   __shared__ __attribute__((aligned(1024))) char lds[C::kLds];
@@ -165,7 +79,8 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, col = lane & 31;
   const int h = blockIdx.x % c.kv_heads;
-  const int chunk = chunk_of<K>(a, bt, target, lane);
+  const Schedule<false, K> work(a, bt, target, kLeastMany<D>, 1);
+  const int chunk = work.chunk;
   const int page_size = 1 << c.log2_page;
   const uint32_t lds_at = __builtin_amdgcn_readfirstlane(lds_addr(lds));
   const float scale2 = fabsf(a.scale2);
@@ -185,9 +100,9 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
   }
 
   for (int64_t u = blockIdx.x / c.kv_heads;; u += gridDim.x / c.kv_heads) {
-    const TileUnit un = find_unit<K>(a, bt, u, chunk, lane);
+    const Unit un = work.find(a, bt, u);
     if (un.b < 0) break;
-    const int r0 = un.tile * kTileRows;
+    const int r0 = un.block * kTileRows;
     const int r1 = un.w.rows < r0 + kTileRows ? un.w.rows : r0 + kTileRows;
     const int len = un.w.s.len, first = len - un.w.s.n;
     const int p0 = first + r0 / a.group, p1 = first + (r1 - 1) / a.group;
@@ -523,50 +438,11 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
   }
 }
 
-// Joins the pieces of each row tile whose keys were split.
-template <int D, int kKeys>
-__global__ __launch_bounds__(kThreads) void tiles_join_kernel(AttnArgs a, int kv_heads, BatchView bt,
-                                                              int target, TilePart part) {
-  const int h = blockIdx.x % kv_heads, lane = threadIdx.x & 63;
-  const int chunk = chunk_of<kKeys>(a, bt, target, lane);
-  // (a block takes the row tile whose first piece its unit is, and passes over others)
-  for (int64_t u = blockIdx.x / kv_heads;; u += gridDim.x / kv_heads) {
-    const TileUnit un = find_unit<kKeys>(a, bt, u, chunk, lane);
-    if (un.b < 0) break;
-    if (un.pieces < 2 || un.piece > 0) continue;
-    const int r0 = un.tile * kTileRows;
-    const int rows = un.w.rows - r0 < kTileRows ? un.w.rows - r0 : kTileRows;
-    const int64_t at0 = ((int64_t)h * part.slots + un.slot) * kTileRows;
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), d = i % (D / 4) * 4, row = r0 + r;
-      float m = kNoMax, l = 0.0f;
-      for (int p = 0; p < un.pieces; ++p) m = fmaxf(m, part.ml[2 * (at0 + p * kTileRows + r)]);
-      v4f v = {0, 0, 0, 0};
-      for (int p = 0; p < un.pieces; ++p) {
-        const int64_t at = at0 + p * kTileRows + r;
-        const float f = __builtin_amdgcn_exp2f(part.ml[2 * at] - m);
-        l += part.ml[2 * at + 1] * f;
-        v += *reinterpret_cast<const v4f *>(part.o + at * D + d) * f;
-      }
-      v *= l != 0.0f ? 1.0f / l : 0.0f;
-      uint16_t *dst = a.out + (int64_t)(un.w.s.start + row / a.group) * a.ld_out +
-                      (h * a.group + row % a.group) * D + d;
-      *reinterpret_cast<v2i_e2 *>(dst) = v2i{(int)bf16x2(v[0], v[1]), (int)bf16x2(v[2], v[3])};
-    }
-  }
-}
-
 template <int D, int kFormat>
 hipError_t launch(const AttnArgs &a, const CacheView &c, const BatchView &b, const AttnPlan &p,
                   float *partial, hipStream_t st) {
-  float *const at = reinterpret_cast<float *>((char *)partial + p.tile_at);
-  const TilePart part{at, at + (size_t)p.tile_slots * c.kv_heads * kTileRows * D, p.tile_slots};
-  const dim3 grid(p.tile_grid * c.kv_heads), block(kThreads);
-  const hipError_t e = launch_kernel(tiles_kernel<D, kFormat>, grid, block, st, {}, a, c, b,
-                                     p.tile_target, part);
-  if (e != hipSuccess || p.tile_slots == 0) return e;
-  return launch_kernel(tiles_join_kernel<D, Cfg<D, kFormat>::kKeys>, grid, block, st, {}, a,
-                       c.kv_heads, b, p.tile_target, part);
+  return launch_kernel(tiles_kernel<D, kFormat>, dim3(p.tile_grid * c.kv_heads), dim3(kThreads), st,
+                       {}, a, c, b, p.tile_target, partial_many(p, c.kv_heads, D, partial));
 }
 template <int D>
 hipError_t launch(const AttnArgs &a, const CacheView &c, int format, const BatchView &b,

@@ -1,0 +1,110 @@
+// attention_work.h -- how attention's work is cut into units, on the device (lengths
+// are known only there). Each kernel takes the sequences of its kind: of few rows (one
+// block of rows), or of many (blocks of kTileRows). The keys of a row block are cut
+// into pieces of `chunk` key tiles, a chunk such that all pieces of a kv head are about
+// `target`; a unit is one piece of one row block. Every wavefront finds its units by
+// itself, its lanes reading 64 sequences at a time. Included by the HIP sources only.
+#pragma once
+
+#include "attention_internal.h"
+
+namespace moe {
+
+constexpr int kFewKeys = 32;  // keys of a tile of the kernel of few rows
+template <int D>
+constexpr int kManyKeys = D == 256 ? 32 : 64;  // of the kernel of tiles
+constexpr int kLeastFew = 4;                   // least chunk: 128 keys, a tile a wavefront
+template <int D>
+constexpr int kLeastMany = 512 / kManyKeys<D>;
+
+struct Work {
+  Seq s;
+  int rows, blocks;  // query rows of a kv head, and blocks of them; 0: not of this kind
+  int t0, keys;      // first key tile (few rows), and key tiles of the last row block
+};
+template <bool kFew, int kKeys>
+__device__ __forceinline__ Work work_of(const AttnArgs &a, const BatchView &bt, int b) {
+  Work w{};
+  if (b >= bt.num_seqs) return w;
+  w.s = seq_of(bt, b);
+  const int n = w.s.n < bt.max_tokens ? w.s.n : bt.max_tokens;
+  if (n > 0 && (n <= a.few_rows / a.group) == kFew) {
+    w.rows = n * a.group;
+    w.blocks = kFew ? 1 : (w.rows + kTileRows - 1) / kTileRows;
+    const int first = w.s.len - w.s.n;
+    const int lo = seen_lo(first + (w.blocks - 1) * kTileRows / a.group, a.window);
+    const int hi = seen_hi(first + n - 1, w.s.len, a.causal);
+    w.t0 = lo / kKeys;
+    w.keys = hi > lo ? (hi + kKeys - 1) / kKeys - w.t0 : 0;
+  }
+  return w;
+}
+
+struct Unit {
+  int b;  // the sequence; -1: there are no more units
+  int block, piece, pieces;
+  int slot;  // of the partial result, where there is more than one piece
+  Work w;
+};
+template <bool kFew, int kKeys>
+struct Schedule {
+  Work first;  // this lane's of sequences 0 .. 63
+  int chunk, lane;
+
+  __device__ __forceinline__ Schedule(const AttnArgs &a, const BatchView &bt, int target, int least,
+                                      int step) {
+    lane = threadIdx.x & 63;
+    first = work_of<kFew, kKeys>(a, bt, lane);
+    uint64_t sum = (uint64_t)first.blocks * (uint64_t)first.keys;
+    for (int b0 = 64; b0 < bt.num_seqs; b0 += 64) {
+      const Work w = work_of<kFew, kKeys>(a, bt, b0 + lane);
+      sum += (uint64_t)w.blocks * (uint64_t)w.keys;
+    }
+    uint64_t c = (wave_sum_u64(sum) + target - 1) / target;
+    if (c > 1u << 30) c = 1u << 30;  // (past any sequence's tiles)
+    const int n = (int)((c + step - 1) / step) * step;
+    chunk = n > least ? n : least;
+  }
+  __device__ __forceinline__ int pieces_of(const Work &w) const {
+    const int n = (w.keys + chunk - 1) / chunk;
+    return n > 1 ? n : 1;
+  }
+  // Unit u: of each sequence its row blocks from the last (which sees the most keys: the
+  // long ones come first), each piece by piece. Only row blocks of two pieces or more
+  // have slots; those have more tiles than a chunk, so that their pieces are at most
+  // 2 target of a kv head.
+  __device__ __forceinline__ Unit find(const AttnArgs &a, const BatchView &bt, int64_t u) const {
+    int64_t before = 0;
+    int slots = 0;
+    for (int b0 = 0; b0 < bt.num_seqs; b0 += 64) {
+      const Work w = b0 ? work_of<kFew, kKeys>(a, bt, b0 + lane) : first;
+      const int p = pieces_of(w), n = w.blocks * p, ns = p > 1 ? n : 0;
+      const int upto = wave_incl_scan(n), supto = slots + wave_incl_scan(ns);
+      const uint64_t hit = __ballot(before + upto > u);
+      if (hit) {
+        const int l = __builtin_ctzll(hit);
+        auto rd = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+        Unit r;
+        r.b = b0 + l;
+        r.pieces = rd(p);
+        const int at = (int)(u - before) - (rd(upto) - rd(n));
+        r.block = rd(w.blocks) - 1 - at / r.pieces;
+        r.piece = at % r.pieces;
+        r.slot = rd(supto) - rd(ns) + at;
+        r.w.s = Seq{rd(w.s.start), rd(w.s.n), rd(w.s.len)};
+        r.w.rows = rd(w.rows);
+        r.w.blocks = rd(w.blocks);
+        r.w.t0 = rd(w.t0);
+        r.w.keys = rd(w.keys);
+        return r;
+      }
+      before += __builtin_amdgcn_readlane(upto, 63);
+      slots = __builtin_amdgcn_readlane(supto, 63);
+    }
+    Unit r{};
+    r.b = -1;
+    return r;
+  }
+};
+
+}  // namespace moe
