@@ -3,7 +3,7 @@
 //   out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p,  M = max m_p,
 // taken along as a running maximum so that nothing waits for all the m_p first.
 //
-// One launch for both kernels' partial results. Each unit's number finds its row block
+// One launch for both kernels' partial results. A slot's number finds its row block
 // again; the pieces of a block share its rows. A row's elements are taken by D / 4
 // lanes, and kWays groups of lanes take the pieces in turn: the loads of one are all in
 // flight at once, which is what a row with many pieces waits for.
@@ -76,21 +76,20 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int kv_heads
                                                         AttnPlan p, Partial few, Partial many) {
   __shared__ __attribute__((aligned(16))) char lds[kThreads * 32];
   const int h = blockIdx.x % kv_heads, x = blockIdx.x / kv_heads;
-  if (x < p.row_grid) {
+  if (x < p.row_target) {
     const Schedule<true, kFewKeys> s(a, bt, p.row_target, kLeastFew, kLeastFew);
-    for (int64_t u = x;; u += p.row_grid) {
-      const Unit un = s.find(a, bt, u);
+    for (int u = x;; u += p.row_target) {
+      const Unit un = s.template find<true>(a, bt, u);
       if (un.b < 0) break;
-      if (un.pieces < 2) continue;
       if (p.row_tiles == 1) join_unit<true, D, kFewKeys, 16>(a, bt, un, few, h, lds);
       else join_unit<true, D, kFewKeys, 32>(a, bt, un, few, h, lds);
     }
   } else {
     const Schedule<false, kManyKeys<D>> s(a, bt, p.tile_target, kLeastMany<D>, 1);
-    for (int64_t u = x - p.row_grid;; u += p.tile_grid) {
-      const Unit un = s.find(a, bt, u);
+    for (int u = x - p.row_target;; u += p.tile_target) {
+      const Unit un = s.template find<true>(a, bt, u);
       if (un.b < 0) break;
-      if (un.pieces >= 2) join_unit<false, D, kManyKeys<D>, kTileRows>(a, bt, un, many, h, lds);
+      join_unit<false, D, kManyKeys<D>, kTileRows>(a, bt, un, many, h, lds);
     }
   }
 }
@@ -101,7 +100,7 @@ hipError_t launch_attention_join(const AttnArgs &a, const CacheView &c, int D, c
                                  const AttnPlan &p, float *partial, hipStream_t st) {
   const Partial few = partial_few(p, c.kv_heads, D, partial),
                 many = partial_many(p, c.kv_heads, D, partial);
-  const dim3 grid((p.row_grid + p.tile_grid) * c.kv_heads), block(kThreads);
+  const dim3 grid((p.row_target + p.tile_target) * c.kv_heads), block(kThreads);
   if (D == 64) return launch_kernel(join_kernel<64>, grid, block, st, {}, a, c.kv_heads, b, p, few, many);
   if (D == 128) return launch_kernel(join_kernel<128>, grid, block, st, {}, a, c.kv_heads, b, p, few, many);
   return launch_kernel(join_kernel<256>, grid, block, st, {}, a, c.kv_heads, b, p, few, many);

@@ -343,14 +343,15 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
       for (int x = 0; x < C::kSub; ++x) ng[x] = page_of(t0 + 1, x);
       put(0);
     }
-    for (int t = t0, buf = 0; t < t1; ++t, buf ^= 1) {
-      // tile t is in LDS, and every wavefront is done with the one before
+    int t = t0, buf = 0;
+    bool ok[C::kSub];
+    // tile t is in LDS and every wavefront done with the one before: the next one is set
+    // on its way; whether every row sees all of this one
+    auto open = [&]() __attribute__((always_inline)) {
       if constexpr (C::k8) __syncthreads();
       else wait_barrier<0>();
       if (t + 1 < t1) fetch(buf ^ 1, t + 1, ng);
-      const int key0 = t * K;
-      bool whole = key0 >= all_lo && key0 + K <= all_hi;
-      bool ok[C::kSub];
+      bool whole = t * K >= all_lo && t * K + K <= all_hi;
 #pragma unroll
       for (int x = 0; x < C::kSub; ++x) {
         ok[x] = exists(pg[x]);
@@ -358,15 +359,35 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
         pg[x] = ng[x];
         ng[x] = page_of(t + 2, x);
       }
-      if (whole) step(std::false_type{}, buf, key0, ok);
-      else step(std::true_type{}, buf, key0, ok);
+      return whole;
+    };
+    auto close = [&]() __attribute__((always_inline)) {
       if (t + 1 < t1) put(buf ^ 1);
+      ++t;
+      buf ^= 1;
+    };
+    // (two loops, so that the results keep their registers from one whole tile to the next)
+    if (t < t1) {
+      bool whole = open();
+      for (;;) {
+        while (whole) {
+          step(std::false_type{}, buf, t * K, ok);
+          close();
+          if (t >= t1) break;
+          whole = open();
+        }
+        if (t >= t1) break;
+        step(std::true_type{}, buf, t * K, ok);
+        close();
+        if (t >= t1) break;
+        whole = open();
+      }
     }
 
     // what was taken out, as marks times the keys that a row sees
-    for (int t = t0; some_odd && t < t1; ++t) {
+    for (t = t0; some_odd && t < t1; ++t) {
       const int key0 = t * K;
-      bool ok[C::kSub], whole = key0 >= all_lo && key0 + K <= all_hi;
+      bool whole = key0 >= all_lo && key0 + K <= all_hi;
 #pragma unroll
       for (int x = 0; x < C::kSub; ++x) {
         pg[x] = page_of(t, x);

@@ -73,12 +73,14 @@ struct Schedule {
   // long ones come first), each piece by piece. Only row blocks of two pieces or more
   // have slots; those have more tiles than a chunk, so that their pieces are at most
   // 2 target of a kv head.
+  // kSlots: u is a slot, not a unit.
+  template <bool kSlots = false>
   __device__ __forceinline__ Unit find(const AttnArgs &a, const BatchView &bt, int64_t u) const {
     int64_t before = 0;
     int slots = 0;
     for (int b0 = 0; b0 < bt.num_seqs; b0 += 64) {
       const Work w = b0 ? work_of<kFew, kKeys>(a, bt, b0 + lane) : first;
-      const int p = pieces_of(w), n = w.blocks * p, ns = p > 1 ? n : 0;
+      const int p = pieces_of(w), ns = p > 1 ? w.blocks * p : 0, n = kSlots ? ns : w.blocks * p;
       const int upto = wave_incl_scan(n), supto = slots + wave_incl_scan(ns);
       const uint64_t hit = __ballot(before + upto > u);
       if (hit) {
