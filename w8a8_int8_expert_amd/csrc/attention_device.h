@@ -111,13 +111,18 @@ struct Tile {
   static constexpr int kBytes = kKeys * kRow;
   static constexpr int kLoads = kBytes / 1024;  // wavefront loads of 1 KB
 
-  // chunk position of chunk c of row r (its own inverse: c from the position)
-  static __device__ __forceinline__ int key_chunk(int r, int c) {
-    return c ^ (kChunks == 4 ? (r >> 1) & 3 : r & 7);
-  }
+  // Chunk position of chunk c of row r (its own inverse: c from the position). LDS serves
+  // 256 bytes at once, 16 chunks in different columns of that width: of keys, one chunk of
+  // each of 16 rows; of 16-bit values, two (kWide: four) neighbours of each of 8 (4) rows;
+  // of 8-bit values, one of each of the 16 rows that two lane groups take.
+  static constexpr int kWin = kChunks < 16 ? 16 / kChunks : 1;  // rows of such a width
+  static constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
+  static __device__ __forceinline__ int key_chunk(int r, int c) { return c ^ (r / kWin & kMask); }
+  template <bool kWide = false>
   static __device__ __forceinline__ int value_chunk(int r, int c) {
-    if constexpr (!k8) return c ^ ((r & 3) << 1);
-    return c ^ (kChunks == 4 ? ((r >> 1) & 1) | ((r >> 4) & 1) << 1 : (r & 3) | ((r >> 4) & 1) << 2);
+    if constexpr (k8) return c ^ (((r & 7) / kWin | (r >> 4 & 1) * (8 / kWin)) & kMask);
+    if constexpr (kWide) return c ^ ((r & 3) / kWin << 2);
+    return c ^ ((r & 7) / kWin << 1);
   }
   // Key fragment (A operand of 16 keys x 32 elements): lane l has key t16 + l % 16.
   // Which elements step s holds is the same for the queries: query_at.

@@ -50,6 +50,18 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
   char *const mine = lds + wave * 2 * C::kStage;
   const uint32_t mine_at = __builtin_amdgcn_readfirstlane(lds_addr(mine));
 
+  // Direct loads of 1 KB: which chunks the lanes read depends on the load's rows, the
+  // same 16 rows on (but for 8-bit values).
+  constexpr int kHalf = TL::kLoads / 2, kValueKinds = TL::k8 ? TL::kLoads : kHalf;
+  uint32_t key_lane[kHalf], value_lane[kValueKinds];
+#pragma unroll
+  for (int i = 0; i < TL::kLoads; ++i) {
+    const int in = i * 1024 + lane * 16, r = in / TL::kRow, p = in % TL::kRow / 16;
+    const int row = lane * 16 / TL::kRow * TL::kRow;
+    if (i < kHalf) key_lane[i] = row + TL::key_chunk(r, p) * 16;
+    if (i < kValueKinds) value_lane[i] = row + TL::value_chunk(r, p) * 16;
+  }
+
   for (int u = blockIdx.x / c.kv_heads;; u += gridDim.x / c.kv_heads) {
     const Unit un = work.find(a, bt, u);
     if (un.b < 0) break;
@@ -95,12 +107,10 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int i = 0; i < TL::kLoads; ++i) {
-          const int byte = i * 1024 + lane * 16, r = byte / TL::kRow, p = byte % TL::kRow / 16;
-          const int ch = x ? TL::value_chunk(r, p) : TL::key_chunk(r, p);
-          const int64_t from = (i * 1024 / TL::kRow < 16 ? b0 : b1) + (r & 15) * TL::kRow + ch * 16;
-          dma16((x ? c.v : c.k) + from, at + x * TL::kBytes + i * 1024);
-        }
+        for (int i = 0; i < TL::kLoads; ++i)
+          dma16((x ? c.v : c.k) + (i < kHalf ? b0 + i * 1024 : b1 + (i - kHalf) * 1024),
+                x ? value_lane[i % kValueKinds] : key_lane[i % kHalf],
+                at + x * TL::kBytes + i * 1024);
       if constexpr (TL::k8) {
         const float *sc = lane < 32 ? c.k_scale : c.v_scale;
         const int r = lane & 31;

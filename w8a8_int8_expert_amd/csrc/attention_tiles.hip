@@ -55,7 +55,7 @@ __device__ __forceinline__ int key_at(int r, int c) {
 }
 template <int D>
 __device__ __forceinline__ int value_at(int r, int c) {
-  return r * 2 * D + Tile<D, kBf16Cache>::value_chunk(r, c) * 16;
+  return r * 2 * D + Tile<D, kBf16Cache>::template value_chunk<true>(r, c) * 16;
 }
 // A operand of 32 elements x 16 keys (keys r0 + 8 e + 4 (l / 32) + 0..3, e = 0, 1):
 // lane l has element 32 dt + l % 32.
@@ -87,16 +87,16 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
   const uint32_t flip = a.scale2 < 0.0f ? 0x80008000u : 0u;  // (queries take the sign)
 
   // Direct loads: a wavefront's kEach loads of 1 KB take consecutive rows; which chunk
-  // a lane reads depends on its row and the exchange, the same for loads 8 rows apart.
+  // a lane reads depends on its row and the exchange, the same for loads 16 rows apart.
   constexpr int kEach = C::kTile / 1024 / kWaves, kLoadRows = 1024 / C::kRow;
-  constexpr int kKinds = kLoadRows >= 8 ? 1 : 8 / kLoadRows < kEach ? 8 / kLoadRows : kEach;
+  constexpr int kKinds = kLoadRows >= 16 ? 1 : 16 / kLoadRows < kEach ? 16 / kLoadRows : kEach;
   uint32_t lane_at[2][kKinds];
 #pragma unroll
   for (int i = 0; i < kKinds; ++i) {
     const int r = wave * kEach * kLoadRows + i * kLoadRows + lane * 16 / C::kRow;
     const int ch = lane * 16 % C::kRow / 16, in = lane * 16 / C::kRow * C::kRow;
     lane_at[0][i] = in + Tile<D, kBf16Cache>::key_chunk(r, ch) * 16;
-    lane_at[1][i] = in + Tile<D, kBf16Cache>::value_chunk(r, ch) * 16;
+    lane_at[1][i] = in + Tile<D, kBf16Cache>::template value_chunk<true>(r, ch) * 16;
   }
 
   for (int64_t u = blockIdx.x / c.kv_heads;; u += gridDim.x / c.kv_heads) {
