@@ -45,6 +45,13 @@ struct Cfg {
   static constexpr int kPerUnit = D == 256 || (k8 && D == 128) ? 1 : 2;  // blocks on a compute unit (registers)
 };
 
+// Order for the scheduler: the next N instructions of a kind.
+enum { kVector = 2, kMatrix = 8 };
+template <int kKind, int N>
+__device__ __forceinline__ void sched() {
+  __builtin_amdgcn_sched_group_barrier(kKind, N, 0);
+}
+
 __device__ __forceinline__ v16f mfma32bf(v8bf a, v8bf b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
@@ -236,17 +243,29 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
       const float *const sc = reinterpret_cast<const float *>(vt + C::kTile);
       if constexpr (kMasked) clear_unseen(vt, key0, ok);
 
-      // scores: block n, register i: key 32 n + 8 (i / 4) + 4 half + i % 4
+      // scores: block n, register i: key 32 n + 8 (i / 4) + 4 half + i % 4. The fragments of
+      // four instructions are on their way while the four before are at work: an LDS read
+      // takes as long as three (the compiler alone reads each where it is needed, 587 us
+      // instead of @ for 8192 tokens).
       v16f s[NB];
+      v8bf f[2][4];
+      auto keys = [&](int i, v8bf *to) __attribute__((always_inline)) {
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        s[n] = v16f{};
+        for (int j = 0; j < 4; ++j)
+          to[j] = *reinterpret_cast<const v8bf *>(
+              kt + key_at<D>(32 * ((i + j) / C::kSteps) + col, 2 * ((i + j) % C::kSteps) + half));
+      };
+      keys(0, f[0]);
 #pragma unroll
-        for (int i = 0; i < C::kSteps; ++i) {
-          const v8bf f = *reinterpret_cast<const v8bf *>(
-              kt + key_at<D>(32 * n + col, 2 * i + half));
-          s[n] = mfma32bf(f, q[i], s[n]);
-        }
+      for (int n = 0; n < NB; ++n) s[n] = v16f{};
+#pragma unroll
+      for (int i = 0; i < NB * C::kSteps; i += 4) {
+        if (i + 4 < NB * C::kSteps) keys(i + 4, f[(i / 4 + 1) % 2]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          s[(i + j) / C::kSteps] = mfma32bf(f[i / 4 % 2][j], q[(i + j) % C::kSteps], s[(i + j) / C::kSteps]);
+        __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (C::k8) {
 #pragma unroll
@@ -302,10 +321,9 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
           asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         }
       }
-      // the probabilities of 16 keys after the other, each set on its way through the
-      // second product while the next is taken
-#pragma unroll
-      for (int x = 0; x < 2 * NB; ++x) {
+      // The probabilities of 16 keys after the other: those of the next 16 are taken, and
+      // their values read, while the matrix instructions of the last are at work.
+      auto probabilities = [&](int x) __attribute__((always_inline)) {
         float e[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -326,12 +344,31 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
         }
         // rounded to bf16 for the second product: half a step of 2^-8 each, which the
         // result, itself rounded so, averages over its keys
-        const v8bf p = __builtin_bit_cast(
+        return __builtin_bit_cast(
             v8bf, v4i{(int)bf16x2(e[0], e[1]), (int)bf16x2(e[2], e[3]), (int)bf16x2(e[4], e[5]),
                       (int)bf16x2(e[6], e[7])});
+      };
+      v8bf p[2], v[2][C::kOut];
+      auto values = [&](int x) __attribute__((always_inline)) {
 #pragma unroll
-        for (int d = 0; d < C::kOut; ++d)
-          o[d] = mfma32bf(value_frag<D>(vt, 16 * x, d, lane), p, o[d]);
+        for (int d = 0; d < C::kOut; ++d) v[x % 2][d] = value_frag<D>(vt, 16 * x, d, lane);
+      };
+      values(0);
+      p[0] = probabilities(0);
+#pragma unroll
+      for (int x = 0; x < 2 * NB; ++x) {
+        if (x + 1 < 2 * NB) values(x + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        if (x + 1 < 2 * NB) p[(x + 1) % 2] = probabilities(x + 1);
+#pragma unroll
+        for (int d = 0; d < C::kOut; ++d) o[d] = mfma32bf(v[x % 2][d], p[x % 2], o[d]);
+        if (x + 1 < 2 * NB)
+#pragma unroll
+          for (int d = 0; d < C::kOut; ++d) {
+            sched<kMatrix, 1>();
+            sched<kVector, 28 / C::kOut>();
+          }
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
 
