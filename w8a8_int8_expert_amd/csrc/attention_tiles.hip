@@ -253,7 +253,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           to[j] = *reinterpret_cast<const v8bf *>(
-              kt + key_at<D>(32 * ((i + j) / C::kSteps) + col, 2 * ((i + j) % C::kSteps) + half));
+              kt + key_at<D>(32 * ((i + j) % NB) + col, 2 * ((i + j) / NB) + half));
       };
       keys(0, f[0]);
 #pragma unroll
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          s[(i + j) / C::kSteps] = mfma32bf(f[i / 4 % 2][j], q[(i + j) % C::kSteps], s[(i + j) / C::kSteps]);
+          s[(i + j) % NB] = mfma32bf(f[i / 4 % 2][j], q[(i + j) / NB], s[(i + j) % NB]);
         __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (C::k8) {
