@@ -570,7 +570,7 @@ int moe_w8a8_add_norm(const moe_w8a8_add_norm_args *args, int64_t T, void *strea
  *   v_scale      scale_stride values apart (a multiple of 4): an element stands for
  *                code * scale. NULL for a bf16 cache.
  * Supported: head_dim 64, 128, 256; page_size 16, 32, 64, 128, 256; kv_heads up to
- * 1024; num_pages from 1; strides up to 2^40. */
+ * 1024; num_pages from 1; strides up to 2^34. */
 #define MOE_W8A8_CACHE_BF16 2
 typedef struct {
   int32_t num_pages, page_size, kv_heads, head_dim;

@@ -10,7 +10,7 @@ using namespace moe;
 
 namespace {
 
-constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxStride = (int64_t)1 << 34;  // (16ths of a page's bytes: 32 bits)
 constexpr int kMaxSeqs = 1 << 20;
 constexpr int kMaxTop = 64;
 constexpr int kMaxVocab = 1 << 20;

@@ -89,6 +89,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
   const Schedule<false, K> work(a, bt, target, kLeastMany<D>, 1);
   const int chunk = work.chunk;
   const int page_size = 1 << c.log2_page;
+  const uint32_t page16 = (uint32_t)(c.page_bytes >> 4);
   const uint32_t lds_at = __builtin_amdgcn_readfirstlane(lds_addr(lds));
   const float scale2 = fabsf(a.scale2);
   const uint32_t flip = a.scale2 < 0.0f ? 0x80008000u : 0u;  // (queries take the sign)
@@ -138,62 +139,52 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
       }
     }
 
-    // page of run x of 16 keys of tile t (-1: no key of it is seen)
-    auto page_of = [&](int t, int x) {
-      const int key = t * K + 16 * x;
-      return key < any_hi && t < t1
-                 ? scalar_word(bt.table, (int64_t)un.b * bt.ld_table + (key >> c.log2_page))
-                 : -1;
-    };
+    // Pages. A wavefront brings kMine consecutive rows of each tile, which lie in one page.
+    // Whether pages are missing at all is found out once, lanes reading 64 at a time.
+    constexpr int kMine = K / kWaves;
+    const int32_t *const table = bt.table + (int64_t)un.b * bt.ld_table;
     auto exists = [&](int p) { return (uint32_t)p < (uint32_t)c.num_pages; };
-    // places of run x of tile t in its page (a page that does not exist: page 0, masked)
-    auto place = [&](int t, int x) {
-      return ((int64_t)h << c.log2_page) + ((t * K + 16 * x) & (page_size - 1));
+    bool holes = false;
+    if (t0 < t1) {
+      const int last = ((t1 * K < any_hi ? t1 * K : any_hi) - 1) >> c.log2_page;
+      for (int i = t0 * K >> c.log2_page; i <= last; i += 64)
+        holes = holes || __any(!exists(table[i + lane < last ? i + lane : last]));
+    }
+    // of run x of 16 keys of tile t (where there are holes)
+    auto run_exists = [&](int t, int x) {
+      const int key = t * K + 16 * x;
+      return key < any_hi && exists(scalar_word(table, key >> c.log2_page));
     };
-
-    typedef int Pages __attribute__((ext_vector_type(C::kSub)));
-    Pages pg, ng;
-    // a tile on its way: direct loads (bf16), or codes in registers, converted when
-    // they are put into LDS
-    constexpr int kPer = C::k8 ? K * D / 16 / kThreads : 1;
+    // this wavefront's page of tile t (past the last key: of that)
+    auto my_page = [&](int t) {
+      const int key = t * K + wave * kMine;
+      return scalar_word(table, (key < any_hi ? key : any_hi - 1) >> c.log2_page);
+    };
+    // a tile on its way: direct loads (bf16), or codes in registers, converted when they are
+    // put into LDS. A page that does not exist is read as page 0, and masked.
+    constexpr int kPer = C::k8 ? kMine * D / 16 / 64 : 1;
     v4i codes[2][kPer];
     float scl = 0.0f;
-    auto fetch = [&](int buf, int t, Pages pages) __attribute__((always_inline)) {
+    int page = t0 < t1 ? my_page(t0) : 0;  // of the next tile to be fetched
+    auto fetch = [&](int buf, int t) __attribute__((always_inline)) {
+      const uint32_t p = exists(page) ? page : 0;
+      page = my_page(t + 1);
+      const uint32_t row = ((uint32_t)h << c.log2_page) + ((t * K + wave * kMine) & (page_size - 1));
       if constexpr (!C::k8) {
-        const int x = wave * (K / kWaves) / 16;
-        int p = pages[0];
-#pragma unroll
-        for (int i = 1; i < C::kSub; ++i) p = x == i ? pages[i] : p;
-        const int64_t from = (exists(p) ? p : 0) * c.page_bytes +
-                             (place(t, x) + wave * (K / kWaves) % 16) * C::kRow;
-#pragma unroll
-        for (int v = 0; v < 2; ++v)
-#pragma unroll
-          for (int i = 0; i < kEach; ++i)
-            // a load's rows: of the four kinds of exchange that its number decides
-            dma16((v ? c.v : c.k) + from + i * 1024, lane_at[v][i % kKinds],
-                  lds_at + buf * C::kStage + v * C::kTile + (wave * kEach + i) * 1024);
+        const uint64_t from = ((uint64_t)p * page16 << 4) + (uint64_t)row * C::kRow;
+        const uint32_t to = lds_at + buf * C::kStage + wave * kEach * 1024;
+        dma16_run<kEach, kKinds>(c.k + from, lane_at[0], to);
+        dma16_run<kEach, kKinds>(c.v + from, lane_at[1], to + C::kTile);
       } else {
+        const uint64_t from = ((uint64_t)p * page16 << 4) + (uint64_t)row * D;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          // (a wavefront's rows lie in one run of 16)
-          const int piece = i * kThreads + tid, r = piece / (D / 16);
-          const int x = __builtin_amdgcn_readfirstlane(r >> 4);
-          int p = pages[0];
-#pragma unroll
-          for (int j = 1; j < C::kSub; ++j) p = x == j ? pages[j] : p;
-          const int64_t from = (exists(p) ? p : 0) * c.page_bytes +
-                               (place(t, x) + (r & 15)) * D + piece % (D / 16) * 16;
-          codes[0][i] = *reinterpret_cast<const v4i *>(c.k + from);
-          codes[1][i] = *reinterpret_cast<const v4i *>(c.v + from);
+          codes[0][i] = *reinterpret_cast<const v4i *>(c.k + from + (i * 64 + lane) * 16);
+          codes[1][i] = *reinterpret_cast<const v4i *>(c.v + from + (i * 64 + lane) * 16);
         }
-        // (the scales of 2 K places, by all threads: the same one more than once)
-        const int r = tid % K, x = r >> 4;
-        int p = pages[0];
-#pragma unroll
-        for (int j = 1; j < C::kSub; ++j) p = x == j ? pages[j] : p;
-        scl = (tid & K ? c.v_scale : c.k_scale)[(exists(p) ? p : 0) * c.scale_stride + place(t, x) +
-                                                (r & 15)];
+        // (the scales of kMine keys, then values, by all lanes: the same one more than once)
+        const float *const sc = lane & kMine ? c.v_scale : c.k_scale;
+        scl = sc[(int64_t)p * c.scale_stride + row + lane % kMine];
       }
     };
     auto put = [&](int buf) {
@@ -201,7 +192,8 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
         char *const st = lds + buf * C::kStage;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const int piece = i * kThreads + tid, r = piece / (D / 16), ch = piece % (D / 16) * 2;
+          const int piece = wave * kPer * 64 + i * 64 + lane;
+          const int r = piece / (D / 16), ch = piece % (D / 16) * 2;
 #pragma unroll
           for (int v = 0; v < 2; ++v)
 #pragma unroll
@@ -211,7 +203,8 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
                                                                : key_at<D>(r, ch + e))) = x;
             }
         }
-        reinterpret_cast<float *>(st + 2 * C::kTile)[tid % (2 * K)] = scl;
+        reinterpret_cast<float *>(st + 2 * C::kTile)[(lane & kMine ? K : 0) + wave * kMine +
+                                                      lane % kMine] = scl;
       }
     };
 
@@ -373,28 +366,26 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
     };
 
     if (t0 < t1) {
-#pragma unroll
-      for (int x = 0; x < C::kSub; ++x) pg[x] = page_of(t0, x);
-      fetch(0, t0, pg);
-#pragma unroll
-      for (int x = 0; x < C::kSub; ++x) ng[x] = page_of(t0 + 1, x);
+      fetch(0, t0);
       put(0);
     }
     int t = t0, buf = 0;
-    bool ok[C::kSub];
+    bool ok[C::kSub];  // (without holes all true: places past the last key are masked anyway)
+#pragma unroll
+    for (int x = 0; x < C::kSub; ++x) ok[x] = true;
     // tile t is in LDS and every wavefront done with the one before: the next one is set
     // on its way; whether every row sees all of this one
     auto open = [&]() __attribute__((always_inline)) {
       if constexpr (C::k8) __syncthreads();
       else wait_barrier<0>();
-      if (t + 1 < t1) fetch(buf ^ 1, t + 1, ng);
+      if (t + 1 < t1) fetch(buf ^ 1, t + 1);
       bool whole = t * K >= all_lo && t * K + K <= all_hi;
+      if (holes) {
 #pragma unroll
-      for (int x = 0; x < C::kSub; ++x) {
-        ok[x] = exists(pg[x]);
-        whole = whole && ok[x];
-        pg[x] = ng[x];
-        ng[x] = page_of(t + 2, x);
+        for (int x = 0; x < C::kSub; ++x) {
+          ok[x] = run_exists(t, x);
+          whole = whole && ok[x];
+        }
       }
       return whole;
     };
@@ -427,13 +418,13 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
       bool whole = key0 >= all_lo && key0 + K <= all_hi;
 #pragma unroll
       for (int x = 0; x < C::kSub; ++x) {
-        pg[x] = page_of(t, x);
-        ok[x] = exists(pg[x]);
+        ok[x] = !holes || run_exists(t, x);
         whole = whole && ok[x];
       }
       if (whole) continue;
       __syncthreads();
-      fetch(0, t, pg);
+      page = my_page(t);
+      fetch(0, t);
       put(0);
       if constexpr (C::k8) __syncthreads();
       else wait_barrier<0>();

@@ -31,6 +31,30 @@ __device__ __forceinline__ void dma16(const void *base, uint32_t off, uint32_t l
                : "v"(off), "s"(base), "s"(lds_base)
                : "memory", "m0");
 }
+// Four of them, each 1 KB further on in memory and in LDS (the instruction's offset counts
+// for both); lane offsets of load i are off[i % kKinds].
+template <int kLoads, int kKinds>
+__device__ __forceinline__ void dma16_run(const void *base, const uint32_t *off,
+                                          uint32_t lds_base) {
+  static_assert(kLoads == 1 || kLoads == 2 || kLoads == 4, "offsets of 12 bits");
+  if constexpr (kLoads == 1)
+    dma16(base, off[0], lds_base);
+  else if constexpr (kLoads == 2)
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %2\n\t"
+                 "global_load_lds_dwordx4 %1, %2 offset:1024"
+                 :
+                 : "v"(off[0]), "v"(off[1 % kKinds]), "s"(base), "s"(lds_base)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %5\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %4\n\t"
+                 "global_load_lds_dwordx4 %1, %4 offset:1024\n\t"
+                 "global_load_lds_dwordx4 %2, %4 offset:2048\n\t"
+                 "global_load_lds_dwordx4 %3, %4 offset:3072"
+                 :
+                 : "v"(off[0]), "v"(off[1 % kKinds]), "v"(off[2 % kKinds]), "v"(off[3 % kKinds]),
+                   "s"(base), "s"(lds_base)
+                 : "memory", "m0");
+}
 // 4 bytes per lane into LDS at lds_base + 4*lane.
 __device__ __forceinline__ void dma4(const void *g, uint32_t lds_base) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
