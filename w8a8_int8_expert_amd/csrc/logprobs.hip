@@ -7,9 +7,10 @@
 //
 // The alternatives are found in the same pass. The n-th largest of the first chunk's
 // thread maxima is a bound that at least n elements reach; only elements past it go
-// into a list in LDS (about n log(V / 2048) of a row in random order), which is cut
-// back to its n best, and the bound raised, when it fills up: an order in which every
-// element is a candidate costs time, not room.
+// into a list in LDS (about n V / 2048 of a row in random order), which is cut back to
+// its n best, and the bound raised, when it fills up: an order in which every element is
+// a candidate costs time, not room. The bound is found by halving over wavefront ballots:
+// counting for each maximum those above it took 6500 cycles, this takes @.
 //
 // Bound by memory for many rows. Few rows are cut into parts of at least 4096
 // elements, one to a block, and joined by a second launch.
@@ -31,16 +32,17 @@ __device__ __forceinline__ float logit(const uint16_t *x, int i) { return bf16_t
 
 // Order of the alternatives as one number: the larger logit first (NaN above
 // everything, -0 as 0), of equal ones the lower token. Never 0.
+__device__ __forceinline__ uint32_t order_of(float v) {
+  const uint32_t u = v == v ? __float_as_uint(v + 0.0f) : 0x7fffffffu;
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float order_value(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
 __device__ __forceinline__ uint64_t rank_of(float v, int i) {
-  uint32_t u = v == v ? __float_as_uint(v + 0.0f) : 0x7fffffffu;
-  u = u & 0x80000000u ? ~u : u | 0x80000000u;
-  return (uint64_t)u << 32 | (uint32_t)~i;
+  return (uint64_t)order_of(v) << 32 | (uint32_t)~i;
 }
-__device__ __forceinline__ float rank_value(uint64_t r) {
-  uint32_t u = (uint32_t)(r >> 32);
-  u = u & 0x80000000u ? u & 0x7fffffffu : ~u;
-  return __uint_as_float(u);
-}
+__device__ __forceinline__ float rank_value(uint64_t r) { return order_value((uint32_t)(r >> 32)); }
 __device__ __forceinline__ int rank_token(uint64_t r) { return (int)~(uint32_t)r; }
 
 // Largest value so far and the two sums relative to it. A row with a NaN has s = NaN
@@ -98,7 +100,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, Parts
   __shared__ uint64_t wave_best[kWaves];
   __shared__ Sums red[kWaves];
   __shared__ int count;
-  __shared__ uint64_t bound;
+  __shared__ uint32_t maxima[kTop ? kThreads : 1];
   const int64_t t = blockIdx.x / parts.parts;
   const int part = blockIdx.x % parts.parts;
   const T *x = reinterpret_cast<const T *>(a.x) + t * a.ld;
@@ -107,8 +109,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, Parts
   const int top = a.top;
   Sums p{kLowest, 0.0f, 0.0f};
   bool nan = false;
-  float bar = 0.0f;       // of elements behind the first chunk: candidates lie above
-  uint64_t bar_rank = 0;  // of those in it: candidates reach it
+  uint32_t bar = 0;  // order of the bound that candidates reach
   if (kTop && tid == 0) count = 0;
 
   // The `n` best of the list, in order, in `best`; the list is spent (every thread).
@@ -158,38 +159,47 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, Parts
       p.e = __builtin_fmaf(d, f, p.e);
     }
     if constexpr (kTop) {
-      const bool first = c == c0;
-      if (first) {
-        // the bound: the top-th largest of the threads' maxima (0 if fewer have any)
-        int j = 0;
+      if (c == c0) {
+        // the bound, bit by bit: the largest number that `top` of the threads' maxima
+        // reach (0 if fewer have any), or the first one met that just so many do
+        maxima[tid] = at < c1 ? order_of(big) : 0;
+        __syncthreads();
+        uint32_t o[kWaves], bound = 0;
 #pragma unroll
-        for (int i = 7; i >= 0; --i) j = v[i] == big ? i : j;
-        const uint64_t mine = at < c1 ? rank_of(big, at + j) : 0;
-        list[tid] = mine;
-        if (tid == 0) bound = 0;
-        __syncthreads();
-        int above = 0;
-        for (int i = 0; i < kThreads; i += 2) {
-          typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
-          const u64x2 o = *reinterpret_cast<const u64x2 *>(&list[i]);
-          above += (o[0] > mine) + (o[1] > mine);
+        for (int w = 0; w < kWaves; ++w) o[w] = maxima[w * 64 + lane];
+        for (int bit = 31; bit >= 0; --bit) {
+          const uint32_t next = bound | 1u << bit;
+          int n = 0;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) n += __popcll(__ballot(o[w] >= next));
+          if (n >= top) bound = next;
+          if (n == top) break;
         }
-        if (mine != 0 && above == top - 1) bound = mine;
-        __syncthreads();
-        bar_rank = bound;
+        bar = bound;
       }
-      bool added = false;
-      if (first ? at < c1 : big > bar) {
+      // candidates reach the bound; each takes its place behind those of lower lanes
+      const bool added = __any(at < c1 && order_of(big) >= bar);
+      if (added) {
+        uint64_t past[8];
+        int n = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const uint64_t r = rank_of(v[j], at + j);
-          if (at + j < c1 && (first ? r >= bar_rank : v[j] > bar)) {
-            list[atomicAdd(&count, 1)] = r;
-            added = true;
-          }
+          past[j] = __ballot(at + j < c1 && order_of(v[j]) >= bar);
+          n += __popcll(past[j]);
+        }
+        int to = 0;
+        if (lane == 0) to = atomicAdd(&count, n);
+        to = __builtin_amdgcn_readfirstlane(to);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (past[j] >> lane & 1)
+            list[to + __builtin_amdgcn_mbcnt_hi((uint32_t)(past[j] >> 32),
+                                                __builtin_amdgcn_mbcnt_lo((uint32_t)past[j], 0))] =
+                rank_of(v[j], at + j);
+          to += __popcll(past[j]);
         }
       }
-      if (first) bar = bar_rank ? rank_value(bar_rank) : -INFINITY;
+      if (c == c0 && bar != 0) ++bar;  // of equal ones those of lower tokens come first
       if (__syncthreads_or(added)) {
         const int have = count;
         __syncthreads();
@@ -197,22 +207,28 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, Parts
           take_best(top, have);
           if (tid < top) list[tid] = best[tid];
           if (tid == 0) count = top;
-          bar = rank_value(best[top - 1]);
+          bar = (uint32_t)(best[top - 1] >> 32) + 1;
           __syncthreads();
         }
       }
     }
   }
 
-  if (__syncthreads_or(nan)) p.s = NAN;
+  // to the block's largest first, then the sums
+  float m = order_value(wave_max_bits(order_of(p.m)));
+  if (lane == 0) red[wave].m = m;
+  nan = __syncthreads_or(nan);
+  m = red[0].m;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1)
-    join(p, Sums{__shfl_xor(p.m, o), __shfl_xor(p.s, o), __shfl_xor(p.e, o)});
-  if (lane == 0) red[wave] = p;
+  for (int w = 1; w < kWaves; ++w) m = fmaxf(m, red[w].m);
+  rescale(p, m);
+  p.s = wave_sum_f32(p.s);
+  p.e = wave_sum_f32(p.e);
+  if (lane == 0) red[wave].s = p.s, red[wave].e = p.e;
   __syncthreads();
-  p = red[0];
+  p = Sums{m, nan ? NAN : 0.0f, 0.0f};
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) join(p, red[w]);
+  for (int w = 0; w < kWaves; ++w) p.s += red[w].s, p.e += red[w].e;
   const bool whole = parts.parts == 1;
   const Result r = result_of(p);
   if (tid == 0) {
@@ -249,6 +265,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, Parts
     for (int i = tid; i < have; i += kThreads) {
       const uint64_t mine = list[i];
       int above = 0;
+#pragma unroll 8
       for (int j = 0; j < have; ++j) above += list[j] > mine;
       if (above < top) put(above, mine);
     }
