@@ -47,12 +47,12 @@ __device__ __forceinline__ void dma16_run(const void *base, const uint32_t *off,
                  : "memory", "m0");
   else
     asm volatile("s_mov_b32 m0, %5\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %4\n\t"
-                 "global_load_lds_dwordx4 %1, %4 offset:1024\n\t"
-                 "global_load_lds_dwordx4 %2, %4 offset:2048\n\t"
-                 "global_load_lds_dwordx4 %3, %4 offset:3072"
+                 "global_load_lds_dwordx4 %1, %4 offset:%6\n\t"
+                 "global_load_lds_dwordx4 %2, %4 offset:2*%6\n\t"
+                 "global_load_lds_dwordx4 %3, %4 offset:3*%6"
                  :
                  : "v"(off[0]), "v"(off[1 % kKinds]), "v"(off[2 % kKinds]), "v"(off[3 % kKinds]),
-                   "s"(base), "s"(lds_base)
+                   "s"(base), "s"(lds_base), "n"(1024)
                  : "memory", "m0");
 }
 // 4 bytes per lane into LDS at lds_base + 4*lane.
