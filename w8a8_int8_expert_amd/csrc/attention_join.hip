@@ -5,8 +5,9 @@
 //
 // One launch for both kernels' partial results. A slot's number finds its row block
 // again; the pieces of a block share its rows. A row's elements are taken by D / 4
-// lanes, and kWays groups of lanes take the pieces in turn: the loads of one are all in
-// flight at once, which is what a row with many pieces waits for.
+// lanes. Few rows have many pieces: all the block's groups of lanes take them in turn, so
+// that their loads are in flight at once. Of many rows each group takes its own, and two
+// blocks share a slot's.
 #include "attention_device.h"
 #include "attention_work.h"
 
@@ -17,9 +18,9 @@ constexpr int kThreads = 256;
 
 template <bool kFew, int D, int kKeys, int kRows>
 __device__ __forceinline__ void join_unit(const AttnArgs &a, const BatchView &bt, const Unit &un,
-                                          const Partial &part, int h, char *lds) {
+                                          const Partial &part, int h, int share, char *lds) {
   constexpr int kLanes = D / 4, kGroups = kThreads / kLanes;
-  constexpr int kWays = kFew ? kGroups : 2, kTake = kGroups / kWays;  // rows at once
+  constexpr int kWays = kFew ? kGroups : 1, kTake = kGroups / kWays;  // rows at once
   struct Got {
     v4f o;
     float m, l;
@@ -31,8 +32,9 @@ __device__ __forceinline__ void join_unit(const AttnArgs &a, const BatchView &bt
   const int rows = un.w.rows - r0 < kRows ? un.w.rows - r0 : kRows;
   const int64_t at0 = ((int64_t)h * part.slots + un.slot - un.piece) * kRows;
   // this piece's share of the rows
-  const int each = (rows + un.pieces - 1) / un.pieces;
-  const int from = un.piece * each, to = from + each < rows ? from + each : rows;
+  constexpr int kShares = kFew ? 1 : 2;
+  const int each = (rows + kShares * un.pieces - 1) / (kShares * un.pieces);
+  const int from = (kShares * un.piece + share) * each, to = from + each < rows ? from + each : rows;
   for (int r = from; r < to; r += kTake) {
     const bool there = r + sub < to;
     const int row = there ? r + sub : to - 1;
@@ -49,9 +51,11 @@ __device__ __forceinline__ void join_unit(const AttnArgs &a, const BatchView &bt
       l = l * f + pl * g;
       v = v * f + o * g;
     }
-    __syncthreads();
-    got[tid] = Got{v, m, l};
-    __syncthreads();
+    if (kWays > 1) {
+      __syncthreads();
+      got[tid] = Got{v, m, l};
+      __syncthreads();
+    }
     if (way == 0 && there) {
 #pragma unroll
       for (int w = 1; w < kWays; ++w) {
@@ -81,15 +85,16 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int kv_heads
     for (int u = x;; u += p.row_target) {
       const Unit un = s.template find<true>(a, bt, u);
       if (un.b < 0) break;
-      if (p.row_tiles == 1) join_unit<true, D, kFewKeys, 16>(a, bt, un, few, h, lds);
-      else join_unit<true, D, kFewKeys, 32>(a, bt, un, few, h, lds);
+      if (p.row_tiles == 1) join_unit<true, D, kFewKeys, 16>(a, bt, un, few, h, 0, lds);
+      else join_unit<true, D, kFewKeys, 32>(a, bt, un, few, h, 0, lds);
     }
   } else {
     const Schedule<false, kManyKeys<D>> s(a, bt, p.tile_target, kLeastMany<D>, 1);
-    for (int u = x - p.row_target;; u += p.tile_target) {
+    const int y = x - p.row_target;
+    for (int u = y >> 1;; u += p.tile_target) {
       const Unit un = s.template find<true>(a, bt, u);
       if (un.b < 0) break;
-      join_unit<false, D, kManyKeys<D>, kTileRows>(a, bt, un, many, h, lds);
+      join_unit<false, D, kManyKeys<D>, kTileRows>(a, bt, un, many, h, y & 1, lds);
     }
   }
 }
@@ -100,7 +105,7 @@ hipError_t launch_attention_join(const AttnArgs &a, const CacheView &c, int D, c
                                  const AttnPlan &p, float *partial, hipStream_t st) {
   const Partial few = partial_few(p, c.kv_heads, D, partial),
                 many = partial_many(p, c.kv_heads, D, partial);
-  const dim3 grid((p.row_target + p.tile_target) * c.kv_heads), block(kThreads);
+  const dim3 grid((p.row_target + 2 * p.tile_target) * c.kv_heads), block(kThreads);
   if (D == 64) return launch_kernel(join_kernel<64>, grid, block, st, {}, a, c.kv_heads, b, p, few, many);
   if (D == 128) return launch_kernel(join_kernel<128>, grid, block, st, {}, a, c.kv_heads, b, p, few, many);
   return launch_kernel(join_kernel<256>, grid, block, st, {}, a, c.kv_heads, b, p, few, many);
