@@ -568,3 +568,178 @@ def test_logprobs_strides_parts_and_graph(m):
         torch.cuda.synchronize()
         for u, v in zip(r, e):
             assert torch.equal(u, v)
+
+
+# --------------------------------------------------------------- together
+class Decoder:
+    """Two decoder layers and an LM head as a user of the W8A8 blocks builds them."""
+    H, F, V, Hq, Hkv, D, PAGE = 320, 200, 333, 6, 2, 64, 16
+
+    def __init__(self, m, fp8, fmt, pages):
+        self.m, self.fmt = m, "fp8" if fp8 else "int8"
+        H, F, V, D = self.H, self.F, self.V, self.D
+        W = (self.Hq + 2 * self.Hkv) * D
+
+        def linear(k, n, seed):
+            p = m.W8A8Linear(k, n, fp8=fp8)
+            p.quantise(cu(randn(n, k, seed=seed) / math.sqrt(k)))
+            return p
+
+        self.layers = []
+        for i in range(2):
+            ffn = m.W8A8FFN(H, F, fp8=fp8)
+            ffn.quantise(cu(randn(2 * F, H, seed=40 + i) / math.sqrt(H)),
+                         cu(randn(H, F, seed=50 + i) / math.sqrt(F)))
+            self.layers.append(dict(
+                qkv=linear(H, W, 10 + i), proj=linear(self.Hq * D, H, 20 + i), ffn=ffn,
+                cache=m.KVCache(pages, self.PAGE, self.Hkv, D, fmt),
+                norms=[cu(1 + 0.1 * randn(H, seed=30 + 2 * i + j)) for j in range(2)],
+                qw=cu(1 + 0.1 * randn(D, seed=60 + i)), kw=cu(1 + 0.1 * randn(D, seed=70 + i))))
+        self.head, self.last = linear(H, V, 99), cu(1 + 0.1 * randn(H, seed=98))
+        self.freq = cu(1e4 ** (-torch.arange(0, D, 2, dtype=F64) / D))
+
+    def __call__(self, x, batch, tokens):
+        m, seen, y, res = self.m, [], x, None
+        for layer in self.layers:
+            a = m.add_norm(y, res, weight=layer["norms"][0], codes=self.fmt, normed=False)
+            q = m.qk_norm_rope(layer["qkv"](codes=(a.codes, a.scales)), layer["cache"], batch,
+                               self.Hq, norm=True, q_weight=layer["qw"], k_weight=layer["kw"],
+                               inv_freq=self.freq)
+            o = m.paged_attention(q, layer["cache"], batch)
+            seen.append((q, o))
+            b = m.add_norm(layer["proj"](o), a.residual, weight=layer["norms"][1],
+                           codes=self.fmt, normed=False)
+            y, res = layer["ffn"](codes=(b.codes, b.scales)), b.residual
+        c = m.add_norm(y, res, weight=self.last, codes=self.fmt, normed=False, residual_out=False)
+        logits = self.head(codes=(c.codes, c.scales), out_dtype=F32)
+        return seen, logits, m.token_logprobs(logits, tokens, top=5)
+
+
+def check_run(run, step, tokens, result):
+    """Attention and answers of a run against the plain forms of their actual operands."""
+    seen, logits, r = result
+    T = step.cu[-1]
+    for layer, (q, o) in zip(run.layers, seen):
+        c = layer["cache"]
+        host = [None if t is None else t.cpu() for t in (c.k, c.k_scale, c.v, c.v_scale)]
+        want, err = A.attention(q.cpu(), *host, step, run.Hq, run.D ** -0.5)
+        R.check(o[:T], want[:T], err[:T], "attention")
+    lp, dlp, ent, dent, tt, tl, dtl = A.logprobs(logits.cpu(), tokens, 5, run.V / 256 + 128)
+    R.check(r.logprobs[:, None], lp[:, None], dlp[:, None], "logprobs")
+    R.check(r.entropy[:, None], ent[:, None], dent[:, None], "entropy")
+    assert torch.equal(r.top_tokens.cpu(), tt)
+    R.check(r.top_logprobs, tl, dtl, "top logprobs")
+
+
+def same(a, b):
+    seen_a, logits_a, ra = a
+    seen_b, logits_b, rb = b
+    for u, v in zip(seen_a, seen_b):
+        for x, y in zip(u, v):
+            assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+    assert torch.equal(logits_a, logits_b)
+    for x, y in zip(ra, rb):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("fp8,fmt", [(False, "int8"), (True, "fp8"), (False, "bf16")])
+def test_decoder_prefill_then_steps_in_a_graph(m, fp8, fmt):
+    """A ragged prefill, then steps of one token: eager on another stream, and captured once
+    and replayed, with the same results. With INT8 weights, whose sums are exact, keys and
+    values of the first layer, which no attention precedes, are those of one prefill."""
+    lens = [37, 5, 0, 64, 1]
+    steps = 3
+    every = A.Step([(n, n + steps) for n in lens], Decoder.PAGE, seed=4)
+    run = Decoder(m, fp8, fmt, every.num_pages)
+    B, V = len(lens), run.V
+    words = [randn(n + steps, run.H, seed=80 + b).to(BF) for b, n in enumerate(lens)]
+
+    def part(new, length):
+        s = A.Step(list(zip(new, length)), Decoder.PAGE)
+        s.table, s.num_pages = every.table, every.num_pages
+        x = torch.cat([words[b][l - n:l] for b, (n, l) in enumerate(zip(new, length))])
+        return s, x
+
+    s, x = part(lens, lens)
+    tokens = torch.arange(s.T) * 7 % V
+    say("prefill", fp8, fmt)
+    check_run(run, s, tokens, run(cu(x), s.batch(m), cu(tokens)))
+
+    # steps of one token over fixed buffers
+    cuv = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    length = torch.zeros(B, dtype=torch.int32, device="cuda")
+    batch = m.SequenceBatch(cuv, length, every.table.cuda(), 1, every.longest)
+    xs, ts = torch.zeros(B, run.H, dtype=BF, device="cuda"), cu(torch.arange(B) * 11 % V)
+    graph, out = None, None
+    side = torch.cuda.Stream()
+    for i in range(steps):
+        s, x = part([1] * B, [n + i + 1 for n in lens])
+        length.copy_(torch.tensor([n + i + 1 for n in lens], dtype=torch.int32))
+        xs.copy_(x)
+        say("step", i)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            eager = run(xs, batch, ts)
+        torch.cuda.synchronize()
+        check_run(run, s, ts.cpu(), eager)
+        if graph is None:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                out = run(xs, batch, ts)
+        for _ in range(2):
+            graph.replay()
+            torch.cuda.synchronize()
+            same(out, eager)
+
+    # one prefill of everything writes the same keys and values in the first layer
+    c = run.layers[0]["cache"]
+    before = [t.clone() for t in (c.k, c.v)]
+    s, x = part([n + steps for n in lens], [n + steps for n in lens])
+    tokens = torch.arange(s.T) % V
+    say("whole")
+    check_run(run, s, tokens, run(cu(x), s.batch(m), cu(tokens)))
+    if not fp8:  # (sums of FP8 products are rounded, in an order of each kernel of the product)
+        for u, v in zip(before, (c.k, c.v)):
+            assert torch.equal(u.view(torch.uint8), v.view(torch.uint8))
+
+
+def test_rope_follows_the_batch_in_a_graph(m):
+    """A captured call writes where lengths and pages say when it is replayed."""
+    cases = [A.Step([(2, 30), (1, 9)], 16, seed=1, spare=3), A.Step([(1, 3), (2, 40)], 16, seed=2)]
+    pages = max(s.num_pages for s in cases)
+    width = max(s.table.shape[1] for s in cases)
+    D, Hq, Hkv = 128, 4, 2
+    cuv = torch.zeros(3, dtype=torch.int32, device="cuda")
+    length = torch.zeros(2, dtype=torch.int32, device="cuda")
+    table = torch.full((2, width), -1, dtype=torch.int32, device="cuda")
+    batch = m.SequenceBatch(cuv, length, table, 2, 40)
+    x = torch.zeros(3, (Hq + 2 * Hkv) * D, dtype=BF, device="cuda")
+    f = cu(1e4 ** (-torch.arange(0, D, 2, dtype=F64) / D))
+    caches = [m.KVCache(pages, 16, Hkv, D, "int8") for _ in range(2)]
+
+    def load(i):
+        s = cases[i]
+        cuv.copy_(torch.tensor(s.cu, dtype=torch.int32))
+        length.copy_(torch.tensor([n for _, n in s.lens], dtype=torch.int32))
+        table.fill_(-1)
+        table[:, :s.table.shape[1]] = s.table.cuda()
+        x.copy_(randn(3, x.shape[1], seed=5 + i).to(BF))
+
+    load(0)
+    call = lambda c: m.qk_norm_rope(x, c, batch, Hq, norm=True, inv_freq=f)  # noqa: E731
+    call(caches[0])
+    for c in caches:
+        for t in (c.k, c.v, c.k_scale, c.v_scale):
+            t.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q = call(caches[0])
+    for i in (0, 1, 0, 1):
+        load(i)
+        graph.replay()
+        e = call(caches[1])
+        torch.cuda.synchronize()
+        assert torch.equal(q.view(torch.int16), e.view(torch.int16))
+        for n in ("k", "v", "k_scale", "v_scale"):
+            assert torch.equal(getattr(caches[0], n), getattr(caches[1], n)), n
