@@ -590,7 +590,8 @@ typedef struct {
  *   lengths     int32 [num_seqs]: keys of the sequence in the cache, its new tokens
  *               (the last ones) included: new token i of n is at place
  *               length - n + i. A token of negative place has no place in the
- *               cache. Lengths are taken into [0, table_width * page_size].
+ *               cache. Lengths are taken into [0, table_width * page_size], and to
+ *               2^31 - 1024 at most.
  *   page_table  int32 [num_seqs][table_width], pitch ld_table: place p of sequence b
  *               lies in page page_table[b][p / page_size]. A page outside [0,
  *               num_pages) holds nothing: its keys are not seen, and what is

@@ -743,3 +743,54 @@ def test_rope_follows_the_batch_in_a_graph(m):
         assert torch.equal(q.view(torch.int16), e.view(torch.int16))
         for n in ("k", "v", "k_scale", "v_scale"):
             assert torch.equal(getattr(caches[0], n), getattr(caches[1], n)), n
+
+
+# ------------------------------------------------------------------ edges
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+def test_attention_last_places(m, n, fmt):
+    """A sequence as long as places are counted (2^31 - 1024 keys), a window over its end:
+    its last pages alone exist."""
+    D, page, W = 64, 256, 300
+    L = (1 << 31) - 1024
+    width = L // page
+    step = A.Step([(n, n + W)], page, seed=3)
+    step.table = step.table[:, :-(-(n + W) // page)]
+    host, cache = setup(m, step, 1, D, fmt, 8)
+    q = randn(n, 2 * D, seed=4).to(BF)
+    # the same keys at the end of a long sequence: places differ by a multiple of a page
+    short = -(-(n + W) // page) * page
+    ref = A.Step([(n, short)], page, seed=3)
+    ref.table, ref.num_pages = step.table, step.num_pages
+    want, err = A.attention(q, *host, ref, 2, D ** -0.5, True, W)
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    table[0, width - short // page:] = cu(ref.table[0])
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    for length in (width * page, (1 << 31) - 1):  # (past the table: as far as it goes)
+        batch = m.SequenceBatch(i32(0, n), i32(length), table, n, 1 << 20)
+        got = m.paged_attention(cu(q), cache, batch, window=W)
+        torch.cuda.synchronize()
+        R.check(got, want, err, "last places")
+
+
+def test_nothing_to_do(m):
+    """No rows, no sequences, sequences without tokens or without pages."""
+    _, cache = setup(m, A.Step([(1, 20)], 16), 1, 64, "bf16", 3)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    for T, cuv, lens, width in ((0, (0, 0), (7,), 1), (0, (0,), (), 2), (2, (0,), (), 0),
+                                (2, (0, 0, 0), (5, 0), 1), (2, (0, 2), (2,), 0)):
+        batch = m.SequenceBatch(i32(*cuv), i32(*lens),
+                                torch.zeros(len(lens), width, dtype=torch.int32, device="cuda"),
+                                2, 20)
+        before = cache.k.clone()
+        x = randn(T, 4 * 64, seed=1).to(BF).cuda()
+        out = torch.full((T, 128), 5.0, dtype=BF, device="cuda")
+        m.qk_norm_rope(x, cache, batch, 2, norm=True, out=out)
+        there = cuv[-1]
+        assert bool((out[there:] == 5.0).all()) and torch.equal(before, cache.k)
+        out.fill_(5.0)
+        m.paged_attention(x[:, :128], cache, batch, out=out)
+        assert bool((out[there:] == 5.0).all()) and bool((out[:there] == 0).all())
+    r = m.token_logprobs(torch.zeros(0, 77, device="cuda"), torch.zeros(0, dtype=torch.int64).cuda(),
+                         top=3)
+    assert r.logprobs.shape == (0,) and r.top_tokens.shape == (0, 3)

@@ -97,7 +97,8 @@ BatchView view(const moe_w8a8_batch &b, int page_size, int64_t T) {
   v.num_seqs = b.num_seqs; v.T = (int)T;
   // (no sequence has more new tokens than there are rows)
   v.max_tokens = b.max_tokens < T ? b.max_tokens : (int)T;
-  const int64_t most = (int64_t)b.table_width * page_size, top = 0x7fffffff - 256;
+  // (tiles are looked up to 8 tiles and a half of 32 keys past a sequence's end, in 32 bits)
+  const int64_t most = (int64_t)b.table_width * page_size, top = 0x7fffffff - 1023;
   v.most = (int)(most < top ? most : top);
   return v;
 }
