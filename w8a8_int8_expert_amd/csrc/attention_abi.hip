@@ -150,7 +150,7 @@ extern "C" int moe_w8a8_qk_norm_rope(const moe_w8a8_qk_norm_rope_args *a,
   return MOE_W8A8_OK;
 }
 
-AttnPlan moe::attention_plan(const CacheView &c, int D, const BatchView &b, int heads,
+AttnPlan moe::attention_plan(const CacheView &c, int D, int format, const BatchView &b, int heads,
                              int max_length) {
   AttnPlan p{};
   const int group = heads / c.kv_heads;
@@ -167,7 +167,7 @@ AttnPlan moe::attention_plan(const CacheView &c, int D, const BatchView &b, int 
   if (all_few || some_few) {
     p.few_rows = most_few;
     p.row_tiles = at_most(rows, most_few) <= 16 ? 1 : 2;
-    p.row_target = (1024 + c.kv_heads - 1) / c.kv_heads;
+    p.row_target = (256 * rows_per_unit(D, format) + c.kv_heads - 1) / c.kv_heads;
     p.row_slots = 2 * p.row_target;
     // (keys of 128 at least make a unit)
     const int64_t units = (int64_t)b.num_seqs * ((max_length + 127) / 128 + 1);
@@ -201,7 +201,8 @@ int attention_shape(const moe_w8a8_kv_cache *c, const moe_w8a8_batch *b, int32_t
   return MOE_W8A8_OK;
 }
 AttnPlan plan_of(const moe_w8a8_kv_cache &c, const moe_w8a8_batch &b, int32_t heads, int64_t T) {
-  return attention_plan(view(c), c.head_dim, view(b, c.page_size, T), heads, b.max_length);
+  return attention_plan(view(c), c.head_dim, c.format, view(b, c.page_size, T), heads,
+                        b.max_length);
 }
 }  // namespace
 

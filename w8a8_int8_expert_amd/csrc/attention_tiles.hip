@@ -42,7 +42,9 @@ struct Cfg {
   static constexpr int kBlocks = kKeys / 32;  // of 32 keys
   static constexpr int kSteps = D / 16;       // matrix instructions of a score block
   static constexpr int kOut = D / 32;
-  static constexpr int kPerUnit = D == 256 || (k8 && D == 128) ? 1 : 2;  // blocks on a compute unit (registers)
+  // Blocks on a compute unit, which share its registers. 8-bit heads of 128 keep some of their
+  // state in memory for it, and win: 4 sequences of 2048 tokens, INT8, 232 us, one block 322.
+  static constexpr int kPerUnit = D == 256 ? 1 : 2;
 };
 
 // Order for the scheduler: the next N instructions of a kind.
