@@ -240,15 +240,20 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
 
       // scores: block n, register i: key 32 n + 8 (i / 4) + 4 half + i % 4. The fragments of
       // four instructions are on their way while the four before are at work: an LDS read
-      // takes as long as three (the compiler alone reads each where it is needed, 587 us
-      // instead of @ for 8192 tokens).
+      // takes as long as three (left to the compiler, which reads each where it is needed,
+      // 8192 tokens of 32 heads of 128 take 549 us instead of 538).
       v16f s[NB];
       v8bf f[2][4];
+      // (of wide bf16 heads, places in LDS are worked out again for each tile: there are no
+      // registers to keep them in, and one read back from memory waits for the loads in
+      // flight. 8192 tokens, 16 heads of 256: 928 us, 1147 with what the compiler kept there)
+      int at_ = lane;
+      if constexpr (D == 256 && !C::k8) asm volatile("" : "+v"(at_));
       auto keys = [&](int i, v8bf *to) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           to[j] = *reinterpret_cast<const v8bf *>(
-              kt + key_at<D>(32 * ((i + j) % NB) + col, 2 * ((i + j) / NB) + half));
+              kt + key_at<D>(32 * ((i + j) % NB) + (at_ & 31), 2 * ((i + j) / NB) + (at_ >> 5)));
       };
       keys(0, f[0]);
 #pragma unroll
@@ -346,7 +351,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
       v8bf p[2], v[2][C::kOut];
       auto values = [&](int x) __attribute__((always_inline)) {
 #pragma unroll
-        for (int d = 0; d < C::kOut; ++d) v[x % 2][d] = value_frag<D>(vt, 16 * x, d, lane);
+        for (int d = 0; d < C::kOut; ++d) v[x % 2][d] = value_frag<D>(vt, 16 * x, d, at_);
       };
       values(0);
       p[0] = probabilities(0);
