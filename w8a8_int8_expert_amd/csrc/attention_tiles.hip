@@ -43,8 +43,10 @@ struct Cfg {
   static constexpr int kSteps = D / 16;       // matrix instructions of a score block
   static constexpr int kOut = D / 32;
   // Blocks on a compute unit, which share its registers. 8-bit heads of 128 keep some of their
-  // state in memory for it, and win: 4 sequences of 2048 tokens, INT8, 232 us, one block 322.
-  static constexpr int kPerUnit = D == 256 ? 1 : 2;
+  // state in memory for two, and win: 4 sequences of 2048 tokens, INT8, 232 us, one block 322.
+  // A third block of 64-wide heads: 8192 tokens, bf16, 321 us, two 346; INT8 ones lose as much
+  // in short chunks (47 us for 42) as they win in long ones (405 for 435).
+  static constexpr int kPerUnit = D == 256 ? 1 : D == 64 && !k8 ? 3 : 2;
 };
 
 // Order for the scheduler: the next N instructions of a kind.
