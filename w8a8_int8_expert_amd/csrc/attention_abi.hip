@@ -167,7 +167,7 @@ AttnPlan moe::attention_plan(const CacheView &c, int D, int format, const BatchV
   if (all_few || some_few) {
     p.few_rows = most_few;
     p.row_tiles = at_most(rows, most_few) <= 16 ? 1 : 2;
-    p.row_target = (256 * rows_per_unit(D, format) + c.kv_heads - 1) / c.kv_heads;
+    p.row_target = (256 * rows_per_unit(D, format, p.row_tiles) + c.kv_heads - 1) / c.kv_heads;
     p.row_slots = 2 * p.row_target;
     // (keys of 128 at least make a unit)
     const int64_t units = (int64_t)b.num_seqs * ((max_length + 127) / 128 + 1);
