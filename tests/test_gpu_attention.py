@@ -794,3 +794,23 @@ def test_nothing_to_do(m):
     r = m.token_logprobs(torch.zeros(0, 77, device="cuda"), torch.zeros(0, dtype=torch.int64).cuda(),
                          top=3)
     assert r.logprobs.shape == (0,) and r.top_tokens.shape == (0, 3)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 90])
+def test_attention_scores_far_below_zero(m, D, n):
+    """Scores of -10^31 and less, far apart: the largest have all the weight."""
+    L, big = 200, 2.0 ** 52
+    step = A.Step([(n, L)], 16, seed=1)
+    _, cache = setup(m, step, 1, D, "bf16", 3)
+    j = torch.arange(L)
+    for p in range(L):
+        cache.k[int(step.table[0, p // 16]), 0, p % 16] = -big * (3 + 37 * p % 101)
+    # (places 0 and 101 have the same key: half the weight each)
+    at = torch.nonzero(37 * j[:L - n + 1] % 101 == 0).flatten().tolist()
+    assert at == [0, 101]
+    q = torch.full((n, 2 * D), big, dtype=BF, device="cuda")
+    got = m.paged_attention(q, cache, step.batch(m))
+    want = (sum(cache.v[int(step.table[0, p // 16]), 0, p % 16].float() for p in at) / 2).to(BF)
+    assert torch.equal(got[0, :D], want) and torch.equal(got[0, D:], want)
+    assert bool(torch.isfinite(got.float()).all())

@@ -12,7 +12,9 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef v2i v2i_e2 __attribute__((aligned(2)));
 
-constexpr float kNoMax = -1e30f;  // running maximum before the first key: finite
+// Running maximum before the first key: finite, so that no difference of two is NaN, and not
+// above any score.
+constexpr float kNoMax = -3.402823466e38f;
 
 __device__ __forceinline__ v4f mfma16bf(v8bf a, v8bf b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);

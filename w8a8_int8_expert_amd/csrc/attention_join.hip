@@ -7,7 +7,8 @@
 // again; the pieces of a block share its rows. A row's elements are taken by D / 4
 // lanes. Few rows have many pieces: all the block's groups of lanes take them in turn, so
 // that their loads are in flight at once. Of many rows each group takes its own, and two
-// blocks share a slot's.
+// blocks share a slot's: 75 MB in 24 us (37 with pieces shared out as of few rows), a few
+// rows of up to 64 pieces in 4 to 6.
 #include "attention_device.h"
 #include "attention_work.h"
 
