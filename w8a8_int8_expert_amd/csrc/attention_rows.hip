@@ -205,7 +205,7 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
           vs[x] = *reinterpret_cast<const v4f *>(sc + 32 + 16 * x + 4 * g);
         }
       }
-      v8bf p[NQ];
+      v8bf p[NQ], rest[NQ];
       uint32_t seen[NQ];
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
@@ -240,10 +240,25 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
           }
         }
         l[n] = l[n] * f + sum;
-        // rounded to bf16 for the second product: half a step of 2^-8 each, which the
-        // result, itself rounded so, averages over its keys
-        p[n] = __builtin_bit_cast(v8bf, v4i{(int)bf16x2(e[0], e[1]), (int)bf16x2(e[2], e[3]),
-                                            (int)bf16x2(e[4], e[5]), (int)bf16x2(e[6], e[7])});
+        // two bf16 terms for the second product, whose matrix instructions are few here: the
+        // rest of what the first one rounds, 2^-17 of the probability at most left out. (With one
+        // term a key that has all the weight moves its row by up to 2^-9: 32 sequences of 8192,
+        // INT8, 107 us instead of 109, but the result's error half again that of its rounding.)
+        v4i w, r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          w[j] = (int)bf16x2(e[2 * j], e[2 * j + 1]);
+          float lo[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float hi = __uint_as_float(i ? (uint32_t)w[j] & 0xffff0000u : (uint32_t)w[j] << 16);
+            lo[i] = e[2 * j + i] - hi;
+            if constexpr (TL::k8) lo[i] = fabsf(hi) < INFINITY ? lo[i] : 0.0f;  // (such a scale)
+          }
+          r[j] = (int)bf16x2(lo[0], lo[1]);
+        }
+        p[n] = __builtin_bit_cast(v8bf, w);
+        rest[n] = __builtin_bit_cast(v8bf, r);
 #pragma unroll
         for (int d = 0; d < kOut; ++d) o[n][d] *= f;
       }
@@ -261,7 +276,7 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
         for (int d = 0; d < kOut; ++d) {
           const v8bf f = TL::value(vt, 0, d, lane);
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) o[n][d] = mfma16bf(f, p[n], o[n][d]);
+          for (int n = 0; n < NQ; ++n) o[n][d] = mfma16bf(f, rest[n], mfma16bf(f, p[n], o[n][d]));
         }
       } else {
 #pragma unroll
@@ -276,6 +291,7 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
             const v8bf f = TL::value(vt, 0, d, lane);
             const v4f marks = mfma16bf(odd_part<true>(f), sees, v4f{0, 0, 0, 0});
             o[n][d] = mfma16bf(odd_part<false>(f), p[n], o[n][d]);
+            o[n][d] = mfma16bf(odd_part<false>(f), rest[n], o[n][d]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[n][d][i] = add_odd(o[n][d][i], marks[i]);
             __builtin_amdgcn_sched_barrier(0);  // (this path need not be fast: few registers)
