@@ -7,7 +7,7 @@
 // lanes but for one exchange over the four lane groups, and the probabilities are
 // where the second product (values transposed by the LDS reads) takes them from.
 // Bound by the cache's bytes (8 sequences of 65536 keys, 8 kv heads of 128, FP8: 1.1 GB in
-// 195 us, 5.7 TB/s; 32 ragged ones of 1 to 8192, INT8: 174 MB in 46, of which about 6 are its
+// 195 us, 5.7 TB/s; 32 ragged ones of 1 to 8192, INT8: 174 MB in 48, of which about 6 are its
 // beginning and end). Every wavefront brings its own tiles of 32 keys into
 // LDS by direct loads, the next in flight while one is worked on, and no two of them
 // meet until the end.
