@@ -1,0 +1,89 @@
+"""Calls of qk_norm_rope and paged_attention at the edges of what their documentation
+allows, on the GPU against the plain 64-bit forms of tests/attention_ref.py."""
+import math
+
+import pytest
+import torch
+
+import attention_ref as A
+import block_ref as R
+
+pytestmark = pytest.mark.gpu
+BF, F32, F64 = A.BF, A.F32, A.F64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def m():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import w8a8_int8_expert_amd as mod
+    mod.load_library()
+    return mod
+
+
+def cu(t):
+    return None if t is None else t.cuda()
+
+
+def i32(*v):
+    return torch.tensor(v, dtype=torch.int32).cuda()
+
+
+def randn(*shape, seed=0):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed))
+
+
+def contents(step, Hkv, D, fmt, seed):
+    """Cache contents on the host: k, scales, v, scales."""
+    shape = (step.num_pages, Hkv, step.page, D)
+    return A.cached(shape, fmt, seed) + A.cached(shape, fmt, seed + 1)
+
+
+def cache_of(m, host):
+    return m.KVCache.of(cu(host[0]), cu(host[2]), cu(host[1]), cu(host[3]))
+
+
+def check(got, want, err, what):
+    """As R.check, and infinities have to be where they are wanted, with their sign."""
+    R.check(got, want, err, what)
+    far = torch.isinf(want)
+    assert torch.equal(got.double().cpu()[far], want[far]), what + ": infinities"
+
+
+def place(step, b, p):
+    """Page and row of place p of sequence b."""
+    return int(step.table[b, p // step.page]), p % step.page
+
+
+# ------------------------------------------------------ values that are not finite
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,n", [(2, 1), (4, 1), (6, 4), (2, 90)])
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "fp8"])
+def test_infinite_values_that_every_row_sees(m, D, G, n, fmt):
+    """Infinities and NaN among the values of keys far from a sequence's end, which all
+    rows see (of codes: infinite scales, NaN codes): each reaches its own column, with its
+    sign, of few rows and of many."""
+    L = 340
+    step = A.Step([(n, L), (1, 70)], 16, seed=3)
+    host = contents(step, 1, D, fmt, 8)
+    k, ks, v, vs = host
+    # (keys alike: probabilities within a factor of 2^4 or so of each other)
+    for p, col, x in ((5, 3, math.inf), (40, 7, -math.inf), (70, 9, math.nan), (100, 11, math.inf),
+                      (131, 11, math.inf), (132, 13, math.inf), (133, 13, -math.inf), (200, 3, math.inf)):
+        page, row = place(step, 0, p)
+        if fmt == "bf16":
+            v[page, 0, row, col] = x
+        elif fmt == "fp8" and math.isnan(x):
+            v.view(torch.uint8)[page, 0, row, col] = 0x7f
+    if fmt != "bf16":
+        page, row = place(step, 0, 260)
+        vs[page, 0, row] = math.inf
+        raw = v.view(torch.uint8)[page, 0, row]
+        raw[torch.arange(D) % 4 == 1] = 0
+    q = randn(step.T, G * D, seed=4).to(BF)
+    want, err = A.attention(q, *host, step, G, D ** -0.5)
+    if fmt != "int8":
+        assert bool(torch.isnan(want[:n]).any())
+    assert bool((want == math.inf).any()) and bool((want == -math.inf).any())
+    got = m.paged_attention(cu(q), cache_of(m, host), step.batch(m))
+    check(got, want, err, "attention")

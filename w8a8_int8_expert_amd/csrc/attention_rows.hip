@@ -123,181 +123,203 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
 
     v4f o[NQ][kOut];
     float m[NQ], l[NQ];
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      m[n] = kNoMax;
-      l[n] = 0.0f;
-#pragma unroll
-      for (int d = 0; d < kOut; ++d) o[n][d] = v4f{0, 0, 0, 0};
-    }
-
-    int t = t0 + wave, stage = 0;
-    int pg0 = -1, pg1 = -1, ng0 = -1, ng1 = -1;
-    if (t < t1) {
-      pg0 = page_of(t * kKeys);
-      pg1 = page_of(t * kKeys + 16);
-      issue(0, t, pg0, pg1);
-      ng0 = page_of((t + W) * kKeys);
-      ng1 = page_of((t + W) * kKeys + 16);
-    }
-    for (; t < t1; t += W, stage ^= 1) {
-      // the stage of the tile before this one has been read to its end
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (t + W < t1) {
-        issue(stage ^ 1, t + W, ng0, ng1);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::kLoads) : "memory");
-      } else {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    int t, stage, pg0, pg1, ng0, ng1;
+    auto begin = [&]() __attribute__((always_inline)) {
+      t = t0 + wave;
+      stage = 0;
+      pg0 = pg1 = ng0 = ng1 = -1;
+      if (t < t1) {
+        pg0 = page_of(t * kKeys);
+        pg1 = page_of(t * kKeys + 16);
+        issue(0, t, pg0, pg1);
+        ng0 = page_of((t + W) * kKeys);
+        ng1 = page_of((t + W) * kKeys + 16);
       }
-      char *const kt = mine + stage * C::kStage, *const vt = kt + TL::kBytes;
-      const float *const sc = reinterpret_cast<const float *>(vt + TL::kBytes);
-      const int key0 = t * kKeys;
-      const bool ok0 = (uint32_t)pg0 < (uint32_t)c.num_pages,
-                 ok1 = (uint32_t)pg1 < (uint32_t)c.num_pages;
-      const bool masked = !(key0 >= all_lo && key0 + kKeys <= all_hi && ok0 && ok1);
-      pg0 = ng0;
-      pg1 = ng1;
-      ng0 = page_of((t + 2 * W) * kKeys);
-      ng1 = page_of((t + 2 * W) * kKeys + 16);
-      if (masked) {
-        // values that no row sees count as zeros, whatever lies there
-        for (int y = 0; y < TL::kBytes / 1024; ++y) {
-          const int i = y * 64 + lane, r = i / TL::kChunks, key = key0 + r;
-          const bool gone = (key < any_lo) | (key >= any_hi) | !(r < 16 ? ok0 : ok1);
-          v4i v = reinterpret_cast<const v4i *>(vt)[i];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = gone ? 0 : v[j];
-          reinterpret_cast<v4i *>(vt)[i] = v;
-        }
-      }
-
-      // scores: keys 16 x + 4 g + i of column col
-      v4f s[NQ][2];
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = v4f{0, 0, 0, 0};
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if constexpr (TL::k8) {
-#pragma unroll
-          for (int s2 = 0; s2 < kSteps / 2; ++s2) {
-            v8bf f[2];
-            TL::key2(kt, 16 * x, s2, lane, f);
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-              s[n][x] = mfma16bf(f[0], q[n][2 * s2], s[n][x]);
-              s[n][x] = mfma16bf(f[1], q[n][2 * s2 + 1], s[n][x]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < kSteps; ++i) {
-            const v8bf f = TL::key(kt, 16 * x, i, lane);
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) s[n][x] = mfma16bf(f, q[n][i], s[n][x]);
-          }
-        }
-      }
-      v4f ks[2], vs[2];
-      if constexpr (TL::k8) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          ks[x] = *reinterpret_cast<const v4f *>(sc + 16 * x + 4 * g);
-          vs[x] = *reinterpret_cast<const v4f *>(sc + 32 + 16 * x + 4 * g);
-        }
-      }
-      v8bf p[NQ], rest[NQ];
-      uint32_t seen[NQ];
+    };
+    begin();
+    // Tiles that all rows see are not searched for values that are not finite: one of those
+    // shows in a result, and the wavefront takes its tiles again, searching all. (Of codes
+    // only the scales can be infinite, whose rests are 0.)
+    for (bool careful = false;; careful = true) {
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        float mx = kNoMax;
-        seen[n] = 0xffu;
+        m[n] = kNoMax;
+        l[n] = 0.0f;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int d = 0; d < kOut; ++d) o[n][d] = v4f{0, 0, 0, 0};
+      }
+      for (; t < t1; t += W, stage ^= 1) {
+        // the stage of the tile before this one has been read to its end
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (t + W < t1) {
+          issue(stage ^ 1, t + W, ng0, ng1);
+          asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::kLoads) : "memory");
+        } else {
+          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        char *const kt = mine + stage * C::kStage, *const vt = kt + TL::kBytes;
+        const float *const sc = reinterpret_cast<const float *>(vt + TL::kBytes);
+        const int key0 = t * kKeys;
+        const bool ok0 = (uint32_t)pg0 < (uint32_t)c.num_pages,
+                   ok1 = (uint32_t)pg1 < (uint32_t)c.num_pages;
+        const bool masked = !(key0 >= all_lo && key0 + kKeys <= all_hi && ok0 && ok1);
+        pg0 = ng0;
+        pg1 = ng1;
+        ng0 = page_of((t + 2 * W) * kKeys);
+        ng1 = page_of((t + 2 * W) * kKeys + 16);
+        if (masked) {
+          // values that no row sees count as zeros, whatever lies there
+          for (int y = 0; y < TL::kBytes / 1024; ++y) {
+            const int i = y * 64 + lane, r = i / TL::kChunks, key = key0 + r;
+            const bool gone = (key < any_lo) | (key >= any_hi) | !(r < 16 ? ok0 : ok1);
+            v4i v = reinterpret_cast<const v4i *>(vt)[i];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v = s[n][x][i] * a.scale2;
-            if constexpr (TL::k8) v *= ks[x][i];
-            if (masked) {
-              const int key = key0 + 16 * x + 4 * g + i;
-              const bool there = key >= lo[n] && key < hi[n] && (x ? ok1 : ok0);
-              v = there ? v : -INFINITY;
-              seen[n] &= ~((uint32_t)!there << (4 * x + i));
-            }
-            s[n][x][i] = v;
-            mx = fmaxf(mx, v);
+            for (int j = 0; j < 4; ++j) v[j] = gone ? 0 : v[j];
+            reinterpret_cast<v4i *>(vt)[i] = v;
           }
-        mx = fmaxf(m[n], groups_max(mx));
-        const float f = __builtin_amdgcn_exp2f(m[n] - mx);
-        m[n] = mx;
-        float e[8], sum = 0.0f;
+        }
+
+        // scores: keys 16 x + 4 g + i of column col
+        v4f s[NQ][2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          e[j] = __builtin_amdgcn_exp2f(s[n][j / 4][j % 4] - mx);
-          sum += e[j];
+        for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = v4f{0, 0, 0, 0};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
           if constexpr (TL::k8) {
-            e[j] *= vs[j / 4][j % 4];
-            e[j] = masked && !(seen[n] >> j & 1) ? 0.0f : e[j];
+#pragma unroll
+            for (int s2 = 0; s2 < kSteps / 2; ++s2) {
+              v8bf f[2];
+              TL::key2(kt, 16 * x, s2, lane, f);
+#pragma unroll
+              for (int n = 0; n < NQ; ++n) {
+                s[n][x] = mfma16bf(f[0], q[n][2 * s2], s[n][x]);
+                s[n][x] = mfma16bf(f[1], q[n][2 * s2 + 1], s[n][x]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+              const v8bf f = TL::key(kt, 16 * x, i, lane);
+#pragma unroll
+              for (int n = 0; n < NQ; ++n) s[n][x] = mfma16bf(f, q[n][i], s[n][x]);
+            }
           }
         }
-        l[n] = l[n] * f + sum;
-        // two bf16 terms for the second product, whose matrix instructions are few here: the
-        // rest of what the first one rounds, 2^-17 of the probability at most left out. (With one
-        // term a key that has all the weight moves its row by up to 2^-9: 32 sequences of 8192,
-        // INT8, 107 us instead of 109, but the result's error half again that of its rounding.)
-        v4i w, r;
+        v4f ks[2], vs[2];
+        if constexpr (TL::k8) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          w[j] = (int)bf16x2(e[2 * j], e[2 * j + 1]);
-          float lo[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float hi = __uint_as_float(i ? (uint32_t)w[j] & 0xffff0000u : (uint32_t)w[j] << 16);
-            lo[i] = e[2 * j + i] - hi;
-            if constexpr (TL::k8) lo[i] = fabsf(hi) < INFINITY ? lo[i] : 0.0f;  // (such a scale)
+          for (int x = 0; x < 2; ++x) {
+            ks[x] = *reinterpret_cast<const v4f *>(sc + 16 * x + 4 * g);
+            vs[x] = *reinterpret_cast<const v4f *>(sc + 32 + 16 * x + 4 * g);
           }
-          r[j] = (int)bf16x2(lo[0], lo[1]);
         }
-        p[n] = __builtin_bit_cast(v8bf, w);
-        rest[n] = __builtin_bit_cast(v8bf, r);
-#pragma unroll
-        for (int d = 0; d < kOut; ++d) o[n][d] *= f;
-      }
-      // values that are not finite, in a tile of which some rows do not see all: an
-      // unseen one must not reach a row through 0 times infinity. They are taken out,
-      // and put back as indicators times the keys that a row sees.
-      bool odd = false;
-      if (masked) {
-#pragma unroll
-        for (int d = 0; d < kOut; ++d) odd |= any_odd(TL::value(vt, 0, d, lane));
-        odd = __any(odd);
-      }
-      if (!odd) {
-#pragma unroll
-        for (int d = 0; d < kOut; ++d) {
-          const v8bf f = TL::value(vt, 0, d, lane);
-#pragma unroll
-          for (int n = 0; n < NQ; ++n) o[n][d] = mfma16bf(f, rest[n], mfma16bf(f, p[n], o[n][d]));
-        }
-      } else {
+        v8bf p[NQ], rest[NQ];
+        uint32_t seen[NQ];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-          v4i one = {0, 0, 0, 0};
+          float mx = kNoMax;
+          seen[n] = 0xffu;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (seen[n] >> j & 1) one[j / 2] |= 0x3f80 << 16 * (j & 1);
-          const v8bf sees = __builtin_bit_cast(v8bf, one);
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float v = s[n][x][i] * a.scale2;
+              if constexpr (TL::k8) v *= ks[x][i];
+              if (masked) {
+                const int key = key0 + 16 * x + 4 * g + i;
+                const bool there = key >= lo[n] && key < hi[n] && (x ? ok1 : ok0);
+                v = there ? v : -INFINITY;
+                seen[n] &= ~((uint32_t)!there << (4 * x + i));
+              }
+              s[n][x][i] = v;
+              mx = fmaxf(mx, v);
+            }
+          mx = fmaxf(m[n], groups_max(mx));
+          const float f = __builtin_amdgcn_exp2f(m[n] - mx);
+          m[n] = mx;
+          float e[8], sum = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            e[j] = __builtin_amdgcn_exp2f(s[n][j / 4][j % 4] - mx);
+            sum += e[j];
+            if constexpr (TL::k8) {
+              e[j] *= vs[j / 4][j % 4];
+              e[j] = masked && !(seen[n] >> j & 1) ? 0.0f : e[j];
+            }
+          }
+          l[n] = l[n] * f + sum;
+          // two bf16 terms for the second product, whose matrix instructions are few here: the
+          // rest of what the first one rounds, 2^-17 of the probability at most left out. (With one
+          // term a key that has all the weight moves its row by up to 2^-9: 32 sequences of 8192,
+          // INT8, 107 us instead of 109, but the result's error half again that of its rounding.)
+          v4i w, r;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            w[j] = (int)bf16x2(e[2 * j], e[2 * j + 1]);
+            float lo[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t u = (uint32_t)w[j];
+              const float hi = __uint_as_float(i ? u & 0xffff0000u : u << 16);
+              lo[i] = e[2 * j + i] - hi;
+              if constexpr (TL::k8) lo[i] = fabsf(hi) < INFINITY ? lo[i] : 0.0f;  // (such a scale)
+            }
+            r[j] = (int)bf16x2(lo[0], lo[1]);
+          }
+          p[n] = __builtin_bit_cast(v8bf, w);
+          rest[n] = __builtin_bit_cast(v8bf, r);
+#pragma unroll
+          for (int d = 0; d < kOut; ++d) o[n][d] *= f;
+        }
+        // values that are not finite, in a tile of which some rows do not see all: an
+        // unseen one must not reach a row through 0 times infinity, nor one that is seen
+        // through the rest of its probability, which may be 0 or negative. They are taken
+        // out, and put back as indicators times the keys that a row sees.
+        bool odd = false;
+        if (masked || careful) {
+#pragma unroll
+          for (int d = 0; d < kOut; ++d) odd |= any_odd(TL::value(vt, 0, d, lane));
+          odd = __any(odd);
+        }
+        if (!odd) {
 #pragma unroll
           for (int d = 0; d < kOut; ++d) {
             const v8bf f = TL::value(vt, 0, d, lane);
-            const v4f marks = mfma16bf(odd_part<true>(f), sees, v4f{0, 0, 0, 0});
-            o[n][d] = mfma16bf(odd_part<false>(f), p[n], o[n][d]);
-            o[n][d] = mfma16bf(odd_part<false>(f), rest[n], o[n][d]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][d][i] = add_odd(o[n][d][i], marks[i]);
-            __builtin_amdgcn_sched_barrier(0);  // (this path need not be fast: few registers)
+            for (int n = 0; n < NQ; ++n) o[n][d] = mfma16bf(f, rest[n], mfma16bf(f, p[n], o[n][d]));
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            v4i one = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (seen[n] >> j & 1) one[j / 2] |= 0x3f80 << 16 * (j & 1);
+            const v8bf sees = __builtin_bit_cast(v8bf, one);
+#pragma unroll
+            for (int d = 0; d < kOut; ++d) {
+              const v8bf f = TL::value(vt, 0, d, lane);
+              const v4f marks = mfma16bf(odd_part<true>(f), sees, v4f{0, 0, 0, 0});
+              o[n][d] = mfma16bf(odd_part<false>(f), p[n], o[n][d]);
+              o[n][d] = mfma16bf(odd_part<false>(f), rest[n], o[n][d]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[n][d][i] = add_odd(o[n][d][i], marks[i]);
+              __builtin_amdgcn_sched_barrier(0);  // (this path need not be fast: few registers)
+            }
           }
         }
       }
+      if (TL::k8 || careful) break;
+      v4f odd = {0, 0, 0, 0};
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int d = 0; d < kOut; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) odd[i] = __builtin_fmaf(o[n][d][i], 0.0f, odd[i]);
+      if (!__any(odd[0] + odd[1] + (odd[2] + odd[3]) != 0.0f)) break;
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (the stages are free again)
+      begin();
     }
 
     // join the wavefronts: o / l with the weights exp2(m - largest m)
