@@ -87,3 +87,22 @@ def test_infinite_values_that_every_row_sees(m, D, G, n, fmt):
     assert bool((want == math.inf).any()) and bool((want == -math.inf).any())
     got = m.paged_attention(cu(q), cache_of(m, host), step.batch(m))
     check(got, want, err, "attention")
+
+
+# ------------------------------------------------------------------------ windows
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("G,lens", [(1, [(6, 2), (3, 40)]), (2, [(300, 250), (5, 1), (80, 80)])])
+def test_window_past_every_place(m, fmt, causal, G, lens):
+    """The widest window, with tokens of negative place (fewer keys than new tokens): as
+    none at all."""
+    step = A.Step(lens, 16, seed=3)
+    host = contents(step, 1, 64, fmt, 8)
+    cache = cache_of(m, host)
+    q = randn(step.T, G * 64, seed=4).to(BF)
+    want, err = A.attention(q, *host, step, G, 64 ** -0.5, causal, 0)
+    none = m.paged_attention(cu(q), cache, step.batch(m), causal=causal)
+    check(none, want, err, "without a window")
+    for window in ((1 << 31) - 1, (1 << 31) - 2, (1 << 31) - 300, 1 << 30):
+        got = m.paged_attention(cu(q), cache, step.batch(m), causal=causal, window=window)
+        assert torch.equal(got.view(torch.int16), none.view(torch.int16)), window

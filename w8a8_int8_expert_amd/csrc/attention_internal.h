@@ -47,8 +47,8 @@ __device__ __forceinline__ int seen_hi(int place, int len, bool causal) {
   return causal ? (place + 1 < len ? place + 1 : len) : len;
 }
 __device__ __forceinline__ int seen_lo(int place, int window) {
-  const int lo = place - window + 1;
-  return window > 0 && lo > 0 ? lo : 0;
+  // (places may be negative: nothing is taken from one)
+  return window > 0 && place >= window ? place - window + 1 : 0;
 }
 #endif
 
