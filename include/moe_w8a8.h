@@ -646,7 +646,8 @@ int moe_w8a8_qk_norm_rope(const moe_w8a8_qk_norm_rope_args *args, const moe_w8a8
  * c <= p (causal) and c > p - window (window > 0), in pages that exist:
  *   out = sum_c softmax_c(scale * q . k_c) v_c
  * A token that sees no key gets zeros; keys and values that it does not see have no
- * part in its result, whatever they hold. Products are exact and summed in fp32, the
+ * part in its result, whatever they hold. What it does see counts as it is: a score of -inf
+ * has no weight, and if every one is, or one is +inf or NaN, the result is NaN. Products are exact and summed in fp32, the
  * softmax is fp32, and each probability (times its value's scale) is rounded to bf16
  * before it multiplies the values (to two bf16 terms for sequences of up to 32 query rows
  * of a kv head, 16 of 256-wide heads); the result is rounded once.

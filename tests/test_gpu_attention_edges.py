@@ -106,3 +106,48 @@ def test_window_past_every_place(m, fmt, causal, G, lens):
     for window in ((1 << 31) - 1, (1 << 31) - 2, (1 << 31) - 300, 1 << 30):
         got = m.paged_attention(cu(q), cache, step.batch(m), causal=causal, window=window)
         assert torch.equal(got.view(torch.int16), none.view(torch.int16)), window
+
+
+# --------------------------------------------------------------- infinite scores
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [2, 8])
+@pytest.mark.parametrize("lens", [[(1, 1), (1, 40), (1, 3000), (2, 3000)],
+                                  [(90, 90), (70, 1500), (1, 200), (3, 3)]])
+def test_scores_of_minus_infinity(m, D, G, lens):
+    """Keys whose score is -inf have no weight; a row that sees keys and whose every score is
+    -inf has a softmax of NaN, one that sees no key is zero (pages that do not exist among
+    them, pieces of a long sequence that hold nothing else)."""
+    step = A.Step(lens, 16, seed=3)
+    if lens[2][1] > 2000:
+        step.table[3] = -1                              # sequence 3: sees nothing
+        step.table[2, 64:] = -1                         # sequence 2: 1024 keys, all -inf
+        gone = {0: lambda p: True, 1: lambda p: p != 7, 2: lambda p: True, 3: lambda p: True}
+    else:
+        step.table[1, 4:] = -1                          # (its first 64 places exist, all -inf)
+        gone = {0: lambda p: p < 37 or p % 3 == 0, 1: lambda p: True, 2: lambda p: p < 199,
+                3: lambda p: p < 2}
+    host = contents(step, 1, D, "bf16", 8)
+    k = host[0]
+    k[..., 0] = 0.0
+    low = torch.zeros(k.shape[:3], dtype=torch.bool)
+    for b, (n, L) in enumerate(lens):
+        for p in range(L):
+            page, row = place(step, b, p)
+            if 0 <= page < step.num_pages and gone[b](p):
+                low[page, 0, row] = True
+    q = randn(step.T, G, D, seed=4).to(BF)
+    q[..., 0] = 1.5
+    q = q.reshape(step.T, G * D)
+    # wanted: the weight of a key 60 below the others, 10^-26, is none
+    k[..., 0] = torch.where(low, torch.tensor(-40.0 * D ** 0.5), torch.tensor(0.0)).to(BF)
+    want, err = A.attention(q, *host, step, G, D ** -0.5)
+    for b, (n, L) in enumerate(lens):
+        for i in range(n):
+            sees = [place(step, b, p) for p in range(L - n + i + 1)]
+            sees = [bool(low[x[0], 0, x[1]]) for x in sees if 0 <= x[0] < step.num_pages]
+            if sees and all(sees):
+                want[step.cu[b] + i] = math.nan
+    assert bool(torch.isnan(want).any()) and bool(torch.isfinite(want).any())
+    k[..., 0] = torch.where(low, torch.tensor(-math.inf), torch.tensor(0.0)).to(BF)
+    got = m.paged_attention(cu(q), cache_of(m, host), step.batch(m))
+    check(got, want, err, "attention")

@@ -15,6 +15,22 @@ typedef v2i v2i_e2 __attribute__((aligned(2)));
 // Running maximum before the first key: finite, so that no difference of two is NaN, and not
 // above any score.
 constexpr float kNoMax = -3.402823466e38f;
+// The maximum that a piece leaves for a row that sees keys in it, but of whose scores every
+// one is -inf: just above kNoMax. A sum of 0 with it, of all pieces, is a softmax of NaN; a row
+// that sees no key gets zeros.
+constexpr float kSeenMax = -0x1.fffffcp127f;
+__device__ __forceinline__ float inverse_sum(float l, float m) {
+  return l != 0.0f ? 1.0f / l : m > kNoMax ? NAN : 0.0f;
+}
+// The maximum m of a row with sum l that sees the places [from, to) of a piece, in pages that
+// exist or not. (A sum is seldom 0: nothing is kept for this while the keys are taken.)
+__device__ __forceinline__ float seen_max(float m, float l, const CacheView &c,
+                                          const int32_t *table, int from, int to) {
+  if (l != 0.0f || from >= to) return m;
+  for (int i = from >> c.log2_page; i << c.log2_page < to; ++i)
+    if ((uint32_t)table[i] < (uint32_t)c.num_pages) return kSeenMax;
+  return m;
+}
 
 __device__ __forceinline__ v4f mfma16bf(v8bf a, v8bf b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);

@@ -67,7 +67,7 @@ __device__ __forceinline__ void join_unit(const AttnArgs &a, const BatchView &bt
         l = l * f + x.l * g;
         v = v * f + x.o * g;
       }
-      v *= l != 0.0f ? 1.0f / l : 0.0f;
+      v *= inverse_sum(l, m);
       const int rr = r0 + row;
       uint16_t *dst = a.out + (int64_t)(un.w.s.start + rr / a.group) * a.ld_out +
                       (h * a.group + rr % a.group) * D + 4 * lane;

@@ -123,6 +123,7 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
 
     v4f o[NQ][kOut];
     float m[NQ], l[NQ];
+    uint32_t some[NQ];  // whether this lane's keys of a row are seen at all
     int t, stage, pg0, pg1, ng0, ng1;
     auto begin = [&]() __attribute__((always_inline)) {
       t = t0 + wave;
@@ -145,6 +146,7 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
       for (int n = 0; n < NQ; ++n) {
         m[n] = kNoMax;
         l[n] = 0.0f;
+        some[n] = 0;
 #pragma unroll
         for (int d = 0; d < kOut; ++d) o[n][d] = v4f{0, 0, 0, 0};
       }
@@ -234,6 +236,7 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
               s[n][x][i] = v;
               mx = fmaxf(mx, v);
             }
+          some[n] |= seen[n];
           mx = fmaxf(m[n], groups_max(mx));
           const float f = __builtin_amdgcn_exp2f(m[n] - mx);
           m[n] = mx;
@@ -326,8 +329,9 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       l[n] = groups_sum(l[n]);
+      const float seen = groups_max(some[n] ? kSeenMax : kNoMax);
       if (g == 0) {
-        ml[wave][n * 16 + col][0] = m[n];
+        ml[wave][n * 16 + col][0] = l[n] != 0.0f ? m[n] : seen;
         ml[wave][n * 16 + col][1] = l[n];
       }
     }
@@ -355,8 +359,7 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
           v += *reinterpret_cast<const v4f *>(jo + (w * 16 + r) * C::kPad + d);
         }
         if (whole) {
-          const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
-          v *= inv;
+          v *= inverse_sum(ll, mm);
           uint16_t *dst = a.out + (int64_t)(un.w.s.start + row / a.group) * a.ld_out +
                           (h * a.group + row % a.group) * D + d;
           *reinterpret_cast<v2i_e2 *>(dst) = v2i{(int)bf16x2(v[0], v[1]), (int)bf16x2(v[2], v[3])};

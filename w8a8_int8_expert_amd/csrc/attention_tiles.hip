@@ -479,8 +479,9 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
 
     l = halves_sum(l);
     if (there) {
+      m = seen_max(m, l, c, table, lo > t0 * K ? lo : t0 * K, hi < t1 * K ? hi : t1 * K);
       if (un.pieces == 1) {
-        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        const float inv = inverse_sum(l, m);
         uint16_t *dst = a.out + (int64_t)(un.w.s.start + tok) * a.ld_out +
                         (h * a.group + row % a.group) * D + 4 * half;
 #pragma unroll
