@@ -647,10 +647,11 @@ int moe_w8a8_qk_norm_rope(const moe_w8a8_qk_norm_rope_args *args, const moe_w8a8
  *   out = sum_c softmax_c(scale * q . k_c) v_c
  * A token that sees no key gets zeros; keys and values that it does not see have no
  * part in its result, whatever they hold. What it does see counts as it is: a score of -inf
- * has no weight, and if every one is, or one is +inf or NaN, the result is NaN. Products are exact and summed in fp32, the
- * softmax is fp32, and each probability (times its value's scale) is rounded to bf16
- * before it multiplies the values (to two bf16 terms for sequences of up to 32 query rows
- * of a kv head, 16 of 256-wide heads); the result is rounded once.
+ * has no weight, and if every one is, or one is +inf or NaN, the result is NaN. Products are
+ * exact and summed in fp32, the softmax is fp32, and each probability (times its value's
+ * scale) is rounded to bf16 before it multiplies the values, half a step of 2^-8: to two bf16
+ * terms, 2^-17, for sequences of up to 32 query rows of a kv head (new tokens times heads /
+ * kv_heads; 16 of 256-wide heads) in any batch. The result is rounded once.
  *   q    bf16 [T][heads D], pitch ld_q;  out  bf16 [T][heads D], pitch ld_out, which
  *        overlaps neither q nor the cache nor the batch's arrays.
  * Supported: heads a multiple of kv_heads up to 65536 / D; window >= 0 (0: none); scale

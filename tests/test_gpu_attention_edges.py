@@ -151,3 +151,39 @@ def test_scores_of_minus_infinity(m, D, G, lens):
     k[..., 0] = torch.where(low, torch.tensor(-math.inf), torch.tensor(0.0)).to(BF)
     got = m.paged_attention(cu(q), cache_of(m, host), step.batch(m))
     check(got, want, err, "attention")
+
+
+# ------------------------------------------------- precision of sequences of few rows
+def two_terms(q, host, step, heads, scale, err):
+    """The bound of A.attention, `err`, with the probabilities' rounding to one bf16 term
+    (2^-8 of the sum of |p v|, the result's rounding on top of it) exchanged for that to
+    two: 2^-17, a rest of half a step at most and half a step of that."""
+    k, ks, v, vs = host
+    size = (v.float().abs() if v.dtype != torch.int8 else v.abs().to(torch.int8)).to(v.dtype)
+    total, _ = A.attention(q, k, ks, size, vs, step, heads, scale)
+    return err - (A.HALF - 2.0 ** -17) * total * (1 + A.HALF) ** 2
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "fp8"])
+@pytest.mark.parametrize("D,G,lens,T,most", [
+    (128, 4, [(1, 300)], 512, 512),             # one token in a step captured for chunks
+    (64, 2, [(16, 700)], 64, 64),
+    (256, 4, [(4, 200)], 300, 300),
+    (128, 4, [(1, 300), (2, 90), (8, 64)], 900, 300),     # rows behind the last sequence
+    (64, 1, [(32, 200), (1, 1), (9, 400)], 120, 40),
+    (128, 4, [(1, 300), (200, 300), (8, 64)], 209, 200),  # beside a chunk
+])
+def test_few_rows_keep_their_precision_in_any_batch(m, fmt, D, G, lens, T, most):
+    """Sequences of up to 32 query rows of a kv head (16 of 256-wide heads) have two terms of
+    each probability, whatever the step has room for."""
+    step = A.Step(lens, 16, seed=3, T=T)
+    host = contents(step, 1, D, fmt, 8)
+    q = randn(T, G * D, seed=4).to(BF)
+    scale = D ** -0.5
+    want, err = A.attention(q, *host, step, G, scale)
+    tight = two_terms(q, host, step, G, scale, err)
+    got = m.paged_attention(cu(q), cache_of(m, host), step.batch(m, most=most))
+    for b, (n, _) in enumerate(lens):
+        few = n * G <= (16 if D == 256 else 32)
+        rows = slice(step.cu[b], step.cu[b] + n)
+        check(got[rows], want[rows], (tight if few else err)[rows], "sequence %d" % b)

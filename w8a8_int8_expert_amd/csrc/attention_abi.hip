@@ -158,11 +158,12 @@ AttnPlan moe::attention_plan(const CacheView &c, int D, int format, const BatchV
   const int most_few = D == 256 ? 16 : 32;
   const int grid_cap = kMostBlocks / 2 / c.kv_heads;
   auto at_most = [](int64_t v, int64_t most) { return (int)(v < most ? v : most); };
-  // All sequences have few rows; or some may, beside longer ones (where one sequence
-  // is all there is, or every row is needed for the longest, none does).
+  // All sequences have few rows; or some may, beside longer ones or alone in a step with room
+  // for more (rows and bounds say nothing of what the arrays hold: a sequence of few rows is
+  // taken the same way in every batch). A launch that finds none costs 4 us: 64 tokens over
+  // 4096 keys, bf16, 30.4 us, 26.5 without it, 8192 from their start 565 and 561.
   const bool all_few = rows <= most_few;
-  const bool some_few =
-      group <= most_few && b.num_seqs > 1 && (int64_t)b.num_seqs * b.max_tokens > b.T;
+  const bool some_few = group <= most_few;
   size_t total = 0;
   if (all_few || some_few) {
     p.few_rows = most_few;
