@@ -187,3 +187,17 @@ def test_few_rows_keep_their_precision_in_any_batch(m, fmt, D, G, lens, T, most)
         few = n * G <= (16 if D == 256 else 32)
         rows = slice(step.cu[b], step.cu[b] + n)
         check(got[rows], want[rows], (tight if few else err)[rows], "sequence %d" % b)
+
+
+# ----------------------------------------------- windows without the causal limit
+@pytest.mark.parametrize("D,fmt,n,L,window", [(64, "bf16", 2300, 2300, 64), (128, "int8", 1100, 1900, 200),
+                                              (256, "bf16", 700, 1500, 33), (64, "fp8", 130, 4000, 5)])
+def test_windows_of_tokens_that_see_what_follows(m, D, fmt, n, L, window):
+    """Without the causal limit a token sees the window before it and all behind it: the
+    first row blocks see the most keys and are cut into pieces, the last ones may see none."""
+    step = A.Step([(n, L), (3, 50), (0, 10), (40, 400)], 16, seed=3)
+    host = contents(step, 1, D, fmt, 8)
+    q = (1.5 * randn(step.T, 2 * D, seed=4)).to(BF)
+    want, err = A.attention(q, *host, step, 2, D ** -0.5, False, window)
+    got = m.paged_attention(cu(q), cache_of(m, host), step.batch(m), causal=False, window=window)
+    check(got, want, err, "attention")

@@ -20,8 +20,13 @@ constexpr int kLeastMany = 512 / kManyKeys<D>;
 struct Work {
   Seq s;
   int rows, blocks;  // query rows of a kv head, and blocks of them; 0: not of this kind
-  int t0, keys;      // first key tile (few rows), and key tiles of the last row block
+  int t0, keys;      // first key tile (few rows), and key tiles of the row block that has most
 };
+// Of a sequence's row blocks the last one sees the most keys; without the causal limit, with a
+// window, the first one: a token then sees the window before it and all behind it.
+__device__ __forceinline__ bool first_sees_most(const AttnArgs &a) {
+  return !a.causal && a.window > 0;
+}
 template <bool kFew, int kKeys>
 __device__ __forceinline__ Work work_of(const AttnArgs &a, const BatchView &bt, int b) {
   Work w{};
@@ -32,7 +37,8 @@ __device__ __forceinline__ Work work_of(const AttnArgs &a, const BatchView &bt, 
     w.rows = n * a.group;
     w.blocks = kFew ? 1 : (w.rows + kTileRows - 1) / kTileRows;
     const int first = w.s.len - w.s.n;
-    const int lo = seen_lo(first + (w.blocks - 1) * kTileRows / a.group, a.window);
+    const int most = first_sees_most(a) ? 0 : w.blocks - 1;
+    const int lo = seen_lo(first + most * kTileRows / a.group, a.window);
     const int hi = seen_hi(first + n - 1, w.s.len, a.causal);
     w.t0 = lo / kKeys;
     w.keys = hi > lo ? (hi + kKeys - 1) / kKeys - w.t0 : 0;
@@ -73,10 +79,10 @@ struct Schedule {
     const int n = (w.keys + chunk - 1) / chunk;
     return n > 1 ? n : 1;
   }
-  // Unit u: of each sequence its row blocks from the last (which sees the most keys: the
-  // long ones come first), each piece by piece. Only row blocks of two pieces or more
-  // have slots; those have more tiles than a chunk, so that their pieces are at most
-  // 2 target of a kv head.
+  // Unit u: of each sequence its row blocks from the one that sees the most keys (the long
+  // ones come first), each piece by piece. Only row blocks of two pieces or more have slots;
+  // those are counted with more tiles than a chunk, so that their pieces are at most 2 target
+  // of a kv head.
   // kSlots: u is a slot, not a unit.
   template <bool kSlots = false>
   __device__ __forceinline__ Unit find(const AttnArgs &a, const BatchView &bt, int64_t u) const {
@@ -94,7 +100,7 @@ struct Schedule {
         r.b = b0 + l;
         r.pieces = rd(p);
         const int at = (int)(u - before) - (rd(upto) - rd(n));
-        r.block = rd(w.blocks) - 1 - at / r.pieces;
+        r.block = first_sees_most(a) ? at / r.pieces : rd(w.blocks) - 1 - at / r.pieces;
         r.piece = at % r.pieces;
         r.slot = rd(supto) - rd(ns) + at;
         r.w.s = Seq{rd(w.s.start), rd(w.s.n), rd(w.s.len)};
