@@ -201,3 +201,33 @@ def test_windows_of_tokens_that_see_what_follows(m, D, fmt, n, L, window):
     want, err = A.attention(q, *host, step, 2, D ** -0.5, False, window)
     got = m.paged_attention(cu(q), cache_of(m, host), step.batch(m), causal=False, window=window)
     check(got, want, err, "attention")
+
+
+# --------------------------------------------------------------------- workspaces
+@pytest.mark.parametrize("D,n,L,B", [(128, 40, 1500, 1), (64, 1, 5000, 3), (256, 90, 1100, 2),
+                                     (128, 3, 129, 2), (128, 200, 513, 2)])
+@pytest.mark.parametrize("again", [False, True])
+def test_workspace_of_the_stated_size(m, D, n, L, B, again):
+    """Nothing is written behind the workspace's end; also where the sequences' rows are given
+    more than once (ends that go back)."""
+    step = A.Step([(n, L)] * B, 16, seed=3)
+    host = contents(step, 2, D, "bf16", 8)
+    cache = cache_of(m, host)
+    T, G = step.T, 4
+    q = cu(randn(T, 2 * G * D, seed=4).to(BF))
+    ends = [0, T] * B if again else step.cu
+    seqs = len(ends) - 1
+    table = cu(step.table).repeat(-(-seqs // B), 1)[:seqs]
+    batch = m.SequenceBatch(i32(*ends), i32(*[L] * seqs), table, T if again else n, L)
+    size = m.moe_w8a8_paged_attention_workspace_size(cache.struct, batch.struct, 2 * G, T)
+    room = torch.full((size + 65536,), 0x5a, dtype=torch.uint8, device="cuda")
+    out = torch.zeros(T, 2 * G * D, dtype=BF, device="cuda")
+    a = m.moe_w8a8_attention_args(2 * G, 1, 0, D ** -0.5, q.data_ptr(), 2 * G * D, out.data_ptr(),
+                                  2 * G * D)
+    assert m.moe_w8a8_paged_attention(a, cache.struct, batch.struct, T, room.data_ptr(), size,
+                                      stream=torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert bool((room[size:] == 0x5a).all())
+    if not again:
+        want, err = A.attention(q.cpu(), *host, step, 2 * G, D ** -0.5)
+        check(out, want, err, "attention")

@@ -158,6 +158,14 @@ AttnPlan moe::attention_plan(const CacheView &c, int D, int format, const BatchV
   const int most_few = D == 256 ? 16 : 32;
   const int grid_cap = kMostBlocks / 2 / c.kv_heads;
   auto at_most = [](int64_t v, int64_t most) { return (int)(v < most ? v : most); };
+  // Slots for pieces: about twice the target at most, and no more than the table's places can
+  // be cut into, for every row block that a sequence may have (whatever the arrays hold). A
+  // sequence whose places make one piece needs none.
+  auto slots = [&](int64_t row_blocks, int keys, int least, int target) {
+    const int64_t tiles = ((int64_t)b.most + keys - 1) / keys, pieces = (tiles + least - 1) / least;
+    const int64_t of_one = at_most(row_blocks * pieces, 2 * target);
+    return pieces > 1 ? at_most(b.num_seqs * of_one, 2 * target) : 0;
+  };
   // All sequences have few rows; or some may, beside longer ones or alone in a step with room
   // for more (rows and bounds say nothing of what the arrays hold: a sequence of few rows is
   // taken the same way in every batch). A launch that finds none costs 4 us: 64 tokens over
@@ -169,7 +177,7 @@ AttnPlan moe::attention_plan(const CacheView &c, int D, int format, const BatchV
     p.few_rows = most_few;
     p.row_tiles = at_most(rows, most_few) <= 16 ? 1 : 2;
     p.row_target = (256 * rows_per_unit(D, format, p.row_tiles) + c.kv_heads - 1) / c.kv_heads;
-    p.row_slots = 2 * p.row_target;
+    p.row_slots = slots(1, kFewKeys, kLeastFew, p.row_target);
     // (keys of 128 at least make a unit)
     const int64_t units = (int64_t)b.num_seqs * ((max_length + 127) / 128 + 1);
     p.row_grid = at_most(at_most(units, (int64_t)p.row_target + b.num_seqs), grid_cap);
@@ -180,8 +188,10 @@ AttnPlan moe::attention_plan(const CacheView &c, int D, int format, const BatchV
     p.tiles = true;
     // blocks of rows that the batch can make
     const int64_t blocks = (int64_t)b.T * group / kTileRows + at_most(b.num_seqs, b.T);
+    const int64_t of_one = (rows + kTileRows - 1) / kTileRows;  // the most of one sequence
     p.tile_target = (1024 + c.kv_heads - 1) / c.kv_heads;
-    p.tile_slots = 2 * p.tile_target;
+    p.tile_slots = D == 256 ? slots(of_one, kManyKeys<256>, kLeastMany<256>, p.tile_target)
+                            : slots(of_one, kManyKeys<128>, kLeastMany<128>, p.tile_target);
     p.tile_grid = at_most(blocks + p.tile_target, grid_cap);
     total += up256((size_t)p.tile_slots * c.kv_heads * kTileRows * (D + 2) * sizeof(float));
   }

@@ -81,6 +81,12 @@ struct AttnArgs {
 };
 
 constexpr int kMostBlocks = 1 << 20;  // a launch counts threads in 32 bits
+constexpr int kFewKeys = 32;  // keys of a tile of the kernel of few rows
+template <int D>
+constexpr int kManyKeys = D == 256 ? 32 : 64;  // of the kernel of tiles
+constexpr int kLeastFew = 4;                   // least piece: 128 keys, a tile a wavefront
+template <int D>
+constexpr int kLeastMany = 512 / kManyKeys<D>;  // 512 keys
 
 // Which kernels run, their launch sizes and the workspace, from shapes alone. Of each
 // kv head: a number of units that the keys are split into, about; the slots for partial

@@ -10,13 +10,6 @@
 
 namespace moe {
 
-constexpr int kFewKeys = 32;  // keys of a tile of the kernel of few rows
-template <int D>
-constexpr int kManyKeys = D == 256 ? 32 : 64;  // of the kernel of tiles
-constexpr int kLeastFew = 4;                   // least chunk: 128 keys, a tile a wavefront
-template <int D>
-constexpr int kLeastMany = 512 / kManyKeys<D>;
-
 struct Work {
   Seq s;
   int rows, blocks;  // query rows of a kv head, and blocks of them; 0: not of this kind
