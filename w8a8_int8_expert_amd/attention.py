@@ -129,7 +129,7 @@ class SequenceBatch:
 
     def __init__(self, cu_tokens, lengths, pages, max_tokens: int, max_length: int):
         _m.load_library()
-        for t, name, dim in ((cu_tokens, "cu_tokens", 1), (lengths, "lengths", 1),
+        for t, name, dim in ((lengths, "lengths", 1), (cu_tokens, "cu_tokens", 1),
                              (pages, "pages", 2)):
             if not isinstance(t, torch.Tensor) or t.dtype != _I32 or t.dim() != dim:
                 _fail("%s must be an int32 tensor of %d dimension%s" % (name, dim, "s"[:dim - 1]))
