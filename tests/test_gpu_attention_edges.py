@@ -231,3 +231,24 @@ def test_workspace_of_the_stated_size(m, D, n, L, B, again):
     if not again:
         want, err = A.attention(q.cpu(), *host, step, 2 * G, D ** -0.5)
         check(out, want, err, "attention")
+
+
+# ------------------------------------------------------------------ norms of heads
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("size,eps", [(1e-20, 16.0), (1e-20, 1e30), (1e-18, 5.0), (1e-30, 1e-3),
+                                      (1e-39, 0.0), (9.2e-41, 0.0), (1e-39, 1e-44), (1e-33, 1e-30),
+                                      (1e-39, 1e-20), (3e38, 1e30), (1e20, 1e38)])
+def test_norms_of_tiny_rows(m, D, size, eps):
+    """Head rows far from 1 against every eps: neither what the squares lose nor what eps
+    becomes when the row is lifted leaves fp32. (One element of each head is not zero, or
+    all of them are.)"""
+    step = A.Step([(4, 20)], 16, seed=1)
+    x = torch.ones(4, 4, D)
+    x[1::2, :, 1:] = 0.0
+    x = (size * x).to(BF)
+    host = contents(step, 1, D, "bf16", 8)
+    q = m.qk_norm_rope(cu(x.view(4, -1)), cache_of(m, host), step.batch(m), 2, norm=True, eps=eps)
+    eps = float(torch.tensor(eps, dtype=F32))
+    y, e = A.rope(x[:, :2], None, eps, True, None, None, False)
+    # (2^-134: half a step of the smallest bf16 numbers)
+    check(q, y.reshape(4, -1), (e + A.HALF * (y.abs() + e)).reshape(4, -1) + 2.0 ** -134, "queries")

@@ -43,9 +43,11 @@ __device__ __forceinline__ void head_norm(float *x, const float *w, int o0, int 
     return lanes_sum<kLanes>(s);
   };
   float ss = squares();
-  // Squares that leave the fp32 range: the head is brought to about 1 by a power
-  // of two first (at most 2^63, so that eps keeps its part).
-  if (!(ss < 1e38f) || ss < 1e-28f) {
+  // Squares that leave the fp32 range: the head is brought to about 1 by a power of two
+  // first. At most 2^63: the square of the smallest number, 2^-133, is 2^-140 then, and that
+  // over 256 elements still a number. Squares below 1e-28 are nothing beside an eps of 1e-20
+  // or more (less than 2^-24 of it), and a smaller eps stays finite when it is lifted.
+  if (!(ss < 1e38f) || (ss < 1e-28f && eps < 1e-20f)) {
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = umax(m, abs_bits(x[j]));
