@@ -651,7 +651,9 @@ int moe_w8a8_qk_norm_rope(const moe_w8a8_qk_norm_rope_args *args, const moe_w8a8
  * exact and summed in fp32, the softmax is fp32, and each probability (times its value's
  * scale) is rounded to bf16 before it multiplies the values, half a step of 2^-8: to two bf16
  * terms, 2^-17, for sequences of up to 32 query rows of a kv head (new tokens times heads /
- * kv_heads; 16 of 256-wide heads) in any batch. The result is rounded once.
+ * kv_heads; 16 of 256-wide heads) in any batch. The result is divided by the probabilities'
+ * sum at the end (values whose sum over the keys passes 2^119 may be infinite there) and
+ * rounded once.
  *   q    bf16 [T][heads D], pitch ld_q;  out  bf16 [T][heads D], pitch ld_out, which
  *        overlaps neither q nor the cache nor the batch's arrays.
  * Supported: heads a multiple of kv_heads up to 65536 / D; window >= 0 (0: none); scale

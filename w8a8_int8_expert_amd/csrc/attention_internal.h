@@ -103,9 +103,9 @@ struct AttnPlan {
 // its LDS holds tiles for (of narrow 8-bit heads half as many; 32 rows of 128-wide heads fill
 // its registers). One round of long units: each wavefront has the next tile on its way all
 // along, and there are fewer partial results. With 1024 units whatever the type, 1 sequence of
-// 16384 keys, 8 kv heads of 128, bf16, took 34.7 us instead of 21.7, 32 of 8192 with 8 tokens 228
-// instead of 191, with INT8 205 instead of 188, 16 of 4096, 2 of 256, 55 instead of 34, 32 of
-// 8192, one token, INT8, 113 instead of 107; with 256 units these last took 139.
+// 16384 keys, 8 kv heads of 128, bf16, takes 33.9 us instead of 22.1, 32 of 8192 with 8 tokens 237
+// instead of 194, with INT8 223 instead of 191, 16 of 4096, 2 of 256, 58 instead of 36, 32 of
+// 8192, one token, INT8, 114 instead of 110; with 256 units these last take 142.
 constexpr int rows_per_unit(int D, int format, int row_tiles) {
   return D * (format == kBf16Cache ? 2 : 1) < 256 && D * row_tiles < 256 ? 2 : 1;
 }

@@ -7,7 +7,7 @@
 // lanes but for one exchange over the four lane groups, and the probabilities are
 // where the second product (values transposed by the LDS reads) takes them from.
 // Bound by the cache's bytes (8 sequences of 65536 keys, 8 kv heads of 128, FP8: 1.1 GB in
-// 195 us, 5.7 TB/s; 32 ragged ones of 1 to 8192, INT8: 174 MB in 48, of which about 6 are its
+// 196 us, 5.7 TB/s; 32 ragged ones of 1 to 8192, INT8: 174 MB in 48, of which about 6 are its
 // beginning and end). Every wavefront brings its own tiles of 32 keys into
 // LDS by direct loads, the next in flight while one is worked on, and no two of them
 // meet until the end.
@@ -254,7 +254,8 @@ __global__ __launch_bounds__((64 * Rows<D, kFormat, NQ>::kWaves)) void rows_kern
           // two bf16 terms for the second product, whose matrix instructions are few here: the
           // rest of what the first one rounds, 2^-17 of the probability at most left out. (With one
           // term a key that has all the weight moves its row by up to 2^-9: 32 sequences of 8192,
-          // INT8, 107 us instead of 109, but the result's error half again that of its rounding.)
+          // INT8, 108 us instead of 110, with 8 tokens each 180 instead of 191, but the result's
+          // error half again that of its rounding.)
           v4i w, r;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {

@@ -14,7 +14,7 @@
 // Bound by the matrix instructions together with the exponentials: of 64 keys, 32
 // matrix instructions of 32 cycles against about 1000 cycles of vector instructions.
 // Two blocks share a compute unit, one's softmax under the other's products. 8192 tokens of 32
-// heads over 8 of 128, causal: 540 us, 1.0 PFLOP/s.
+// heads over 8 of 128, causal: 532 to 565 us with the card's clocks, 1.0 PFLOP/s.
 //
 // Nothing between a tile's barriers diverges (loops run by shared counts, conditions of
 // single lanes select): the compiler has been seen to put a copy of a live register,
@@ -44,7 +44,8 @@ struct Cfg {
   static constexpr int kSteps = D / 16;       // matrix instructions of a score block
   static constexpr int kOut = D / 32;
   // Blocks on a compute unit, which share its registers. 8-bit heads of 128 keep some of their
-  // state in memory for two, and win: 4 sequences of 2048 tokens, INT8, 232 us, one block 322.
+  // state in memory for two (32 registers), and win: 4 sequences of 2048 tokens, INT8, 230 us,
+  // one block 322. 256-wide heads have room for one: no other products run under its softmax.
   // A third block of 64-wide heads: 8192 tokens, bf16, 321 us, two 346; INT8 ones lose as much
   // in short chunks (47 us for 42) as they win in long ones (405 for 435).
   static constexpr int kPerUnit = D == 256 ? 1 : D == 64 && !k8 ? 3 : 2;
@@ -356,8 +357,13 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, kFormat>::kPerUnit)) void tiles_k
             }
           }
         }
-        // rounded to bf16 for the second product: half a step of 2^-8 each, which the
-        // result, itself rounded so, averages over its keys
+        // rounded to bf16 for the second product: half a step of 2^-8 each, which the result,
+        // itself rounded so, averages over its keys; the row's sum is of the unrounded ones. The
+        // result is off by 0.0021 to 0.0023 of its size (root mean square), by its own rounding
+        // alone 0.0016 to 0.0017. A second term, which the few rows of a decode step have, brings
+        // it there for half again the matrix instructions: 8192 tokens, 32 heads of 128, 705 us
+        // instead of 541, 16 heads of 256 1058 instead of 919, the mixed batch of 12 sequences
+        // 482 instead of 384, 9 windowed chunks of 64-wide INT8 heads 45 instead of 42.
         return __builtin_bit_cast(
             v8bf, v4i{(int)bf16x2(e[0], e[1]), (int)bf16x2(e[2], e[3]), (int)bf16x2(e[4], e[5]),
                       (int)bf16x2(e[6], e[7])});
