@@ -153,6 +153,34 @@ def test_scores_of_minus_infinity(m, D, G, lens):
     check(got, want, err, "attention")
 
 
+@pytest.mark.parametrize("x", [math.inf, math.nan])
+@pytest.mark.parametrize("D,G,lens", [(64, 2, [(1, 40), (2, 3000), (1, 9)]), (128, 4, [(90, 1500), (3, 70)]),
+                                      (256, 8, [(1, 2000), (40, 600)])])
+def test_scores_of_infinity_and_nan(m, x, D, G, lens):
+    """A key with an infinite or NaN score in the middle of each sequence: NaN for the rows
+    that see it, in whatever piece it lies, and nothing for those that do not."""
+    step = A.Step(lens, 16, seed=3)
+    host = contents(step, 1, D, "bf16", 8)
+    q = randn(step.T, G, D, seed=4).to(BF)
+    q[..., 0] = 1.5
+    q = q.reshape(step.T, G * D)
+    want, err = A.attention(q, *host, step, G, D ** -0.5, True, 30)
+    whole, werr = A.attention(q, *host, step, G, D ** -0.5)
+    for b, (n, L) in enumerate(lens):
+        p = max(0, L - n // 2 - 20)
+        page, row = place(step, b, p)
+        host[0][page, 0, row, 0] = x
+        for i in range(n):
+            at = L - n + i
+            if p <= at:
+                whole[step.cu[b] + i] = math.nan
+                if p > at - 30:
+                    want[step.cu[b] + i] = math.nan
+    cache = cache_of(m, host)
+    check(m.paged_attention(cu(q), cache, step.batch(m), window=30), want, err, "window")
+    check(m.paged_attention(cu(q), cache, step.batch(m)), whole, werr, "whole")
+
+
 # ------------------------------------------------- precision of sequences of few rows
 def two_terms(q, host, step, heads, scale, err):
     """The bound of A.attention, `err`, with the probabilities' rounding to one bf16 term
