@@ -181,6 +181,24 @@ def test_scores_of_infinity_and_nan(m, x, D, G, lens):
     check(m.paged_attention(cu(q), cache, step.batch(m)), whole, werr, "whole")
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "fp8"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,n,L,gone", [(1, 150, 150, 3), (4, 100, 100, 5), (2, 300, 900, 45), (3, 5, 20, 1),
+                                        (2, 1300, 1300, 70)])
+def test_rows_whose_first_pages_do_not_exist(m, fmt, D, G, n, L, gone):
+    """Rows that see places but no page (zeros) beside rows of the same block that see keys,
+    with and without a window."""
+    step = A.Step([(n, L), (2, 30)], 16, seed=3)
+    step.table[0, :gone] = -1
+    host = contents(step, 1, D, fmt, 8)
+    cache = cache_of(m, host)
+    q = randn(step.T, G * D, seed=4).to(BF)
+    for window in (0, 21):
+        want, err = A.attention(q, *host, step, G, D ** -0.5, True, window)
+        assert bool((want[:n] == 0).all(1).any()) == (L - n < 16 * gone)
+        check(m.paged_attention(cu(q), cache, step.batch(m), window=window), want, err, "attention")
+
+
 # ------------------------------------------------- precision of sequences of few rows
 def two_terms(q, host, step, heads, scale, err):
     """The bound of A.attention, `err`, with the probabilities' rounding to one bf16 term

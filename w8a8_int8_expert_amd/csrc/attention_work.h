@@ -38,8 +38,8 @@ __device__ __forceinline__ Work work_of(const AttnArgs &a, const BatchView &bt, 
 }
 
 // Pieces of many rows: about 1024 in all, of 512 keys at least. 12 sequences of up to 512 tokens
-// over 16384 keys take 396 us, 389 with 1536 pieces and 397 with 2048; 9 of up to 613 tokens with
-// a window of 1000 take 42.4, 43.5 and 45.2, and 47.8 with pieces of 256 keys. A lone chunk of 64
+// over 16384 keys take 387 us, 379 with 1536 pieces and 388 with 2048; 9 of up to 613 tokens with
+// a window of 1000 take 43.5, 44.9 and 47.3, and 48.5 with pieces of 256 keys. A lone chunk of 64
 // tokens, 32 heads over 8 of 128, bf16, with pieces of 512, 256 and 128 keys at least: over 1024
 // keys 28, 24 and 22 us, over 4096 31, 30 and 40, over 16384 50, 87 and 88 (the join takes a
 // row's pieces one after the other). Of few rows one round of blocks (rows_per_unit), of 128 keys
